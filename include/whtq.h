@@ -474,6 +474,142 @@ whtq_status qwha_init_refine(const float* g, int64_t n, const float* p, int64_t 
                              const int32_t* col_idx, float* vals, void* stream);
 
 /*
+ * ---- Paged key/value cache and attention.  Serving a model whose weights
+ * are rotated low-bit codes needs the other half of a decode step: a cache
+ * of keys and values and the attention that reads it.  The rotation that
+ * makes weights quantisable ([HARP] 1: the RHT spreads outliers over every
+ * coordinate) does the same for keys and values, so the cache is either the
+ * 16-bit vectors themselves or INT4 codes of their RHT along the head
+ * dimension with ONE fp16 scale per vector; since Hn S is orthogonal,
+ * (Hn S q).(Hn S k) = q.k and the attention works on the codes directly.
+ *
+ * A cache is num_pages pages of page_size token slots for each of kv_heads
+ * heads.  Slot number = page * page_size + offset.  Entry (page, head,
+ * offset) starts at k + page * k_stride[0] + head * k_stride[1] + offset *
+ * k_stride[2] and its dim values (or codes) are contiguous:
+ *   WHTQ_KV_DENSE: dim values in `dtype` (bf16 or fp16); strides in elements.
+ *   WHTQ_KV_INT4:  dim/2 bytes, the row format of rht_quantize_rtn with
+ *     bits = 4, group = dim and sign_bits; strides in bytes.  Its scale is
+ *     k_scales[page * ks_stride[0] + head * ks_stride[1] + offset] (fp16
+ *     bits; the offsets of a page are contiguous).  The entry stands for
+ *     S Hn (code * scale), the row rht_dequantize_inverse would write.
+ *   dim: 64 or 128.  page_size: a power of two in [16, 65536].  Strides are
+ *   non-negative; 16-byte alignment of k, v and of every stride (in bytes),
+ *   8-byte alignment of the scales and of their strides.  Offsets are 64-bit:
+ *   a cache may exceed 4 GiB.
+ */
+typedef enum { WHTQ_KV_DENSE = 0, WHTQ_KV_INT4 = 1 } whtq_kv_format;
+
+typedef struct {
+  void* k;
+  void* v;
+  uint16_t* k_scales; /* INT4 only (else NULL) */
+  uint16_t* v_scales;
+  const uint32_t* sign_bits; /* INT4: uint32[dim / 32] or NULL (all +1), shared by keys, values and heads */
+  int64_t num_pages, page_size, kv_heads, dim;
+  int64_t k_stride[3], v_stride[3];   /* page, head, offset */
+  int64_t ks_stride[2], vs_stride[2]; /* page, head (elements) */
+  int32_t format;                     /* whtq_kv_format */
+  int32_t dtype;                      /* DENSE: WHTQ_BF16 or WHTQ_F16; INT4: ignored */
+} whtq_kv_cache;
+
+/*
+ * Rotary positions: coordinates a and b of a pair become
+ *   a cos - b sin,  b cos + a sin
+ * with cos / sin the row `positions[token]` of fp32 tables [max_position][ld]
+ * (rot_dim / 2 entries used).  Pairs: (i, i + rot_dim / 2), or (2i, 2i + 1)
+ * with interleaved = 1; coordinates from rot_dim on are left alone.
+ * rot_dim: a multiple of 16 in [16, dim].  cos, sin 16-byte aligned, ld a
+ * multiple of 4.
+ */
+typedef struct {
+  const float* cos;
+  const float* sin;
+  const int32_t* positions; /* device int32[tokens] */
+  int64_t ld, max_position;
+  int32_t rot_dim, interleaved;
+} whtq_rope;
+
+/*
+ * kv_append -- rotates `tokens` new keys (and queries, if q is given) and
+ * writes keys and values into their cache slots.
+ *   k, v: rows k + token * k_stride[0] + head * k_stride[1] (elements) of dim
+ *   contiguous values in `dtype` (bf16 or fp16; a DENSE cache has the same
+ *   dtype).  slots: device int64[tokens]; a token whose slot lies outside
+ *   [0, num_pages * page_size) (-1 for padding) leaves the cache alone; two
+ *   tokens with one slot leave either's entry.  rope: NULL for no rotation; a
+ *   token whose position lies outside [0, max_position) leaves the cache and
+ *   its q_out rows alone.
+ *   q (may be NULL): `heads` rows per token, written rotated to q_out (q_out
+ *   == q with equal strides is allowed).
+ *   Arithmetic: fp32, rounded once to the stored type.  INT4: y = Hn S k' of
+ *   the unrounded rotated key, s = fp16_rne(max|y| / 7), code = rint(y * (1 /
+ *   s)) held to [-7, 7] (s = 0 gives 0).
+ *   Alignment: rows 16-byte aligned (pointers and strides); slots 8 bytes.
+ */
+whtq_status kv_append(const whtq_kv_cache* cache, const void* k, const int64_t* k_stride, const void* v,
+                      const int64_t* v_stride, whtq_dtype dtype, int64_t tokens, const int64_t* slots,
+                      const whtq_rope* rope, const void* q, const int64_t* q_stride, int64_t heads, void* q_out,
+                      const int64_t* q_out_stride, void* stream);
+
+/*
+ * kv_gather -- the keys and values that `tokens` slots stand for, as dense
+ *   rows k_out / v_out [tokens][kv_heads][dim] in `dtype` (a DENSE cache's own
+ *   dtype; INT4: bf16 or fp16), strides as in kv_append; either output may be
+ *   NULL.  INT4: S Hn (code * scale) in fp32, rounded once.  A slot outside
+ *   the cache gives zeros.
+ */
+whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t* slots, void* k_out,
+                      const int64_t* k_stride, void* v_out, const int64_t* v_stride, whtq_dtype dtype,
+                      void* stream);
+
+/*
+ * kv_attention -- softmax attention of new tokens over their sequence's
+ * cached keys and values (which the new tokens have already joined).
+ *   q, out: rows q + token * q_stride[0] + head * q_stride[1] of dim values in
+ *   `dtype` (DENSE: the cache's; INT4: bf16 or fp16).  heads is a multiple of
+ *   kv_heads; query head h reads key/value head h / (heads / kv_heads).
+ *   Sequence b: query tokens q_start[b] .. q_start[b + 1) (device
+ *   int32[seqs + 1], non-decreasing, q_start[seqs] <= q_tokens), kv_len[b]
+ *   keys (device int32[seqs]), key j in slot table[b][j / page_size] *
+ *   page_size + j % page_size (block_table device int32, row stride
+ *   table_stride, table_width entries a row).  Query i of a chunk of n sits at
+ *   p = kv_len - n + i and sees the keys j < kv_len with j <= p (causal = 1)
+ *   and j > p - window (window > 0; 0 = all).
+ *   out = sum_j softmax_j(scale q.k_j) v_j; lse (float [q_tokens][heads]
+ *   contiguous, or NULL) = log sum_j exp(scale q.k_j).  A query that sees
+ *   nothing gives out = 0, lse = -inf.  What a masked place holds (NaN and
+ *   infinities included) does not reach the result, except keys and values
+ *   inside the sequence that some query of the same call and sequence sees:
+ *   there a value that is not finite reaches only the queries that see it.
+ *   Device values are not read on the host: max_q_len and max_kv_len bound
+ *   the chunk and key counts.  They choose the kernel and the split of the
+ *   keys; with max_q_len too small the results of queries beyond it
+ *   are undefined, any max_kv_len gives right results; so are the rows of
+ *   tokens that belong to no sequence.  kv_len is held to [0, table_width *
+ *   page_size]; a table entry outside the cache reads page 0 (no access
+ *   outside the cache, a meaningless result).
+ *   workspace: device memory of kv_attention_workspace_bytes(...), 16-byte
+ *   aligned, overwritten (fp32 partial results where the keys are split
+ *   across blocks); may be NULL when that is 0.
+ *   Arithmetic: 16-bit products on the matrix cores with fp32 accumulation,
+ *   softmax statistics, sums and the joining of splits in fp32; the
+ *   probabilities are rounded to the 16-bit type for the second product.
+ *   INT4: queries rotated in fp32 and rounded to fp16 under a power of two
+ *   per row, codes exact in fp16, the key's scale applied to the fp32 score
+ *   and the value's to the fp32 probability.  Deterministic.
+ */
+int64_t kv_attention_workspace_bytes(const whtq_kv_cache* cache, int64_t q_tokens, int64_t heads, int64_t seqs,
+                                     int64_t max_q_len, int64_t max_kv_len); /* -1: invalid sizes or no device */
+
+whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_t* q_stride, whtq_dtype dtype,
+                         int64_t q_tokens, int64_t heads, int64_t seqs, const int32_t* q_start,
+                         const int32_t* kv_len, const int32_t* block_table, int64_t table_stride,
+                         int64_t table_width, int64_t max_q_len, int64_t max_kv_len, float scale, int causal,
+                         int64_t window, void* out, const int64_t* out_stride, float* lse, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/*
  * whtq_stream_probe -- measurement helper, not part of the transform path:
  *   reads in_bytes of src and writes out_bytes of dst (an index pattern) with
  *   coalesced 16-byte accesses, blocks split between the two streams in

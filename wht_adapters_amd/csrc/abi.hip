@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/whtq.h"
+#include "kv_attn.hpp"
 
 namespace whtq {
 
@@ -60,6 +61,19 @@ hipError_t launch_qi_select(const float* f, int64_t ldf, int64_t rows, int n, co
                             int32_t* col_idx, hipStream_t s);
 hipError_t launch_qi_refine(const float* g, int64_t n, const float* p, int64_t rows, const int32_t* row_ptr,
                             const int32_t* col_idx, float* vals, hipStream_t s);
+
+hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const void* k,
+                            const int64_t* ks, const void* v, const int64_t* vs, const int64_t* slots,
+                            int64_t capacity, const float* cos, const float* sin, const int32_t* pos, int64_t ld_cs,
+                            int64_t max_pos, int rot, int interleaved, const void* q, const int64_t* qs, int heads,
+                            void* qo, const int64_t* qos, hipStream_t s);
+hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const int64_t* slots,
+                            int64_t capacity, void* ko, const int64_t* ks, void* vo, const int64_t* vs,
+                            hipStream_t s);
+hipError_t launch_kv_step(const KvAttnArgs& a, int dim, int dt, bool int4, int nq, hipStream_t s);
+hipError_t launch_kv_join(const KvAttnArgs& a, int dim, int dt, bool int4, hipStream_t s);
+hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int64_t tiles, hipStream_t s);
+int kv_chunk_rows();
 
 static thread_local int g_last_hip = 0;
 
@@ -704,6 +718,227 @@ whtq_status qwha_init_refine(const float* g, int64_t n, const float* p, int64_t 
   st = need_device();
   if (st != WHTQ_OK) return st;
   return hip_status(launch_qi_refine(g, n, p, rows, row_ptr, col_idx, vals, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- paged key/value cache
+
+namespace {
+
+constexpr int64_t kMost = int64_t(1) << 30;  // tokens, keys, pages: 32-bit positions in the kernels
+
+bool kv_dtype(int dt) { return dt == WHTQ_BF16 || dt == WHTQ_F16; }
+
+// the rules of a cache; fills the kernels' view of it
+whtq_status kv_check(const whtq_kv_cache* c, KvCache* out) {
+  if (!c) return WHTQ_EINVAL;
+  if (c->format != WHTQ_KV_DENSE && c->format != WHTQ_KV_INT4) return WHTQ_EINVAL;
+  const bool int4 = c->format == WHTQ_KV_INT4;
+  if (!int4 && !kv_dtype(c->dtype)) return WHTQ_EINVAL;
+  if (c->num_pages < 1 || c->kv_heads < 1 || c->dim < 1 || c->page_size < 1) return WHTQ_EINVAL;
+  if (!c->k || !c->v || (int4 && (!c->k_scales || !c->v_scales))) return WHTQ_EINVAL;
+  const int64_t esz = int4 ? 1 : 2;
+  for (int i = 0; i < 3; ++i)
+    if (c->k_stride[i] < 0 || c->v_stride[i] < 0) return WHTQ_EINVAL;
+  if (int4)
+    for (int i = 0; i < 2; ++i)
+      if (c->ks_stride[i] < 0 || c->vs_stride[i] < 0) return WHTQ_EINVAL;
+  const int shift = ilog2_pow2(c->page_size);
+  if (c->dim != 64 && c->dim != 128) return WHTQ_EUNSUPPORTED;
+  if (shift < 4 || shift > 16 || c->num_pages > kMost || c->kv_heads > 65535) return WHTQ_EUNSUPPORTED;
+  if (!aligned16(c->k) || !aligned16(c->v)) return WHTQ_EALIGN;
+  for (int i = 0; i < 3; ++i)
+    if ((c->k_stride[i] * esz & 15) || (c->v_stride[i] * esz & 15)) return WHTQ_EALIGN;
+  if (int4) {
+    if ((reinterpret_cast<uintptr_t>(c->k_scales) & 7u) || (reinterpret_cast<uintptr_t>(c->v_scales) & 7u)) return WHTQ_EALIGN;
+    for (int i = 0; i < 2; ++i)
+      if ((c->ks_stride[i] & 3) || (c->vs_stride[i] & 3)) return WHTQ_EALIGN;
+    if (reinterpret_cast<uintptr_t>(c->sign_bits) & 3u) return WHTQ_EALIGN;
+  }
+  *out = KvCache{};
+  out->k = {(uint8_t*)c->k, c->k_scales, c->k_stride[0] * esz, c->k_stride[1] * esz, c->k_stride[2] * esz,
+            c->ks_stride[0], c->ks_stride[1]};
+  out->v = {(uint8_t*)c->v, c->v_scales, c->v_stride[0] * esz, c->v_stride[1] * esz, c->v_stride[2] * esz,
+            c->vs_stride[0], c->vs_stride[1]};
+  out->signs = int4 ? c->sign_bits : nullptr;
+  out->num_pages = c->num_pages;
+  out->page_shift = shift;
+  out->kv_heads = (int)c->kv_heads;
+  return WHTQ_OK;
+}
+
+// rows of 16-bit head vectors: [token][head] strides in elements
+bool kv_rows_valid(const int64_t* st) { return st && st[0] >= 0 && st[1] >= 0; }
+bool kv_rows_aligned(const void* p, const int64_t* st) { return aligned16(p) && !((st[0] * 2) & 15) && !((st[1] * 2) & 15); }
+
+// how an attention call runs: which kernel, and over how many blocks the keys of a row are split
+struct KvPlan {
+  bool step;
+  int nq, splits, split_keys;
+  int64_t tiles, bytes;
+};
+
+KvPlan kv_plan(int64_t dim, int64_t kv_heads, int64_t q_tokens, int64_t heads, int64_t seqs, int64_t max_q,
+               int64_t max_kv, int cus) {
+  KvPlan p{};
+  const int64_t group = heads / kv_heads;
+  p.step = max_q * group <= 32;
+  p.nq = max_q * group <= 16 ? 1 : 2;
+  const int64_t rows = kv_chunk_rows();
+  p.tiles = q_tokens * group / rows + seqs;
+  // blocks without a split, how many are wanted, and the fewest keys worth a block
+  const int64_t blocks = p.step ? seqs * kv_heads : (q_tokens * group + rows - 1) / rows * kv_heads;
+  const int64_t want = p.step ? 4 * cus : 2 * cus, least = p.step ? 256 : 512, grain = p.step ? 128 : 64;
+  int64_t splits = std::max<int64_t>(1, std::min((want + blocks - 1) / blocks, max_kv / least));
+  const int64_t keys = std::max<int64_t>(grain, ((max_kv + splits - 1) / splits + grain - 1) / grain * grain);
+  splits = std::max<int64_t>(1, (max_kv + keys - 1) / keys);
+  p.splits = (int)splits;
+  p.split_keys = (int)keys;
+  p.bytes = splits > 1 ? (splits * q_tokens * heads * (dim + 2) * 4 + 15) / 16 * 16 : 0;
+  return p;
+}
+
+whtq_status kv_attn_sizes(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t seqs, int64_t max_q,
+                          int64_t max_kv) {
+  if (q_tokens < 0 || seqs < 0 || heads < 1 || max_q < 0 || max_kv < 0 || heads % c->kv_heads) return WHTQ_EINVAL;
+  if (q_tokens > kMost || seqs > kMost || heads > 65535 || max_q > kMost || max_kv > kMost) return WHTQ_EUNSUPPORTED;
+  return WHTQ_OK;
+}
+
+int kv_cus() {
+  int dev = 0;
+  (void)hipGetDevice(&dev);
+  return device_cu_count(dev);
+}
+
+}  // namespace
+
+extern "C" {
+
+whtq_status kv_append(const whtq_kv_cache* cache, const void* k, const int64_t* k_stride, const void* v,
+                      const int64_t* v_stride, whtq_dtype dtype, int64_t tokens, const int64_t* slots,
+                      const whtq_rope* rope, const void* q, const int64_t* q_stride, int64_t heads, void* q_out,
+                      const int64_t* q_out_stride, void* stream) {
+  KvCache c;
+  whtq_status st = kv_check(cache, &c);
+  if (st != WHTQ_OK) return st;
+  if (!kv_dtype(dtype) || tokens < 0) return WHTQ_EINVAL;
+  if (cache->format == WHTQ_KV_DENSE && dtype != cache->dtype) return WHTQ_EINVAL;
+  if (!kv_rows_valid(k_stride) || !kv_rows_valid(v_stride)) return WHTQ_EINVAL;
+  if (tokens > 0 && (!k || !v || !slots)) return WHTQ_EINVAL;
+  if (q && (heads < 1 || !q_out || !kv_rows_valid(q_stride) || !kv_rows_valid(q_out_stride))) return WHTQ_EINVAL;
+  if (q && q == q_out && (q_stride[0] != q_out_stride[0] || q_stride[1] != q_out_stride[1])) return WHTQ_EINVAL;
+  if (rope) {
+    if (rope->rot_dim < 16 || rope->rot_dim > cache->dim || rope->rot_dim % 16) return WHTQ_EINVAL;
+    if (rope->interleaved != 0 && rope->interleaved != 1) return WHTQ_EINVAL;
+    if (rope->max_position < 1 || rope->ld < rope->rot_dim / 2) return WHTQ_EINVAL;
+    if (tokens > 0 && (!rope->cos || !rope->sin || !rope->positions)) return WHTQ_EINVAL;
+  }
+  if (tokens > kMost || (q && heads > 65535)) return WHTQ_EUNSUPPORTED;
+  if (!kv_rows_aligned(k, k_stride) || !kv_rows_aligned(v, v_stride)) return WHTQ_EALIGN;
+  if (q && (!kv_rows_aligned(q, q_stride) || !kv_rows_aligned(q_out, q_out_stride))) return WHTQ_EALIGN;
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return WHTQ_EALIGN;
+  if (rope && (!aligned16(rope->cos) || !aligned16(rope->sin) || (rope->ld & 3) || !aligned4(rope->positions)))
+    return WHTQ_EALIGN;
+  if (tokens == 0) return WHTQ_OK;
+  st = need_device();
+  if (st != WHTQ_OK) return st;
+  return hip_status(launch_kv_append(c, (int)cache->dim, dtype, cache->format == WHTQ_KV_INT4, tokens, k, k_stride, v,
+                                     v_stride, slots, cache->num_pages * cache->page_size, rope ? rope->cos : nullptr,
+                                     rope ? rope->sin : nullptr, rope ? rope->positions : nullptr,
+                                     rope ? rope->ld : 0, rope ? rope->max_position : 0, rope ? rope->rot_dim : 0,
+                                     rope ? rope->interleaved : 0, q, q_stride, q ? (int)heads : 0, q_out,
+                                     q_out_stride, (hipStream_t)stream));
+}
+
+whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t* slots, void* k_out,
+                      const int64_t* k_stride, void* v_out, const int64_t* v_stride, whtq_dtype dtype,
+                      void* stream) {
+  KvCache c;
+  whtq_status st = kv_check(cache, &c);
+  if (st != WHTQ_OK) return st;
+  if (!kv_dtype(dtype) || tokens < 0) return WHTQ_EINVAL;
+  if (cache->format == WHTQ_KV_DENSE && dtype != cache->dtype) return WHTQ_EINVAL;
+  if ((k_out && !kv_rows_valid(k_stride)) || (v_out && !kv_rows_valid(v_stride))) return WHTQ_EINVAL;
+  if (tokens > 0 && ((!k_out && !v_out) || !slots)) return WHTQ_EINVAL;
+  if (tokens > kMost) return WHTQ_EUNSUPPORTED;
+  if ((k_out && !kv_rows_aligned(k_out, k_stride)) || (v_out && !kv_rows_aligned(v_out, v_stride))) return WHTQ_EALIGN;
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return WHTQ_EALIGN;
+  if (tokens == 0) return WHTQ_OK;
+  st = need_device();
+  if (st != WHTQ_OK) return st;
+  return hip_status(launch_kv_gather(c, (int)cache->dim, dtype, cache->format == WHTQ_KV_INT4, tokens, slots,
+                                     cache->num_pages * cache->page_size, k_out, k_stride, v_out, v_stride,
+                                     (hipStream_t)stream));
+}
+
+int64_t kv_attention_workspace_bytes(const whtq_kv_cache* cache, int64_t q_tokens, int64_t heads, int64_t seqs,
+                                     int64_t max_q_len, int64_t max_kv_len) {
+  KvCache c;
+  if (kv_check(cache, &c) != WHTQ_OK) return -1;
+  if (kv_attn_sizes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len) != WHTQ_OK) return -1;
+  if (need_device() != WHTQ_OK) return -1;
+  if (q_tokens == 0 || seqs == 0) return 0;
+  return kv_plan(cache->dim, cache->kv_heads, q_tokens, heads, seqs, max_q_len, max_kv_len, kv_cus()).bytes;
+}
+
+whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_t* q_stride, whtq_dtype dtype,
+                         int64_t q_tokens, int64_t heads, int64_t seqs, const int32_t* q_start,
+                         const int32_t* kv_len, const int32_t* block_table, int64_t table_stride,
+                         int64_t table_width, int64_t max_q_len, int64_t max_kv_len, float scale, int causal,
+                         int64_t window, void* out, const int64_t* out_stride, float* lse, void* workspace,
+                         int64_t workspace_bytes, void* stream) {
+  KvAttnArgs a{};
+  whtq_status st = kv_check(cache, &a.c);
+  if (st != WHTQ_OK) return st;
+  st = kv_attn_sizes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len);
+  if (st != WHTQ_OK) return st;
+  if (!kv_dtype(dtype) || (cache->format == WHTQ_KV_DENSE && dtype != cache->dtype)) return WHTQ_EINVAL;
+  if ((causal != 0 && causal != 1) || window < 0 || !std::isfinite(scale) || workspace_bytes < 0) return WHTQ_EINVAL;
+  if (table_width < 0 || table_stride < table_width) return WHTQ_EINVAL;
+  if (!kv_rows_valid(q_stride) || !kv_rows_valid(out_stride)) return WHTQ_EINVAL;
+  const bool any = q_tokens > 0 && seqs > 0;
+  if (any && (!q || !out || !q_start || !kv_len || (table_width > 0 && !block_table))) return WHTQ_EINVAL;
+  if (any && q == out) return WHTQ_EINVAL;
+  if (table_width > kMost) return WHTQ_EUNSUPPORTED;
+  if (!kv_rows_aligned(q, q_stride) || !kv_rows_aligned(out, out_stride) || !aligned16(workspace)) return WHTQ_EALIGN;
+  if (!aligned4(q_start) || !aligned4(kv_len) || !aligned4(block_table) || !aligned4(lse)) return WHTQ_EALIGN;
+  if (!any) return WHTQ_OK;
+  st = need_device();
+  if (st != WHTQ_OK) return st;
+  const KvPlan p = kv_plan(cache->dim, cache->kv_heads, q_tokens, heads, seqs, max_q_len, max_kv_len, kv_cus());
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return WHTQ_EINVAL;
+  if ((p.step ? seqs : p.tiles) * cache->kv_heads * p.splits > INT32_MAX) return WHTQ_EUNSUPPORTED;
+  a.q = (const uint8_t*)q;
+  a.out = (uint8_t*)out;
+  a.q_tok = q_stride[0] * 2;
+  a.q_head = q_stride[1] * 2;
+  a.o_tok = out_stride[0] * 2;
+  a.o_head = out_stride[1] * 2;
+  a.lse = lse;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.table_width = (int)table_width;
+  a.q_tokens = q_tokens;
+  a.heads = (int)heads;
+  a.group = (int)(heads / cache->kv_heads);
+  a.seqs = (int)seqs;
+  a.causal = causal;
+  a.window = (int)std::min(window, kMost);
+  a.splits = p.splits;
+  a.split_keys = p.split_keys;
+  a.scale = scale * 1.4426950408889634f;
+  a.part_o = (float*)workspace;
+  a.part_ml = a.part_o + (int64_t)p.splits * q_tokens * heads * cache->dim;
+  const bool int4 = cache->format == WHTQ_KV_INT4;
+  const hipStream_t s = (hipStream_t)stream;
+  const int dim = (int)cache->dim;
+  hipError_t e = p.step ? launch_kv_step(a, dim, dtype, int4, p.nq, s) : launch_kv_chunk(a, dim, dtype, int4, p.tiles, s);
+  if (e == hipSuccess && p.splits > 1) e = launch_kv_join(a, dim, dtype, int4, s);
+  return hip_status(e);
 }
 
 }  // extern "C"

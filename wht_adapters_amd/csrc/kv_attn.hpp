@@ -1,0 +1,74 @@
+// Shared by the attention kernels over a paged cache: arguments, the keys a
+// query sees, and the softmax of scores held as S^T.
+//
+// Both kernels compute S^T = K Q^T and O^T = V^T P^T, so that a lane's
+// column is ONE query: its scores, maximum, sum and outputs stay in that
+// lane (and the few lanes that share the column), the probabilities are
+// already the second product's operand, and no score crosses lanes but for
+// the maximum.  The order of the keys inside a product is free, so the
+// values are read in the order the scores came out in.
+#pragma once
+
+#include "kv.hpp"
+
+namespace whtq {
+
+struct KvAttnArgs {
+  KvCache c;
+  const uint8_t* q;
+  uint8_t* out;
+  int64_t q_tok, q_head, o_tok, o_head;  // bytes
+  float* lse;
+  const int32_t *q_start, *kv_len, *table;
+  int64_t table_stride;
+  float *part_o, *part_ml;  // [split][q_tokens * heads][D], [..][2]; splits > 1
+  int64_t q_tokens;
+  int table_width, heads, group, seqs, causal, window, splits, split_keys;
+  float scale;  // times log2(e)
+};
+
+constexpr float KV_NEG_INF = -__builtin_huge_valf();
+
+// exp2 of a score against the running maximum (a maximum of -inf means that
+// nothing was seen yet: the score is -inf too and gives 0).
+__device__ __forceinline__ float kv_base(float m) { return m == KV_NEG_INF ? 0.f : m; }
+// What sums and outputs are multiplied by when the maximum goes from m to mn.
+__device__ __forceinline__ float kv_alpha(float m, float mn) {
+  return m == KV_NEG_INF ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+}
+
+// Scores are compared with a maximum that may lag behind by up to 2^KV_LAG:
+// the accumulators are rescaled only when a score exceeds it by more.  The
+// probabilities then reach 2^KV_LAG at most (far inside fp16's range) and the
+// final division by the sum makes the result the same.
+constexpr float KV_LAG = 6.f;
+
+// The page a table entry names; entries outside the cache read page 0.
+__device__ __forceinline__ int64_t kv_page(const KvAttnArgs& a, const int32_t* row, int key) {
+  const int p = row[key >> a.c.page_shift];
+  return (uint32_t)p < (uint64_t)a.c.num_pages ? p : 0;
+}
+
+template <int T>
+__device__ __forceinline__ f32x4 kv_mfma16(u32x4 x, u32x4 y, f32x4 c) {
+  if constexpr (T == KV_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x), __builtin_bit_cast(bf16x8_t, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, x), __builtin_bit_cast(f16x8_t, y), c, 0, 0, 0);
+}
+template <int T>
+__device__ __forceinline__ f32x16 kv_mfma32(u32x4 x, u32x4 y, f32x16 c) {
+  if constexpr (T == KV_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, x), __builtin_bit_cast(bf16x8_t, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, x), __builtin_bit_cast(f16x8_t, y), c, 0, 0, 0);
+}
+
+// Whether any 16-bit float among the words folded into m (absmax16) is an
+// infinity or NaN.
+template <int T>
+__device__ __forceinline__ bool kv_not_finite(u16x2 m) {
+  return absmax16(m) >= (T == KV_BF16 ? 0x7f80u : 0x7c00u);
+}
+
+}  // namespace whtq

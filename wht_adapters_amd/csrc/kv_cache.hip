@@ -1,0 +1,297 @@
+// kv_append and kv_gather: rows between dense tensors and a paged cache.
+//
+// A row (one head vector of D values) belongs to L = D / 16 lanes; lane i
+// holds the 8-value chunks i and i + L, so that a full-width rotation in
+// halves pairs values inside a lane, every access is 16 bytes and L lanes
+// cover contiguous runs.  The transform of an INT4 row is then one butterfly
+// between the two chunks, three inside a chunk and log2 L between lanes.
+//
+// Both kernels move bytes: what bounds them is memory (and, for a few
+// tokens, the latency of the chain slot / position -> table row -> store).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kv.hpp"
+#include "launch.hpp"
+
+namespace whtq {
+
+struct KvRows {
+  const uint8_t* p;
+  int64_t tok, head;  // bytes
+};
+struct KvAppendArgs {
+  KvCache c;
+  KvRows k, v, q, qo;
+  const int64_t* slots;
+  const float *cos, *sin;
+  const int32_t* pos;
+  int64_t ld_cs, max_pos, capacity;
+  uint32_t rows;  // tokens * (heads + 2 kv_heads)
+  int heads, rot, interleaved;
+};
+
+// The two chunks of a lane rotated in place.  Each product and each sum is
+// rounded by itself (no contraction), so the result is the same wherever it
+// is computed.
+template <int D, int T>
+__device__ __forceinline__ void kv_rotate(float (&x)[16], const KvAppendArgs& a, int64_t pos, int i, const uint8_t* row) {
+#pragma clang fp contract(off)
+  constexpr int L = D / 16;
+  const float* cs = a.cos + pos * a.ld_cs;
+  const float* sn = a.sin + pos * a.ld_cs;
+  if (!a.interleaved && a.rot == D) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 c = ldg<f32x4>(cs + 8 * i + 4 * h), s = ldg<f32x4>(sn + 8 * i + 4 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = x[4 * h + e], w = x[8 + 4 * h + e];
+        x[4 * h + e] = u * c[e] - w * s[e];
+        x[8 + 4 * h + e] = w * c[e] + u * s[e];
+      }
+    }
+    return;
+  }
+  const int pair = a.rot / 16;  // chunks in a half
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int ch = i + b * L;
+    if (ch * 8 >= a.rot) continue;
+    if (a.interleaved) {
+      const f32x4 c = ldg<f32x4>(cs + 4 * ch), s = ldg<f32x4>(sn + 4 * ch);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = x[8 * b + 2 * e], w = x[8 * b + 2 * e + 1];
+        x[8 * b + 2 * e] = u * c[e] - w * s[e];
+        x[8 * b + 2 * e + 1] = w * c[e] + u * s[e];
+      }
+    } else {
+      const bool low = ch < pair;
+      const int at = low ? ch : ch - pair;
+      float o[8];
+      kv_widen8<T>(ldg<u32x4>(row + 16 * (low ? ch + pair : ch - pair)), o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float c = cs[8 * at + e], s = sn[8 * at + e], u = x[8 * b + e];
+        const float os = o[e] * s;
+        x[8 * b + e] = low ? u * c - os : u * c + os;
+      }
+    }
+  }
+}
+
+template <int D, int T, bool INT4>
+__global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
+  constexpr int L = D / 16, RB = 256 / L;
+  const uint32_t r = blockIdx.x * RB + threadIdx.x / L;
+  const int i = threadIdx.x % L, lane = threadIdx.x & 63;
+  const uint32_t per = a.heads + 2 * a.c.kv_heads;
+  const bool live = r < a.rows;
+  const uint32_t t = live ? r / per : 0, hs = live ? r % per : 0;
+  const int64_t pos = a.pos ? (int64_t)a.pos[t] : 0;
+  // head slots of a token: its keys, its values, its queries
+  const bool is_k = hs < (uint32_t)a.c.kv_heads, is_q = hs >= 2u * a.c.kv_heads;
+  const int h = is_k ? hs : is_q ? hs - 2 * a.c.kv_heads : hs - a.c.kv_heads;
+  const KvRows& in = is_k ? a.k : is_q ? a.q : a.v;
+  const uint8_t* row = in.p + t * in.tok + h * in.head;
+  float x[16];
+  kv_widen8<T>(ldg<u32x4>(row + 16 * i), x);
+  kv_widen8<T>(ldg<u32x4>(row + 16 * (i + L)), x + 8);
+  bool ok = live;
+  if (a.pos) ok = ok && pos >= 0 && pos < a.max_pos;
+  if (a.pos && ok && (is_k || is_q)) kv_rotate<D, T>(x, a, pos, i, row);
+  if (is_q) {
+    if (ok) {
+      uint8_t* o = const_cast<uint8_t*>(a.qo.p) + t * a.qo.tok + h * a.qo.head;
+      stg<u32x4>(o + 16 * i, kv_round8<T>(x));
+      stg<u32x4>(o + 16 * (i + L), kv_round8<T>(x + 8));
+    }
+    return;
+  }
+  const int64_t slot = a.slots[t];
+  ok = ok && slot >= 0 && slot < a.capacity;
+  const KvSide& c = is_k ? a.c.k : a.c.v;
+  const int64_t page = slot >> a.c.page_shift, off = slot & ((1 << a.c.page_shift) - 1);
+  if constexpr (!INT4) {
+    if (!ok) return;
+    uint8_t* o = c.p + page * c.page + h * c.head + off * c.tok;
+    stg<u32x4>(o + 16 * i, kv_round8<T>(x));
+    stg<u32x4>(o + 16 * (i + L), kv_round8<T>(x + 8));
+  } else {
+    if (a.c.signs) {
+      kv_sign8(x, (a.c.signs[i >> 2] >> (8 * (i & 3))) & 255u);
+      kv_sign8(x + 8, (a.c.signs[(i + L) >> 2] >> (8 * ((i + L) & 3))) & 255u);
+    }
+    kv_bfly<8>(x);
+    kv_bfly<8>(x + 8);
+#pragma unroll
+    for (int m = 1; m < L; m *= 2) kv_lane_bfly<16>(x, m, lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bfly(x[e], x[8 + e]);
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      x[e] *= D == 64 ? 0.125f : 0.08838834764831845f;  // 1 / sqrt(D)
+      top = fmaxf(top, fabsf(x[e]));
+    }
+#pragma unroll
+    for (int m = 1; m < L; m *= 2) top = fmaxf(top, __shfl_xor(top, m, 64));
+    const _Float16 s16 = (_Float16)(top / 7.0f);
+    const float s = (float)s16, inv = s > 0.f ? 1.0f / s : 0.f;
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int q = (int)__builtin_rintf(fminf(fmaxf(x[e] * inv, -7.f), 7.f));
+      w[e >> 3] |= (uint32_t)(q & 15) << (4 * (e & 7));
+    }
+    if (!ok) return;
+    uint8_t* o = c.p + page * c.page + h * c.head + off * c.tok;
+    stg<uint32_t>(o + 4 * i, w[0]);
+    stg<uint32_t>(o + 4 * (i + L), w[1]);
+    if (i == 0) c.scale[page * c.s_page + h * c.s_head + off] = __builtin_bit_cast(uint16_t, s16);
+  }
+}
+
+struct KvGatherArgs {
+  KvCache c;
+  KvRows k, v;
+  const int64_t* slots;
+  int64_t capacity;
+  uint32_t rows;  // tokens * kv_heads * sides
+  int sides;      // bit 0: keys, bit 1: values
+};
+
+template <int D, int T, bool INT4>
+__global__ __launch_bounds__(256) void k_kv_gather(const KvGatherArgs a) {
+  constexpr int L = D / 16, RB = 256 / L;
+  const uint32_t r = blockIdx.x * RB + threadIdx.x / L;
+  const int i = threadIdx.x % L, lane = threadIdx.x & 63;
+  const uint32_t per = a.c.kv_heads * (a.sides == 3 ? 2 : 1);
+  const bool live = r < a.rows;
+  const uint32_t t = live ? r / per : 0, hs = live ? r % per : 0;
+  const bool is_k = a.sides == 3 ? hs < (uint32_t)a.c.kv_heads : a.sides == 1;
+  const int h = hs < (uint32_t)a.c.kv_heads ? hs : hs - a.c.kv_heads;
+  const int64_t slot = a.slots[t];
+  const bool ok = slot >= 0 && slot < a.capacity;
+  const KvSide& c = is_k ? a.c.k : a.c.v;
+  const KvRows& out = is_k ? a.k : a.v;
+  const int64_t page = ok ? slot >> a.c.page_shift : 0, off = ok ? slot & ((1 << a.c.page_shift) - 1) : 0;
+  const uint8_t* e0 = c.p + page * c.page + h * c.head + off * c.tok;
+  uint8_t* o = const_cast<uint8_t*>(out.p) + t * out.tok + h * out.head;
+  u32x4 w0 = {0u, 0u, 0u, 0u}, w1 = w0;
+  if constexpr (!INT4) {
+    if (ok) {
+      w0 = ldg<u32x4>(e0 + 16 * i);
+      w1 = ldg<u32x4>(e0 + 16 * (i + L));
+    }
+  } else {
+    const uint32_t c0 = ldg<uint32_t>(e0 + 4 * i), c1 = ldg<uint32_t>(e0 + 4 * (i + L));
+    const uint16_t sb = c.scale[page * c.s_page + h * c.s_head + off];
+    const float s = (float)__builtin_bit_cast(_Float16, sb);
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = (float)((int)(c0 << (28 - 4 * e)) >> 28) * s;
+      x[8 + e] = (float)((int)(c1 << (28 - 4 * e)) >> 28) * s;
+    }
+    kv_bfly<8>(x);
+    kv_bfly<8>(x + 8);
+#pragma unroll
+    for (int m = 1; m < L; m *= 2) kv_lane_bfly<16>(x, m, lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bfly(x[e], x[8 + e]);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] *= D == 64 ? 0.125f : 0.08838834764831845f;  // 1 / sqrt(D)
+    if (a.c.signs) {
+      kv_sign8(x, (a.c.signs[i >> 2] >> (8 * (i & 3))) & 255u);
+      kv_sign8(x + 8, (a.c.signs[(i + L) >> 2] >> (8 * ((i + L) & 3))) & 255u);
+    }
+    if (ok) {
+      w0 = kv_round8<T>(x);
+      w1 = kv_round8<T>(x + 8);
+    }
+  }
+  if (!live) return;
+  stg<u32x4>(o + 16 * i, w0);
+  stg<u32x4>(o + 16 * (i + L), w1);
+}
+
+// Tokens go in launches of at most 2^30 rows (32-bit row numbers in the
+// kernels); one launch in any ordinary call.
+template <typename F>
+static hipError_t by_tokens(int64_t tokens, int64_t per, F launch) {
+  const int64_t most = std::max<int64_t>(1, (int64_t(1) << 30) / per);
+  for (int64_t t = 0; t < tokens; t += most) {
+    launch(t, std::min(most, tokens - t));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+#define KV_DISPATCH(KERNEL, D, T, INT4, GRID, S, ARGS)                                                      \
+  do {                                                                                                      \
+    if ((D) == 128 && (T) == KV_BF16 && (INT4)) hipLaunchKernelGGL((KERNEL<128, KV_BF16, true>), GRID, dim3(256), 0, S, ARGS); \
+    else if ((D) == 128 && (T) == KV_BF16) hipLaunchKernelGGL((KERNEL<128, KV_BF16, false>), GRID, dim3(256), 0, S, ARGS);     \
+    else if ((D) == 128 && (INT4)) hipLaunchKernelGGL((KERNEL<128, KV_F16, true>), GRID, dim3(256), 0, S, ARGS);               \
+    else if ((D) == 128) hipLaunchKernelGGL((KERNEL<128, KV_F16, false>), GRID, dim3(256), 0, S, ARGS);                        \
+    else if ((T) == KV_BF16 && (INT4)) hipLaunchKernelGGL((KERNEL<64, KV_BF16, true>), GRID, dim3(256), 0, S, ARGS);           \
+    else if ((T) == KV_BF16) hipLaunchKernelGGL((KERNEL<64, KV_BF16, false>), GRID, dim3(256), 0, S, ARGS);                    \
+    else if ((INT4)) hipLaunchKernelGGL((KERNEL<64, KV_F16, true>), GRID, dim3(256), 0, S, ARGS);                              \
+    else hipLaunchKernelGGL((KERNEL<64, KV_F16, false>), GRID, dim3(256), 0, S, ARGS);                                         \
+  } while (0)
+
+hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const void* k,
+                            const int64_t* ks, const void* v, const int64_t* vs, const int64_t* slots,
+                            int64_t capacity, const float* cos, const float* sin, const int32_t* pos, int64_t ld_cs,
+                            int64_t max_pos, int rot, int interleaved, const void* q, const int64_t* qs, int heads,
+                            void* qo, const int64_t* qos, hipStream_t s) {
+  const int rb = 256 / (dim / 16);
+  const int64_t per = (q ? heads : 0) + 2 * (int64_t)c.kv_heads;
+  return by_tokens(tokens, per, [&](int64_t t0, int64_t n) {
+    KvAppendArgs a{};
+    a.c = c;
+    a.k = {(const uint8_t*)k + t0 * ks[0] * 2, ks[0] * 2, ks[1] * 2};
+    a.v = {(const uint8_t*)v + t0 * vs[0] * 2, vs[0] * 2, vs[1] * 2};
+    if (q) {
+      a.q = {(const uint8_t*)q + t0 * qs[0] * 2, qs[0] * 2, qs[1] * 2};
+      a.qo = {(const uint8_t*)qo + t0 * qos[0] * 2, qos[0] * 2, qos[1] * 2};
+      a.heads = heads;
+    }
+    a.slots = slots + t0;
+    a.capacity = capacity;
+    a.cos = cos;
+    a.sin = sin;
+    a.pos = pos ? pos + t0 : nullptr;
+    a.ld_cs = ld_cs;
+    a.max_pos = max_pos;
+    a.rot = rot;
+    a.interleaved = interleaved;
+    a.rows = (uint32_t)(n * per);
+    const dim3 grid((unsigned)((n * per + rb - 1) / rb));
+    KV_DISPATCH(k_kv_append, dim, dt, int4, grid, s, a);
+  });
+}
+
+hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const int64_t* slots,
+                            int64_t capacity, void* ko, const int64_t* ks, void* vo, const int64_t* vs,
+                            hipStream_t s) {
+  const int rb = 256 / (dim / 16);
+  const int sides = (ko ? 1 : 0) | (vo ? 2 : 0);
+  const int64_t per = (int64_t)c.kv_heads * (sides == 3 ? 2 : 1);
+  return by_tokens(tokens, per, [&](int64_t t0, int64_t n) {
+    KvGatherArgs a{};
+    a.c = c;
+    if (ko) a.k = {(const uint8_t*)ko + t0 * ks[0] * 2, ks[0] * 2, ks[1] * 2};
+    if (vo) a.v = {(const uint8_t*)vo + t0 * vs[0] * 2, vs[0] * 2, vs[1] * 2};
+    a.slots = slots + t0;
+    a.capacity = capacity;
+    a.sides = sides;
+    a.rows = (uint32_t)(n * per);
+    const dim3 grid((unsigned)((n * per + rb - 1) / rb));
+    KV_DISPATCH(k_kv_gather, dim, dt, int4, grid, s, a);
+  });
+}
+
+}  // namespace whtq

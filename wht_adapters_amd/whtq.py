@@ -6,7 +6,9 @@ and every step of the computation runs in the library's HIP kernels.  There
 is no CPU fallback: importing this module fails if the library is missing.
 """
 import ctypes
+import dataclasses
 import os
+from typing import Optional
 
 import torch
 
@@ -18,7 +20,22 @@ if not os.path.exists(lib_path):
         f"libwhtq.so not found at {lib_path}; build it with `python -m wht_adapters_amd.build`")
 _lib = ctypes.CDLL(lib_path)
 
-_i64, _int, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+_i64, _int, _vp, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float
+
+
+class _Cache(ctypes.Structure):  # whtq_kv_cache
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scales", _vp), ("v_scales", _vp), ("sign_bits", _vp),
+                ("num_pages", _i64), ("page_size", _i64), ("kv_heads", _i64), ("dim", _i64),
+                ("k_stride", _i64 * 3), ("v_stride", _i64 * 3), ("ks_stride", _i64 * 2), ("vs_stride", _i64 * 2),
+                ("format", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):  # whtq_rope
+    _fields_ = [("cos", _vp), ("sin", _vp), ("positions", _vp), ("ld", _i64), ("max_position", _i64),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+_cache_p, _rope_p, _i64_p = ctypes.POINTER(_Cache), ctypes.POINTER(_Rope), ctypes.POINTER(_i64)
 
 _SIG = {
     "wht_batched": [_vp, _int, _vp, _int, _i64, _i64, _i64, _i64, _vp, _int, _int, _vp],
@@ -47,6 +64,10 @@ _SIG = {
     "qwha_forward_plan": [_i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp],
     "qwha_adapter_forward_planned": [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _int, _i64, _i64, _vp, _i64,
                                      _vp, _int, _i64, _vp],
+    "kv_append": [_cache_p, _vp, _i64_p, _vp, _i64_p, _int, _i64, _vp, _rope_p, _vp, _i64_p, _i64, _vp, _i64_p, _vp],
+    "kv_gather": [_cache_p, _i64, _vp, _vp, _i64_p, _vp, _i64_p, _int, _vp],
+    "kv_attention": [_cache_p, _vp, _i64_p, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32,
+                     _int, _i64, _vp, _i64_p, _vp, _vp, _i64, _vp],
 }
 for _name, _args in _SIG.items():
     _f = getattr(_lib, _name)
@@ -56,6 +77,8 @@ _lib.qwha_grad_values_workspace_bytes.argtypes = [_i64, _i64, _i64]
 _lib.qwha_grad_values_workspace_bytes.restype = _i64
 _lib.qwha_forward_plan_bytes.argtypes = [_i64, _i64, _i64, _i64]
 _lib.qwha_forward_plan_bytes.restype = _i64
+_lib.kv_attention_workspace_bytes.argtypes = [_cache_p, _i64, _i64, _i64, _i64, _i64]
+_lib.kv_attention_workspace_bytes.restype = _i64
 _lib.whtq_status_string.argtypes = [_int]
 _lib.whtq_status_string.restype = ctypes.c_char_p
 _lib.whtq_last_hip_error.restype = _int
@@ -590,6 +613,225 @@ def qwha_initialize(w, codes, scales, signs, bits, group, x, total, floor, cap):
     col_idx = qwha_init_select(f, row_ptr)
     vals = qwha_init_refine(g, p, row_ptr, col_idx)
     return row_ptr, col_idx, vals, err
+
+
+# ------------------------------------------------------------ paged key/value cache
+
+@dataclasses.dataclass
+class KVCache:
+    """A paged cache of keys and values (include/whtq.h, whtq_kv_cache).
+
+    k, v: [pages, kv_heads, page_size, dim] bfloat16 or float16, or uint8
+    [pages, kv_heads, page_size, dim / 2] INT4 codes with float16 k_scales,
+    v_scales [pages, kv_heads, page_size] and a sign bitmask (dim / 32 words,
+    or None).  Any strides with a contiguous last dimension that the header's
+    alignment allows (a transposed [pages, page_size, kv_heads, dim] too).
+    The tensors stay the caller's; their addresses are read when the cache is
+    first used, so give a changed tensor to a new KVCache."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: Optional[torch.Tensor] = None
+    v_scales: Optional[torch.Tensor] = None
+    signs: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        for nm, t in (("k", self.k), ("v", self.v)):
+            _need_cuda(nm, t)
+            if t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError(f"{nm} must be [pages, kv_heads, page_size, dim] with a contiguous last dimension")
+        if self.k.shape != self.v.shape or self.k.dtype != self.v.dtype or self.k.device != self.v.device:
+            raise ValueError("k and v must have one shape, dtype and device")
+        c = _Cache()
+        self.int4 = self.k.dtype == torch.uint8
+        if not self.int4 and self.k.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("k and v must be bfloat16, float16 or uint8 (INT4 codes)")
+        c.num_pages, c.kv_heads, c.page_size, c.dim = self.k.shape
+        c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
+        c.k_stride[:], c.v_stride[:] = self.k.stride()[:3], self.v.stride()[:3]
+        c.format = int(self.int4)
+        if self.int4:
+            c.dim = 2 * self.k.shape[3]
+            for nm, t in (("k_scales", self.k_scales), ("v_scales", self.v_scales)):
+                _need_cuda(nm, t)
+                if t.dtype != torch.float16 or t.shape != self.k.shape[:3] or t.stride(2) != 1:
+                    raise ValueError(f"{nm} must be float16 [pages, kv_heads, page_size] with contiguous offsets")
+                if t.device != self.k.device:
+                    raise ValueError(f"{nm} must be on k's device")
+            c.k_scales, c.v_scales = self.k_scales.data_ptr(), self.v_scales.data_ptr()
+            c.ks_stride[:], c.vs_stride[:] = self.k_scales.stride()[:2], self.v_scales.stride()[:2]
+            c.sign_bits = _sign_ptr(self.signs, c.dim, self.k.device).value
+        else:
+            if self.k_scales is not None or self.v_scales is not None or self.signs is not None:
+                raise ValueError("scales and signs belong to INT4 caches")
+            c.dtype = _DT[self.k.dtype]
+        self._c = c
+
+    @property
+    def dim(self):
+        return self._c.dim
+
+    @property
+    def kv_heads(self):
+        return self._c.kv_heads
+
+    @property
+    def page_size(self):
+        return self._c.page_size
+
+
+def kv_cache_alloc(num_pages, page_size, kv_heads, dim, *, int4=False, dtype=torch.bfloat16, signs=None, device="cuda"):
+    """A zero-filled KVCache: 16-bit pages, or INT4 codes with scales."""
+    if not int4:
+        shape = (num_pages, kv_heads, page_size, dim)
+        return KVCache(*(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)))
+    codes = [torch.zeros((num_pages, kv_heads, page_size, dim // 2), dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.zeros((num_pages, kv_heads, page_size), dtype=torch.float16, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales, signs)
+
+
+def _head_rows(name, t, cache, heads=None, dtype=None):
+    """Strides of a [tokens, heads, dim] tensor with contiguous head vectors."""
+    _need_cuda(name, t)
+    if t.dim() != 3 or t.shape[2] != cache.dim or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens, heads, {cache.dim}] with a contiguous last dimension")
+    if heads is not None and t.shape[1] != heads:
+        raise ValueError(f"{name} must have {heads} heads")
+    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'bfloat16 or float16'}")
+    if not cache.int4 and t.dtype != cache.k.dtype:
+        raise ValueError(f"{name} must have the cache's dtype")
+    if t.device != cache.k.device:
+        raise ValueError(f"{name} must be on the cache's device")
+    # the stride of a dimension of one entry is meaningless
+    return (_i64 * 2)(t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _ints(name, t, dtype, device, shape=None):
+    _need_cuda(name, t)
+    if t.dtype != dtype or not t.is_contiguous() or t.device != device or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape) if shape is not None else ''} on the cache's device")
+
+
+def kv_append(cache, k, v, slots, *, q=None, cos=None, sin=None, positions=None, rot_dim=None, interleaved=False,
+              q_out=None):
+    """Rotates new keys (and queries) by their positions and writes keys and
+    values [tokens, kv_heads, dim] into the cache's slots (int64 [tokens];
+    outside the cache: not written).  cos, sin: float32 [positions, rot_dim /
+    2] tables, or None for no rotation; positions: int32 [tokens].  Returns
+    the rotated queries (q_out, q's shape; q_out=q rotates in place)."""
+    ks = _head_rows("k", k, cache, cache.kv_heads)
+    vs = _head_rows("v", v, cache, cache.kv_heads, k.dtype)
+    tokens, dev = k.shape[0], k.device
+    if v.shape[0] != tokens:
+        raise ValueError("k and v must have the same number of tokens")
+    _ints("slots", slots, torch.int64, dev, (tokens,))
+    rope = None
+    if cos is not None or sin is not None or positions is not None:
+        for nm, t in (("cos", cos), ("sin", sin)):
+            _need_cuda(nm, t)
+            if t.dtype != torch.float32 or t.dim() != 2 or t.stride(1) != 1 or t.device != dev:
+                raise ValueError(f"{nm} must be float32 [positions, rot_dim / 2] with a contiguous last dimension")
+        if cos.shape != sin.shape or cos.stride() != sin.stride():
+            raise ValueError("cos and sin must have one shape and layout")
+        _ints("positions", positions, torch.int32, dev, (tokens,))
+        rot = int(rot_dim) if rot_dim is not None else 2 * cos.shape[1]
+        if rot > 2 * cos.shape[1]:
+            raise ValueError("cos and sin must hold rot_dim / 2 entries a row")
+        ld = cos.stride(0) if cos.shape[0] > 1 else -(-cos.shape[1] // 4) * 4
+        rope = _Rope(cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), ld, cos.shape[0], rot, int(bool(interleaved)))
+    qs = qos = None
+    heads = 0
+    if q is not None:
+        qs = _head_rows("q", q, cache, None, k.dtype)
+        heads = q.shape[1]
+        if q.shape[0] != tokens:
+            raise ValueError("q and k must have the same number of tokens")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        qos = _head_rows("q_out", q_out, cache, heads, q.dtype)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out shape mismatch")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    with torch.cuda.device(dev):
+        _check("kv_append", _lib.kv_append(
+            cache._c, _ptr(k), ks, _ptr(v), vs, _DT[k.dtype], tokens, _ptr(slots), rope, _ptr(q), qs, heads,
+            _ptr(q_out), qos, _stream(k)))
+    return q_out
+
+
+def kv_gather(cache, slots, *, dtype=None, k_out=None, v_out=None):
+    """(k, v) [tokens, kv_heads, dim]: what the cache's slots (int64 [tokens])
+    stand for; zeros for a slot outside the cache.  dtype: an INT4 cache's
+    output type (bfloat16 by default)."""
+    dev = cache.k.device
+    _ints("slots", slots, torch.int64, dev)
+    tokens = slots.numel()
+    dtype = dtype or (torch.bfloat16 if cache.int4 else cache.k.dtype)
+    outs = []
+    for nm, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = torch.empty((tokens, cache.kv_heads, cache.dim), dtype=dtype, device=dev)
+        outs.append((t, _head_rows(nm, t, cache, cache.kv_heads, dtype)))
+        if t.shape[0] != tokens:
+            raise ValueError(f"{nm} must have one row per slot")
+    (k, ks), (v, vs) = outs
+    with torch.cuda.device(dev):
+        _check("kv_gather", _lib.kv_gather(cache._c, tokens, _ptr(slots), _ptr(k), ks, _ptr(v), vs, _DT[dtype],
+                                           _stream(cache.k)))
+    return k, v
+
+
+def kv_attention_workspace_bytes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len):
+    with torch.cuda.device(cache.k.device):
+        return int(_lib.kv_attention_workspace_bytes(cache._c, q_tokens, heads, seqs, max_q_len, max_kv_len))
+
+
+def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_len, scale=None, causal=True, window=0,
+                 out=None, lse=None, workspace=None):
+    """Attention of new tokens q [tokens, heads, dim] over their sequences'
+    pages.  q_start: int32 [seqs + 1]; kv_len: int32 [seqs] (keys, the new
+    tokens' included); block_table: int32 [seqs, width].  max_q_len and
+    max_kv_len bound the lengths (host numbers).  scale: 1 / sqrt(dim) by
+    default; window: 0, or how many of the latest keys a query sees.  lse: a
+    float32 [tokens, heads] tensor to fill.  workspace: a uint8 tensor of
+    kv_attention_workspace_bytes, allocated here if not given."""
+    qs = _head_rows("q", q, cache)
+    dev = q.device
+    tokens, heads = q.shape[:2]
+    seqs = kv_len.numel()
+    _ints("q_start", q_start, torch.int32, dev, (seqs + 1,))
+    _ints("kv_len", kv_len, torch.int32, dev, (seqs,))
+    _need_cuda("block_table", block_table)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != seqs or \
+            block_table.device != dev or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [seqs, width] with a contiguous last dimension")
+    width = block_table.shape[1]
+    if heads % cache.kv_heads:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if out.shape != q.shape:
+        raise ValueError("out shape mismatch")
+    outs = _head_rows("out", out, cache, heads, q.dtype)
+    if lse is not None:
+        _need_cuda("lse", lse)
+        if lse.dtype != torch.float32 or lse.shape != (tokens, heads) or not lse.is_contiguous() or lse.device != dev:
+            raise ValueError("lse must be contiguous float32 [tokens, heads]")
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = _lib.kv_attention_workspace_bytes(cache._c, tokens, heads, seqs, max_q_len, max_kv_len)
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check("kv_attention", _lib.kv_attention(
+            cache._c, _ptr(q), qs, _DT[q.dtype], tokens, heads, seqs, _ptr(q_start), _ptr(kv_len),
+            _ptr(block_table), block_table.stride(0) if seqs > 1 else width, width, max_q_len, max_kv_len,
+            cache.dim ** -0.5 if scale is None else scale, int(bool(causal)), window, _ptr(out), outs, _ptr(lse),
+            _ptr(workspace), wbytes, _stream(q)))
+    return out
 
 
 def stream_probe(src, dst):
