@@ -43,10 +43,11 @@ __device__ __forceinline__ float kv_alpha(float m, float mn) {
 // final division by the sum makes the result the same.
 constexpr float KV_LAG = 6.f;
 
-// The page a table entry names; entries outside the cache read page 0.
-__device__ __forceinline__ int64_t kv_page(const KvAttnArgs& a, const int32_t* row, int key) {
-  const int p = row[key >> a.c.page_shift];
-  return (uint32_t)p < (uint64_t)a.c.num_pages ? p : 0;
+// The page a table entry names; entries outside the cache read page 0.  The
+// kernels load entries one tile of keys ahead of the keys themselves, so that
+// a tile's copies never wait for them.
+__device__ __forceinline__ int kv_page(const KvAttnArgs& a, int entry) {
+  return (uint32_t)entry < (uint64_t)a.c.num_pages ? entry : 0;
 }
 
 template <int T>

@@ -133,12 +133,16 @@ __global__ __launch_bounds__(256) void k_kv_step(const KvAttnArgs a) {
     uint32_t v[8][VW];
     u32x2 ks[2], vs[2];
   };
-  auto fetch = [&](Tile& t, int key0) {
+  // 16 keys lie in one page; lane kb holds the page of the tile's half kb
+  auto look_up = [&](int key0) {
+    const int k = min(max(key0 + 16 * (lane & 1), kfirst), klast);
+    return kv_page(a, table[k >> a.c.page_shift]);
+  };
+  auto fetch = [&](Tile& t, int key0, int pages) {
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      const int kk0 = key0 + 16 * kb;  // 16 keys lie in one page
-      const bool any = kk0 <= klast && kk0 + 15 >= kfirst;
-      const int64_t page = any ? kv_page(a, table, kk0) : 0;
+      const int kk0 = key0 + 16 * kb;
+      const int64_t page = __builtin_amdgcn_readlane(pages, kb);
       const int off = kk0 & ((1 << a.c.page_shift) - 1);
       const uint8_t* kp = kbase + page * a.c.k.page + (off + r) * a.c.k.tok;
       if constexpr (!INT4) {
@@ -179,10 +183,17 @@ __global__ __launch_bounds__(256) void k_kv_step(const KvAttnArgs a) {
   Tile cur, nxt;
   int t = t0 + wave;
   const bool work = kfirst <= klast;
-  if (work && t <= t1) fetch(cur, 32 * t);
+  int ahead = 0;
+  if (work && t <= t1) {
+    fetch(cur, 32 * t, look_up(32 * t));
+    ahead = look_up(32 * (t + 4));
+  }
   for (; work && t <= t1; t += 4) {
     const bool more = t + 4 <= t1;
-    if (more) fetch(nxt, 32 * (t + 4));
+    if (more) {
+      fetch(nxt, 32 * (t + 4), ahead);
+      ahead = look_up(32 * (t + 8));
+    }
     const int key0 = 32 * t;
     // every row sees the whole tile? (wave-uniform)
     const bool full = key0 >= (a.window > 0 ? max(kfirst, p0 + nq - a.window) : kfirst) &&
