@@ -495,8 +495,9 @@ whtq_status qwha_init_refine(const float* g, int64_t n, const float* p, int64_t 
  *     S Hn (code * scale), the row rht_dequantize_inverse would write.
  *   dim: 64 or 128.  page_size: a power of two in [16, 65536].  Strides are
  *   non-negative; 16-byte alignment of k, v and of every stride (in bytes),
- *   8-byte alignment of the scales and of their strides.  Offsets are 64-bit:
- *   a cache may exceed 4 GiB.
+ *   8-byte alignment of the scales and of their strides.  Offsets are 64-bit
+ *   (a cache may exceed 4 GiB), those inside one page of one head below 2^31
+ *   bytes.
  */
 typedef enum { WHTQ_KV_DENSE = 0, WHTQ_KV_INT4 = 1 } whtq_kv_format;
 

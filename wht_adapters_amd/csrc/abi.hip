@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <mutex>
@@ -74,6 +75,7 @@ hipError_t launch_kv_step(const KvAttnArgs& a, int dim, int dt, bool int4, int n
 hipError_t launch_kv_join(const KvAttnArgs& a, int dim, int dt, bool int4, hipStream_t s);
 hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int64_t tiles, hipStream_t s);
 int kv_chunk_rows();
+int kv_step_unit(int dim, bool int4, bool whole);
 
 static thread_local int g_last_hip = 0;
 
@@ -104,10 +106,13 @@ static whtq_status hip_status(hipError_t e) {
 
 // A device must be present and current before anything is launched.
 static whtq_status need_device() {
+  static std::atomic<bool> found{false};  // devices do not go away; the count costs a microsecond a call
+  if (found.load(std::memory_order_relaxed)) return WHTQ_OK;
   int n = 0;
   hipError_t e = hipGetDeviceCount(&n);
   if (e != hipSuccess) return hip_status(e);
   if (n < 1) return hip_status(hipErrorNoDevice);
+  found.store(true, std::memory_order_relaxed);
   return WHTQ_OK;
 }
 
@@ -747,6 +752,8 @@ whtq_status kv_check(const whtq_kv_cache* c, KvCache* out) {
   const int shift = ilog2_pow2(c->page_size);
   if (c->dim != 64 && c->dim != 128) return WHTQ_EUNSUPPORTED;
   if (shift < 4 || shift > 16 || c->num_pages > kMost || c->kv_heads > 65535) return WHTQ_EUNSUPPORTED;
+  // offsets inside a page of one head are 32-bit
+  if (std::max(c->k_stride[2], c->v_stride[2]) * esz >= (int64_t(1) << 31) / c->page_size) return WHTQ_EUNSUPPORTED;
   if (!aligned16(c->k) || !aligned16(c->v)) return WHTQ_EALIGN;
   for (int i = 0; i < 3; ++i)
     if ((c->k_stride[i] * esz & 15) || (c->v_stride[i] * esz & 15)) return WHTQ_EALIGN;
@@ -775,27 +782,46 @@ bool kv_rows_aligned(const void* p, const int64_t* st) { return aligned16(p) && 
 // how an attention call runs: which kernel, and over how many blocks the keys of a row are split
 struct KvPlan {
   bool step;
-  int nq, splits, split_keys;
-  int64_t tiles, bytes;
+  int nq, blocks, rows, splits, split_keys;
+  int64_t tiles, grid, parts, bytes;  // parts: partial rows kept
 };
 
-KvPlan kv_plan(int64_t dim, int64_t kv_heads, int64_t q_tokens, int64_t heads, int64_t seqs, int64_t max_q,
-               int64_t max_kv, int cus) {
+KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t seqs, int64_t max_q, int64_t max_kv,
+               int cus) {
   KvPlan p{};
-  const int64_t group = heads / kv_heads;
+  const int64_t group = heads / c->kv_heads, kvh = c->kv_heads;
+  const bool int4 = c->format == WHTQ_KV_INT4;
+  p.splits = 1;
   p.step = max_q * group <= 32;
-  p.nq = max_q * group <= 16 ? 1 : 2;
-  const int64_t rows = kv_chunk_rows();
-  p.tiles = q_tokens * group / rows + seqs;
-  // blocks without a split, how many are wanted, and the fewest keys worth a block
-  const int64_t blocks = p.step ? seqs * kv_heads : (q_tokens * group + rows - 1) / rows * kv_heads;
-  const int64_t want = p.step ? 4 * cus : 2 * cus, least = p.step ? 256 : 512, grain = p.step ? 128 : 64;
-  int64_t splits = std::max<int64_t>(1, std::min((want + blocks - 1) / blocks, max_kv / least));
-  const int64_t keys = std::max<int64_t>(grain, ((max_kv + splits - 1) / splits + grain - 1) / grain * grain);
-  splits = std::max<int64_t>(1, (max_kv + keys - 1) / keys);
-  p.splits = (int)splits;
-  p.split_keys = (int)keys;
-  p.bytes = splits > 1 ? (splits * q_tokens * heads * (dim + 2) * 4 + 15) / 16 * 16 : 0;
+  if (p.step) {
+    p.nq = max_q * group <= 16 ? 1 : 2;
+    p.rows = (int)std::max<int64_t>(1, max_q * group);
+    // A block takes a whole sequence when there is little to share: at most 4
+    // units each, or enough sequences to fill the machine with equal keys
+    const int64_t unit = kv_step_unit((int)c->dim, int4, true), shared = kv_step_unit((int)c->dim, int4, false);
+    if (p.nq == 1 && max_kv <= 4 * unit) {
+      p.grid = seqs * kvh;
+      return p;
+    }
+    const int64_t want = 2 * (int64_t)cus;
+    const int64_t most = seqs * ((std::max<int64_t>(max_kv, 1) + shared - 1) / shared + 1);
+    p.blocks = (int)std::max<int64_t>(1, std::min((want + kvh - 1) / kvh, most));
+    p.grid = p.blocks * kvh;
+    p.parts = (p.blocks + seqs) * kvh * p.rows;
+  } else {
+    const int64_t rows = kv_chunk_rows();
+    p.tiles = q_tokens * group / rows + seqs;
+    // blocks without a split, how many are wanted, and the fewest keys worth a block
+    const int64_t blocks = (q_tokens * group + rows - 1) / rows * kvh, want = 2 * cus, least = 512;
+    int64_t splits = std::max<int64_t>(1, std::min((want + blocks - 1) / blocks, max_kv / least));
+    const int64_t keys = std::max<int64_t>(64, ((max_kv + splits - 1) / splits + 63) / 64 * 64);
+    splits = std::max<int64_t>(1, (max_kv + keys - 1) / keys);
+    p.splits = (int)splits;
+    p.split_keys = (int)keys;
+    p.grid = p.tiles * kvh * splits;
+    if (splits > 1) p.parts = splits * q_tokens * heads;
+  }
+  if (p.parts) p.bytes = (p.parts * (c->dim + 2) * 4 + (p.step ? seqs * 8 : 0) + 15) / 16 * 16;
   return p;
 }
 
@@ -880,7 +906,7 @@ int64_t kv_attention_workspace_bytes(const whtq_kv_cache* cache, int64_t q_token
   if (kv_attn_sizes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len) != WHTQ_OK) return -1;
   if (need_device() != WHTQ_OK) return -1;
   if (q_tokens == 0 || seqs == 0) return 0;
-  return kv_plan(cache->dim, cache->kv_heads, q_tokens, heads, seqs, max_q_len, max_kv_len, kv_cus()).bytes;
+  return kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, kv_cus()).bytes;
 }
 
 whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_t* q_stride, whtq_dtype dtype,
@@ -907,9 +933,9 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   if (!any) return WHTQ_OK;
   st = need_device();
   if (st != WHTQ_OK) return st;
-  const KvPlan p = kv_plan(cache->dim, cache->kv_heads, q_tokens, heads, seqs, max_q_len, max_kv_len, kv_cus());
+  const KvPlan p = kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, kv_cus());
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return WHTQ_EINVAL;
-  if ((p.step ? seqs : p.tiles) * cache->kv_heads * p.splits > INT32_MAX) return WHTQ_EUNSUPPORTED;
+  if (p.grid > INT32_MAX) return WHTQ_EUNSUPPORTED;
   a.q = (const uint8_t*)q;
   a.out = (uint8_t*)out;
   a.q_tok = q_stride[0] * 2;
@@ -932,12 +958,15 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   a.split_keys = p.split_keys;
   a.scale = scale * 1.4426950408889634f;
   a.part_o = (float*)workspace;
-  a.part_ml = a.part_o + (int64_t)p.splits * q_tokens * heads * cache->dim;
+  a.part_ml = a.part_o + p.parts * cache->dim;
+  a.reach = (int*)(a.part_ml + 2 * p.parts);
+  a.blocks = p.blocks;
+  a.rows = p.rows;
   const bool int4 = cache->format == WHTQ_KV_INT4;
   const hipStream_t s = (hipStream_t)stream;
   const int dim = (int)cache->dim;
   hipError_t e = p.step ? launch_kv_step(a, dim, dtype, int4, p.nq, s) : launch_kv_chunk(a, dim, dtype, int4, p.tiles, s);
-  if (e == hipSuccess && p.splits > 1) e = launch_kv_join(a, dim, dtype, int4, s);
+  if (e == hipSuccess && !p.step && p.splits > 1) e = launch_kv_join(a, dim, dtype, int4, s);
   return hip_status(e);
 }
 

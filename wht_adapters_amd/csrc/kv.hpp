@@ -25,6 +25,15 @@ struct KvCache {
   int page_shift, kv_heads;
 };
 
+// Load at a wave-uniform base plus a lane's 32-bit offset: one register pair
+// for the base serves every lane.
+template <typename V>
+__device__ __forceinline__ V kv_load(const void* base, uint32_t off) {
+  const __attribute__((address_space(1))) uint8_t* p =
+      reinterpret_cast<const __attribute__((address_space(1))) uint8_t*>(reinterpret_cast<uintptr_t>(base));
+  return *reinterpret_cast<const __attribute__((address_space(1))) V*>(p + off);
+}
+
 template <int T>
 __device__ __forceinline__ uint32_t kv_pack(float lo, float hi) {
   if constexpr (T == KV_BF16) return pack_bf16(lo, hi);

@@ -21,9 +21,14 @@ struct KvAttnArgs {
   float* lse;
   const int32_t *q_start, *kv_len, *table;
   int64_t table_stride;
-  float *part_o, *part_ml;  // [split][q_tokens * heads][D], [..][2]; splits > 1
+  // partial results in fp32 (maximum and sum apart from the outputs): chunk
+  // kernel [split][q_tokens * heads], step kernel [run + sequence][kv_heads][rows]
+  float *part_o, *part_ml;
+  int* reach;  // step kernel: first and last run of each sequence
   int64_t q_tokens;
-  int table_width, heads, group, seqs, causal, window, splits, split_keys;
+  int table_width, heads, group, seqs, causal, window;
+  int splits, split_keys;  // chunk kernel
+  int blocks, rows;        // step kernel: runs a head (0: a block per sequence), rows of a sequence and head
   float scale;  // times log2(e)
 };
 

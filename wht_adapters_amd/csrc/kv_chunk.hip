@@ -150,7 +150,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   auto copy_key = [&](int n, int key0) {          // first key of copy n, wave-uniform for a given n
     return min(max(key0 + (n * NW + wave) * CR, kfirst & ~(CR - 1)), klast & ~(CR - 1));
   };
-  auto copy = [&](int buf, int key0, int pages) {  // dense; pages: lane n holds the page of copy n
+  auto copy = [&](int buf, int key0, int entry) {  // dense; lane n holds the table entry of copy n
+    const int pages = kv_page(a, entry);
 #pragma unroll
     for (int n = 0; n < COPIES; ++n) {
       const int r0 = (n * NW + wave) * CR, lr = lane / CH;
@@ -174,18 +175,19 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   uint16_t scl = 0;
   auto unit_row = [&](int n) { return (n * 64 * NW + (int)threadIdx.x) % (UNITS / 2) / UR; };
   auto inside = [&](int key) { return min(max(key, kfirst), klast); };
-  // Page numbers of a tile, held by the lanes that need them: dense, copy n's
-  // in lane n; INT4, of the thread's units and of its scale.
+  // Table entries of a tile, held by the lanes that need them: dense, copy n's
+  // in lane n; INT4, of the thread's units and of its scale.  Memory answers
+  // in order: they are asked for before the copies of the tile before.
   struct Pages {
     int at[INT4 ? UT + 1 : 1];
   };
   auto look_up = [&](Pages& p, int key0) {
     if constexpr (INT4) {
 #pragma unroll
-      for (int n = 0; n < UT; ++n) p.at[n] = kv_page(a, table[inside(key0 + unit_row(n)) >> a.c.page_shift]);
-      p.at[UT] = kv_page(a, table[inside(key0 + (int)(threadIdx.x % KV_TILE)) >> a.c.page_shift]);
+      for (int n = 0; n < UT; ++n) p.at[n] = table[inside(key0 + unit_row(n)) >> a.c.page_shift];
+      p.at[UT] = table[inside(key0 + (int)(threadIdx.x % KV_TILE)) >> a.c.page_shift];
     } else {
-      p.at[0] = kv_page(a, table[copy_key(lane % COPIES, key0) >> a.c.page_shift]);
+      p.at[0] = table[copy_key(lane % COPIES, key0) >> a.c.page_shift];
     }
   };
   auto fetch = [&](int key0, const Pages& p) {
@@ -193,13 +195,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
 #pragma unroll
       for (int n = 0; n < UT; ++n) {
         const int u = n * 64 * NW + threadIdx.x, c = u % UR;
-        const int64_t page = p.at[n];
+        const int64_t page = kv_page(a, p.at[n]);
         const int off = inside(key0 + unit_row(n)) & ((1 << a.c.page_shift) - 1);
         code[n] = u >= UNITS / 2 ? ldg_global<u32x4>(vbase + page * a.c.v.page + off * a.c.v.tok + 16 * c)
                                  : ldg_global<u32x4>(kbase + page * a.c.k.page + off * a.c.k.tok + 16 * c);
       }
       if (threadIdx.x < 2 * KV_TILE) {
-        const int64_t page = p.at[UT];
+        const int64_t page = kv_page(a, p.at[UT]);
         const int off = inside(key0 + (int)(threadIdx.x % KV_TILE)) & ((1 << a.c.page_shift) - 1);
         scl = threadIdx.x < KV_TILE ? a.c.k.scale[page * a.c.k.s_page + h * a.c.k.s_head + off]
                                     : a.c.v.scale[page * a.c.v.s_page + h * a.c.v.s_head + off];
@@ -382,14 +384,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   const int f1 = min(max(f0, (bfull1 + 1) / KV_TILE), t1 + 1);
   Pages ahead = {};
   if (work) {
-    look_up(ahead, t0 * KV_TILE);
+    Pages now;
+    look_up(now, t0 * KV_TILE);
+    look_up(ahead, (t0 + 1) * KV_TILE);
     if constexpr (INT4) {
-      fetch(t0 * KV_TILE, ahead);
+      fetch(t0 * KV_TILE, now);
       spread(0);
     } else {
-      copy(0, t0 * KV_TILE, ahead.at[0]);
+      copy(0, t0 * KV_TILE, now.at[0]);
     }
-    look_up(ahead, (t0 + 1) * KV_TILE);
   }
   int buf = 0;
   auto walk = [&](auto mask, int from, int to) {
@@ -398,9 +401,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (t < t1) {
-        if constexpr (INT4) fetch((t + 1) * KV_TILE, ahead);
-        else copy(buf ^ 1, (t + 1) * KV_TILE, ahead.at[0]);
+        const Pages now = ahead;
         look_up(ahead, (t + 2) * KV_TILE);
+        if constexpr (INT4) fetch((t + 1) * KV_TILE, now);
+        else copy(buf ^ 1, (t + 1) * KV_TILE, now.at[0]);
       }
       if constexpr (decltype(mask)::value && !INT4) {
         if (__syncthreads_or(wild(buf))) take_out(buf, t * KV_TILE);

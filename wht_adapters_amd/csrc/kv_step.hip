@@ -46,422 +46,522 @@ __device__ __forceinline__ void kv_row_rht(float* x, int sub, int step, int lane
   if constexpr (SIGN_AFTER) sign();
 }
 
+// Work of a call.  A sequence's keys are counted in units of one tile for
+// every wave of a block, at least one unit where it has queries.
+//  - whole (a.blocks == 0): a block is one sequence and head.
+//  - shared: a.blocks blocks a head take equal runs of all sequences' units
+//    (run i starts at unit i T / n).  A run that holds a sequence whole writes
+//    its result; other pieces leave (maximum, sum, output) in slot i + b,
+//    which no other piece has (a step to the right adds to i or to b), and
+//    the run with a sequence's first unit notes the runs it reaches over.
+struct KvSpan {  // a sequence's share of the work
+  int q0, nq, chunk, p0, first, last, units;
+};
+template <int NQ>
+__device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, int q0, int q1, int kv_len, int unit) {
+  KvSpan s;
+  s.q0 = q0;
+  s.chunk = q1 - q0;
+  s.nq = min(s.chunk, (16 * NQ) / a.group);
+  const int kv = min(kv_len, (int)min<int64_t>((int64_t)a.table_width << a.c.page_shift, INT32_MAX));
+  s.p0 = kv - s.chunk;  // position of the first query
+  s.first = a.window > 0 ? max(0, s.p0 - a.window + 1) : 0;  // the keys any of its queries sees
+  s.last = a.causal ? min(kv - 1, s.p0 + s.nq - 1) : kv - 1;
+  s.units = s.nq <= 0 ? 0 : max(1, s.last / unit - s.first / unit + 1);
+  if (s.last < s.first) s.units = s.nq > 0;
+  return s;
+}
+
+// Values every lane has alike, kept as such (scalar registers and branches).
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t scalar(int64_t x) {
+  return (int64_t)((uint64_t)(uint32_t)scalar((int)(x >> 32)) << 32 | (uint32_t)scalar((int)x));
+}
+
 // T: type of q and out; the operands of the products are T (dense) or fp16.
-template <int D, int T, bool INT4, int NQ>
-__global__ __launch_bounds__(256) void k_kv_step(const KvAttnArgs a) {
+template <int D, int T, bool INT4, int NQ, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
   constexpr int MT = INT4 ? KV_F16 : T;
   constexpr int KK = D / 32;   // products per 16 keys of S^T
   constexpr int DL = D / 16;   // dims a lane holds of a value row
   constexpr int VW = INT4 ? 1 : DL / 2;  // words of a value row in a lane
+  constexpr int KL = INT4 ? 1 : KK;      // loads of a lane's key share
+  constexpr int KP = (D == 128 && !INT4) ? 1 : 2;  // pairs of 16 keys in a tile
+  constexpr int TK = 32 * KP, UNIT = TK * NW;
   constexpr int PAD = D + 4;
+  constexpr int LR = D / 8;  // lanes of a row in the join
+  __shared__ __attribute__((aligned(16))) float so[NW][16][PAD];
+  __shared__ float sm[NW][16], sl[NW][16];
+  __shared__ int se[NW];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  int id = blockIdx.x;
-  const int split = id % a.splits;
-  id /= a.splits;
-  const int h = id % a.c.kv_heads, b = id / a.c.kv_heads;
 
-  const int q0 = a.q_start[b], nq = min(a.q_start[b + 1] - q0, (16 * NQ) / a.group);
-  const int rows = nq * a.group;
-  const int kv = min(a.kv_len[b], (int)min<int64_t>((int64_t)a.table_width << a.c.page_shift, INT32_MAX));
-  if (rows <= 0) return;
-  const int chunk = a.q_start[b + 1] - q0;  // positions count from the whole chunk
-  const int p0 = kv - chunk;
-  // keys any row of the block sees: [first, last]
-  int first = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
-  int last = a.causal ? min(kv - 1, p0 + nq - 1) : kv - 1;
-  const int lo = split * a.split_keys, hi = split == a.splits - 1 ? INT32_MAX : lo + a.split_keys - 1;
-  const int kfirst = max(first, lo), klast = min(last, hi);
-  const int32_t* table = a.table + b * a.table_stride;
-
-  // the lane's queries (column r of each block of 16) and what they see
-  int qpos[NQ];
-  bool qlive[NQ];
-  u32x4 qf[NQ][KK];
-  float qs[NQ];  // scale of the scores
+  // the block's run of units [u, u1), starting `at` units into sequence b
+  int h, b, run = 0, runs = 1;
+  int64_t u = 0, u1 = 1, at = 0, total = 1;
+  if (a.blocks == 0) {
+    h = blockIdx.x % a.c.kv_heads;
+    b = blockIdx.x / a.c.kv_heads;
+  } else {
+    h = blockIdx.x % a.c.kv_heads;
+    run = blockIdx.x / a.c.kv_heads;
+    auto units_of = [&](int s) {
+      return s < a.seqs ? kv_span<NQ>(a, a.q_start[s], a.q_start[s + 1], a.kv_len[s], UNIT).units : 0;
+    };
+    total = 0;
+    for (int s = 0; s < a.seqs; s += 64) {
+      int n = units_of(s + lane);
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const int row = 16 * n + r, tok = row / a.group;
-    qlive[n] = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
-    qpos[n] = p0 + tok;
-    qs[n] = a.scale;
-    const uint8_t* qp = a.q + (int64_t)(q0 + tok) * a.q_tok + (int64_t)(h * a.group + row % a.group) * a.q_head;
-    if constexpr (!INT4) {
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-        qf[n][kk] = qlive[n] ? ldg<u32x4>(qp + 64 * kk + 16 * g) : u32x4{0u, 0u, 0u, 0u};
-    } else {
-      float x[D / 4];
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-        kv_widen8<T>(qlive[n] ? ldg<u32x4>(qp + g * (D / 2) + 16 * kk) : u32x4{0u, 0u, 0u, 0u}, x + 8 * kk);
-      kv_row_rht<D, D / 4, false>(x, g, 16, lane, a.c.signs);
-      float top = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(x[e]));
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      // an exact power of two brings the row's largest value to [1, 2)
-      const int ex = top > 0.f && top < __builtin_huge_valf() ? max(-126, min(126, __builtin_amdgcn_frexp_expf(top) - 1)) : 0;
-      const float down = __builtin_ldexpf(1.f, -ex);
-      qs[n] = a.scale * __builtin_ldexpf(1.f, ex);
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          qf[n][kk][w] = pack_f16(x[8 * kk + kv_perm(2 * w)] * down, x[8 * kk + kv_perm(2 * w + 1)] * down);
-      }
+      for (int m = 1; m < 64; m *= 2) n += __shfl_xor(n, m, 64);
+      total += n;
     }
+    total = scalar(total);
+    runs = (int)min<int64_t>(a.blocks, total);
+    if (run >= runs) return;
+    u = run * total / runs;
+    u1 = (run + 1) * total / runs;
+    int64_t before = 0;
+    for (b = 0;; b += 64) {  // ends: u < total
+      const int n = units_of(b + lane);
+      int sum = n;
+#pragma unroll
+      for (int m = 1; m < 64; m *= 2) {
+        const int o = __shfl_up(sum, m, 64);
+        if (lane >= m) sum += o;
+      }
+      const uint64_t past = __ballot(before + sum > u);
+      if (past) {
+        const int i = __builtin_ctzll(past);
+        at = u - before - (__shfl(sum, i, 64) - __shfl(n, i, 64));
+        b += i;
+        break;
+      }
+      before += scalar(__shfl(sum, 63, 64));
+    }
+    at = scalar(at);
   }
 
-  float m[NQ], l[NQ];
-  f32x4 o[NQ][DL];
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    m[n] = KV_NEG_INF;
-    l[n] = 0.f;
-#pragma unroll
-    for (int i = 0; i < DL; ++i) o[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  int ve = -30;  // INT4: the outputs are in units of 2^ve (fp16's least scale is 2^-24)
+  for (; u < u1; ++b) {
+    const KvSpan sp = kv_span<NQ>(a, scalar(a.q_start[b]), scalar(a.q_start[b + 1]), scalar(a.kv_len[b]), UNIT);
+    if (sp.units == 0) {
+      if (a.blocks == 0) return;
+      continue;
+    }
+    const int q0 = sp.q0, nq = sp.nq, p0 = sp.p0, rows = nq * a.group;
+    // this piece: units [at, at + take) of the sequence
+    const int from = (int)at;
+    const int take = a.blocks == 0 ? sp.units : (int)min<int64_t>(sp.units - from, u1 - u);
+    const bool whole = take == sp.units;
+    const int base_key = sp.first / UNIT * UNIT;
+    const int kfirst = max(sp.first, base_key + from * UNIT);
+    const int klast = min(sp.last, base_key + (from + take) * UNIT - 1);
+    const int32_t* table = a.table + b * a.table_stride;
 
-  const uint8_t* kbase = a.c.k.p + h * a.c.k.head;
-  const uint8_t* vbase = a.c.v.p + h * a.c.v.head;
-  constexpr int KL = INT4 ? 1 : KK;  // 16-byte loads of a lane's key share (INT4, D = 64: 8 bytes)
-  struct Tile {
-    u32x4 k[2][KL];
-    uint32_t v[8][VW];
-    u32x2 ks[2], vs[2];
-  };
-  // 16 keys lie in one page; lane kb holds the page of the tile's half kb
-  auto look_up = [&](int key0) {
-    const int k = min(max(key0 + 16 * (lane & 1), kfirst), klast);
-    return kv_page(a, table[k >> a.c.page_shift]);
-  };
-  auto fetch = [&](Tile& t, int key0, int pages) {
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      const int kk0 = key0 + 16 * kb;
-      const int64_t page = __builtin_amdgcn_readlane(pages, kb);
-      const int off = kk0 & ((1 << a.c.page_shift) - 1);
-      const uint8_t* kp = kbase + page * a.c.k.page + (off + r) * a.c.k.tok;
-      if constexpr (!INT4) {
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) t.k[kb][kk] = ldg_global<u32x4>(kp + 64 * kk + 16 * g);
-      } else if constexpr (D == 128) {
-        t.k[kb][0] = ldg_global<u32x4>(kp + 16 * g);
-      } else {
-        const u32x2 w = ldg_global<u32x2>(kp + 8 * g);
-        t.k[kb][0] = u32x4{w.x, w.y, 0u, 0u};
-      }
-      const uint8_t* vp = vbase + page * a.c.v.page + (off + 4 * g) * a.c.v.tok + r * (INT4 ? DL / 2 : 2 * DL);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* p = vp + j * a.c.v.tok;
-        if constexpr (!INT4 && D == 128) {
-          const u32x4 w = ldg_global<u32x4>(p);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t.v[4 * kb + j][i % VW] = w[i];
-        } else if constexpr (!INT4) {
-          const u32x2 w = ldg_global<u32x2>(p);
-          t.v[4 * kb + j][0] = w.x;
-          t.v[4 * kb + j][1 % VW] = w.y;
-        } else if constexpr (D == 128) {
-          t.v[4 * kb + j][0] = ldg_global<uint32_t>(p);
-        } else {
-          t.v[4 * kb + j][0] = ldg_global<uint16_t>(p);
-        }
-      }
-      if constexpr (INT4) {
-        t.ks[kb] = ldg_global<u32x2>(a.c.k.scale + page * a.c.k.s_page + h * a.c.k.s_head + off + 4 * g);
-        t.vs[kb] = ldg_global<u32x2>(a.c.v.scale + page * a.c.v.s_page + h * a.c.v.s_head + off + 4 * g);
-      }
-    }
-  };
-
-  const int t0 = kfirst >> 5, t1 = klast >> 5;  // tiles of 32 keys; kfirst > klast: none
-  Tile cur, nxt;
-  int t = t0 + wave;
-  const bool work = kfirst <= klast;
-  int ahead = 0;
-  if (work && t <= t1) {
-    fetch(cur, 32 * t, look_up(32 * t));
-    ahead = look_up(32 * (t + 4));
-  }
-  for (; work && t <= t1; t += 4) {
-    const bool more = t + 4 <= t1;
-    if (more) {
-      fetch(nxt, 32 * (t + 4), ahead);
-      ahead = look_up(32 * (t + 8));
-    }
-    const int key0 = 32 * t;
-    // every row sees the whole tile? (wave-uniform)
-    const bool full = key0 >= (a.window > 0 ? max(kfirst, p0 + nq - a.window) : kfirst) &&
-                      key0 + 31 <= (a.causal ? min(klast, p0) : klast);
-    // what lies outside [kfirst, klast] may be anything: the values become 0
-    if constexpr (!INT4) {
-      if (key0 < kfirst || key0 + 31 > klast) {
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const int key = key0 + (s < 4 ? 0 : 16) + 4 * g + (s & 3);
-          const bool in = key >= kfirst && key <= klast;
-#pragma unroll
-          for (int w = 0; w < VW; ++w) cur.v[s][w] = in ? cur.v[s][w] : 0u;
-        }
-      }
-    }
-    float ks[8], vs[8];
-    if constexpr (INT4) {
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const uint32_t kw = cur.ks[s >> 2][(s >> 1) & 1], vw = cur.vs[s >> 2][(s >> 1) & 1];
-        ks[s] = (float)__builtin_bit_cast(_Float16, (uint16_t)(s & 1 ? kw >> 16 : kw & 0xffffu));
-        vs[s] = (float)__builtin_bit_cast(_Float16, (uint16_t)(s & 1 ? vw >> 16 : vw & 0xffffu));
-      }
-      // the largest value scale of the tile, as a power of two, sets the unit
-      float top = 0.f;
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const int key = key0 + (s < 4 ? 0 : 16) + 4 * g + (s & 3);
-        if (key >= kfirst && key <= klast && vs[s] < 65536.f) top = fmaxf(top, vs[s]);
-      }
-      if (__any(top >= __builtin_ldexpf(1.f, ve + 1))) {
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const int e = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top) - 1);
-        const float f = __builtin_ldexpf(1.f, ve - e);
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int i = 0; i < DL; ++i) o[n][i] *= f;
-        ve = e;
-      }
-      const float unit = __builtin_ldexpf(1.f, -ve);
-#pragma unroll
-      for (int s = 0; s < 8; ++s) vs[s] *= unit;
-    }
-    // S^T: s[n][4 kb + e] is key 16 kb + 4 g + e
-    float sc[NQ][8];
-    {
-      u32x4 kf[2][KK];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-          if constexpr (INT4) kf[kb][kk] = kv_codes8(cur.k[kb][0][kk]);
-          else kf[kb][kk] = cur.k[kb][kk];
-        }
-#pragma unroll
-      for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int kk = 0; kk < KK; ++kk) acc = kv_mfma16<MT>(kf[kb][kk], qf[n][kk], acc);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][4 * kb + e] = acc[e];
-        }
-    }
-    u32x4 pf[NQ];
+    // the lane's queries (column r of each block of 16) and what they see
+    int qpos[NQ];
+    u32x4 qf[NQ][KK];
+    float qs[NQ];  // scale of the scores
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      float top = KV_NEG_INF;
+      const int row = 16 * n + r, tok = row / a.group;
+      const bool live = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
+      qpos[n] = p0 + tok;
+      qs[n] = a.scale;
+      const uint8_t* qp = a.q + (int64_t)(q0 + tok) * a.q_tok + (int64_t)(h * a.group + row % a.group) * a.q_head;
+      if constexpr (!INT4) {
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        sc[n][s] *= INT4 ? qs[n] * ks[s] : qs[n];
-        if (!full) {
-          const int key = key0 + (s < 4 ? 0 : 16) + 4 * g + (s & 3);
-          const bool in = key >= kfirst && key <= klast && (!a.causal || key <= qpos[n]) &&
-                          (a.window <= 0 || key > qpos[n] - a.window);
-          sc[n][s] = in ? sc[n][s] : KV_NEG_INF;
-        }
-        top = fmaxf(top, sc[n][s]);
-      }
-      if (__any(top > m[n] + KV_LAG)) {
+        for (int kk = 0; kk < KK; ++kk)
+          qf[n][kk] = live ? ldg<u32x4>(qp + 64 * kk + 16 * g) : u32x4{0u, 0u, 0u, 0u};
+      } else {
+        float x[D / 4];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+          kv_widen8<T>(live ? ldg<u32x4>(qp + g * (D / 2) + 16 * kk) : u32x4{0u, 0u, 0u, 0u}, x + 8 * kk);
+        kv_row_rht<D, D / 4, false>(x, g, 16, lane, a.c.signs);
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(x[e]));
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float mn = fmaxf(m[n], top);
-        const float al = kv_alpha(m[n], mn);
-        l[n] *= al;
+        // an exact power of two brings the row's largest value to [1, 2)
+        const int ex = top > 0.f && top < __builtin_huge_valf() ? max(-126, min(126, __builtin_amdgcn_frexp_expf(top) - 1)) : 0;
+        const float down = __builtin_ldexpf(1.f, -ex);
+        qs[n] = a.scale * __builtin_ldexpf(1.f, ex);
 #pragma unroll
-        for (int i = 0; i < DL; ++i) o[n][i] *= al;
-        m[n] = mn;
+        for (int kk = 0; kk < KK; ++kk) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            qf[n][kk][w] = pack_f16(x[8 * kk + kv_perm(2 * w)] * down, x[8 * kk + kv_perm(2 * w + 1)] * down);
+        }
       }
-      const float base = kv_base(m[n]);
-      float p[8];
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        p[s] = __builtin_amdgcn_exp2f(sc[n][s] - base);
-        l[n] += p[s];
-        if constexpr (INT4) p[s] = sc[n][s] == KV_NEG_INF ? 0.f : p[s] * vs[s];
-      }
-#pragma unroll
-      for (int w = 0; w < 4; ++w) pf[n][w] = kv_pack<MT>(p[2 * w], p[2 * w + 1]);
     }
-    // O^T: product i yields dim DL r + i
-    auto value = [&](int i, auto keep) {  // A operand of product i; keep(s): whether slot s counts
-      u32x4 f;
+
+    float m[NQ], l[NQ];
+    f32x4 o[NQ][DL];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t x0 = keep(2 * w) ? cur.v[2 * w][i / 2 % VW] : 0u;
-        const uint32_t x1 = keep(2 * w + 1) ? cur.v[2 * w + 1][i / 2 % VW] : 0u;
-        f[w] = __builtin_amdgcn_perm(x1, x0, (i & 1) ? 0x07060302u : 0x05040100u);
-      }
-      return f;
+    for (int n = 0; n < NQ; ++n) {
+      m[n] = KV_NEG_INF;
+      l[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < DL; ++i) o[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    int ve = -30;  // INT4: the outputs are in units of 2^ve (fp16's least scale is 2^-24)
+
+    const uint8_t* kbase = a.c.k.p + h * a.c.k.head;
+    const uint8_t* vbase = a.c.v.p + h * a.c.v.head;
+    // a lane's places in 16 keys (a page's extent is below 2^31 bytes)
+    const uint32_t klane = r * (uint32_t)a.c.k.tok + g * (INT4 ? D / 8 : 16);
+    const uint32_t vlane = 4 * g * (uint32_t)a.c.v.tok + r * (INT4 ? DL / 2 : 2 * DL);
+    const int pmask = (1 << a.c.page_shift) - 1;
+
+    // keys and scales, and values, of the tile at hand; each is loaded again
+    // for the next tile as soon as it was used
+    u32x4 kr[2 * KP][KL];
+    uint32_t vr[8 * KP][VW];
+    u32x2 ksr[2 * KP], vsr[2 * KP];
+    // 16 keys lie in one page; lane i holds the page of the tile's i-th 16
+    auto look_up = [&](int key0) {
+      const int k = min(max(key0 + 16 * (lane & (2 * KP - 1)), kfirst), klast);
+      return table[k >> a.c.page_shift];
     };
-    if constexpr (INT4) {
+    auto fetch_k = [&](int key0, int pages) {
 #pragma unroll
-      for (int s = 0; s < 8; ++s) cur.v[s][0] ^= 0x88888888u;
+      for (int kb = 0; kb < 2 * KP; ++kb) {
+        const int64_t page = __builtin_amdgcn_readlane(pages, kb);
+        const int off = (key0 + 16 * kb) & pmask;
+        const uint8_t* kp = kbase + (page * a.c.k.page + off * a.c.k.tok);
+        if constexpr (!INT4) {
 #pragma unroll
-      for (int i = 0; i < DL; i += 2) {
-        u32x4 f0, f1;
+          for (int kk = 0; kk < KK; ++kk) kr[kb][kk] = kv_load<u32x4>(kp, klane + 64 * kk);
+        } else if constexpr (D == 128) {
+          kr[kb][0] = kv_load<u32x4>(kp, klane);
+        } else {
+          const u32x2 w = kv_load<u32x2>(kp, klane);
+          kr[kb][0] = u32x4{w.x, w.y, 0u, 0u};
+        }
+        if constexpr (INT4)
+          ksr[kb] = kv_load<u32x2>(a.c.k.scale + (page * a.c.k.s_page + h * a.c.k.s_head + off), 8 * g);
+      }
+    };
+    auto fetch_v = [&](int key0, int pages) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          // byte i / 2 of two keys' words, each alone in a half
-          const uint32_t x = __builtin_amdgcn_perm(cur.v[2 * w + 1][0], cur.v[2 * w][0], 0x0c040c00u + 0x00010001u * (i / 2));
-          f0[w] = kv_code_lo(x);
-          f1[w] = kv_code_hi(x);
+      for (int kb = 0; kb < 2 * KP; ++kb) {
+        const int64_t page = __builtin_amdgcn_readlane(pages, kb);
+        const int off = (key0 + 16 * kb) & pmask;
+        const uint8_t* vp = vbase + (page * a.c.v.page + off * a.c.v.tok);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t p = vlane + j * (uint32_t)a.c.v.tok;
+          uint32_t* to = vr[4 * kb + j];
+          if constexpr (!INT4 && D == 128) {
+            const u32x4 w = kv_load<u32x4>(vp, p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i % VW] = w[i];
+          } else if constexpr (!INT4) {
+            const u32x2 w = kv_load<u32x2>(vp, p);
+            to[0] = w.x;
+            to[1 % VW] = w.y;
+          } else if constexpr (D == 128) {
+            to[0] = kv_load<uint32_t>(vp, p);
+          } else {
+            to[0] = kv_load<uint16_t>(vp, p);
+          }
+        }
+        if constexpr (INT4)
+          vsr[kb] = kv_load<u32x2>(a.c.v.scale + (page * a.c.v.s_page + h * a.c.v.s_head + off), 8 * g);
+      }
+    };
+
+    const bool work = kfirst <= klast;
+    const int t1 = klast / TK;
+    // memory answers in order: the next tile's table entries are asked for
+    // before this tile's keys and values, and so are there with them
+    int t = kfirst / TK + wave, entry = 0;
+    if (work && t <= t1) {
+      const int pages = kv_page(a, look_up(t * TK));
+      entry = look_up((t + NW) * TK);
+      fetch_k(t * TK, pages);
+      fetch_v(t * TK, pages);
+    }
+    for (; work && t <= t1; t += NW) {
+      // the last tile is loaded again (from near caches) rather than nothing:
+      // without branches around the loads each wait is for its own data alone
+      const int key0 = TK * t, next0 = t + NW <= t1 ? key0 + TK * NW : key0;
+      // every row sees the whole tile? (wave-uniform)
+      const bool full = key0 >= (a.window > 0 ? max(kfirst, p0 + nq - a.window) : kfirst) &&
+                        key0 + TK - 1 <= (a.causal ? min(klast, p0) : klast);
+      auto key_of = [&](int s) { return key0 + 16 * (s >> 2) + 4 * g + (s & 3); };
+      float ks[8 * KP], vs[8 * KP];
+      if constexpr (INT4) {
+#pragma unroll
+        for (int s = 0; s < 8 * KP; ++s) {
+          const uint32_t w = ksr[s >> 2][(s >> 1) & 1];
+          ks[s] = (float)__builtin_bit_cast(_Float16, (uint16_t)(s & 1 ? w >> 16 : w & 0xffffu));
+        }
+      }
+      // S^T: sc[n][4 kb + e] is key 16 kb + 4 g + e
+      float sc[NQ][8 * KP];
+#pragma unroll
+      for (int kb = 0; kb < 2 * KP; ++kb) {
+        u32x4 kf[KK];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+          if constexpr (INT4) kf[kk] = kv_codes8(kr[kb][0][kk]);
+          else kf[kk] = kr[kb][kk];
         }
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          o[n][i] = kv_mfma16<MT>(f0, pf[n], o[n][i]);
-          o[n][i + 1] = kv_mfma16<MT>(f1, pf[n], o[n][i + 1]);
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk) acc = kv_mfma16<MT>(kf[kk], qf[n][kk], acc);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][4 * kb + e] = acc[e];
         }
       }
-    } else {
-      bool bad = false;
-      if (!full && nq > 1) {
-        // a masked probability of 0 does not hide a value that is not finite
-        u16x2 top = {0, 0};
+      const int pages = kv_page(a, entry);
+      entry = look_up(next0 + TK * NW);
+      fetch_k(next0, pages);
+      if constexpr (INT4) {
+        // the largest value scale of the tile, as a power of two, sets the unit
+        float top = 0.f;
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-#pragma unroll
-          for (int w = 0; w < VW; ++w) top = absmax16(top, cur.v[s][w]);
-        bad = __any(kv_not_finite<T>(top));
-      }
-      if (!bad) {
-#pragma unroll
-        for (int i = 0; i < DL; ++i) {
-          const u32x4 f = value(i, [](int) { return true; });
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) o[n][i] = kv_mfma16<MT>(f, pf[n], o[n][i]);
+        for (int s = 0; s < 8 * KP; ++s) {
+          const uint32_t w = vsr[s >> 2][(s >> 1) & 1];
+          vs[s] = (float)__builtin_bit_cast(_Float16, (uint16_t)(s & 1 ? w >> 16 : w & 0xffffu));
+          if (key_of(s) >= kfirst && key_of(s) <= klast && vs[s] < 65536.f) top = fmaxf(top, vs[s]);
         }
-      } else {
-        // once per token of the chunk, with the keys it does not see cleared
-        for (int tok = 0; tok < nq; ++tok) {
-          const int pos = p0 + tok;
-          auto keep = [&](int s) {
-            const int key = key0 + (s < 4 ? 0 : 16) + 4 * g + (s & 3);
-            return (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
-          };
+        if (__any(top >= __builtin_ldexpf(1.f, ve + 1))) {
 #pragma unroll
-          for (int i = 0; i < DL; ++i) {
-            const u32x4 f = value(i, keep);
+          for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x, 64));
+          const int e = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top) - 1);
+          const float f = __builtin_ldexpf(1.f, ve - e);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int i = 0; i < DL; ++i) o[n][i] *= f;
+          ve = e;
+        }
+        const float unit = __builtin_ldexpf(1.f, -ve);
+#pragma unroll
+        for (int s = 0; s < 8 * KP; ++s) vs[s] *= unit;
+      } else if (key0 < kfirst || key0 + TK - 1 > klast) {
+        // what lies outside [kfirst, klast] may be anything: the values become 0
+#pragma unroll
+        for (int s = 0; s < 8 * KP; ++s) {
+          const bool in = key_of(s) >= kfirst && key_of(s) <= klast;
+#pragma unroll
+          for (int w = 0; w < VW; ++w) vr[s][w] = in ? vr[s][w] : 0u;
+        }
+      }
+      u32x4 pf[NQ][KP];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float top = KV_NEG_INF;
+#pragma unroll
+        for (int s = 0; s < 8 * KP; ++s) {
+          sc[n][s] *= INT4 ? qs[n] * ks[s] : qs[n];
+          if (!full) {
+            const int key = key_of(s);
+            const bool in = key >= kfirst && key <= klast && (!a.causal || key <= qpos[n]) &&
+                            (a.window <= 0 || key > qpos[n] - a.window);
+            sc[n][s] = in ? sc[n][s] : KV_NEG_INF;
+          }
+          top = fmaxf(top, sc[n][s]);
+        }
+        if (__any(top > m[n] + KV_LAG)) {
+          top = fmaxf(top, __shfl_xor(top, 16, 64));
+          top = fmaxf(top, __shfl_xor(top, 32, 64));
+          const float mn = fmaxf(m[n], top);
+          const float al = kv_alpha(m[n], mn);
+          l[n] *= al;
+#pragma unroll
+          for (int i = 0; i < DL; ++i) o[n][i] *= al;
+          m[n] = mn;
+        }
+        const float base = kv_base(m[n]);
+        float p[8 * KP];
+#pragma unroll
+        for (int s = 0; s < 8 * KP; ++s) {
+          p[s] = __builtin_amdgcn_exp2f(sc[n][s] - base);
+          l[n] += p[s];
+          if constexpr (INT4) p[s] = sc[n][s] == KV_NEG_INF ? 0.f : p[s] * vs[s];
+        }
+#pragma unroll
+        for (int w = 0; w < 4 * KP; ++w) pf[n][w / 4][w % 4] = kv_pack<MT>(p[2 * w], p[2 * w + 1]);
+      }
+      // O^T: product i yields dim DL r + i
+      auto value = [&](int kp, int i, auto keep) {  // A operand; keep(s): whether slot s counts
+        u32x4 f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int s = 8 * kp + 2 * w;
+          const uint32_t x0 = keep(s) ? vr[s][i / 2 % VW] : 0u;
+          const uint32_t x1 = keep(s + 1) ? vr[s + 1][i / 2 % VW] : 0u;
+          f[w] = __builtin_amdgcn_perm(x1, x0, (i & 1) ? 0x07060302u : 0x05040100u);
+        }
+        return f;
+      };
+      if constexpr (INT4) {
+#pragma unroll
+        for (int kp = 0; kp < KP; ++kp)
+#pragma unroll
+          for (int i = 0; i < DL; i += 2) {
+            u32x4 f0, f1;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              // byte i / 2 of two keys' words, each alone in a half, offset by 8
+              const int s = 8 * kp + 2 * w;
+              const uint32_t x = __builtin_amdgcn_perm(vr[s + 1][0], vr[s][0], 0x0c040c00u + 0x00010001u * (i / 2)) ^ 0x00880088u;
+              f0[w] = kv_code_lo(x);
+              f1[w] = kv_code_hi(x);
+            }
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-              const f32x4 one = kv_mfma16<MT>(f, pf[n], f32x4{0.f, 0.f, 0.f, 0.f});
+              o[n][i] = kv_mfma16<MT>(f0, pf[n][kp], o[n][i]);
+              o[n][i + 1] = kv_mfma16<MT>(f1, pf[n][kp], o[n][i + 1]);
+            }
+          }
+      } else {
+        bool bad = false;
+        if (!full && nq > 1) {
+          // a masked probability of 0 does not hide a value that is not finite
+          u16x2 top = {0, 0};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[n][i][e] += qpos[n] == pos ? one[e] : 0.f;
+          for (int s = 0; s < 8 * KP; ++s)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) top = absmax16(top, vr[s][w]);
+          bad = __any(kv_not_finite<T>(top));
+        }
+        if (!bad) {
+#pragma unroll
+          for (int kp = 0; kp < KP; ++kp)
+#pragma unroll
+            for (int i = 0; i < DL; ++i) {
+              const u32x4 f = value(kp, i, [](int) { return true; });
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) o[n][i] = kv_mfma16<MT>(f, pf[n][kp], o[n][i]);
+            }
+        } else {
+          // once per token of the chunk, with the keys it does not see cleared
+          for (int tok = 0; tok < nq; ++tok) {
+            const int pos = p0 + tok;
+            auto keep = [&](int s) {
+              return (!a.causal || key_of(s) <= pos) && (a.window <= 0 || key_of(s) > pos - a.window);
+            };
+#pragma unroll
+            for (int kp = 0; kp < KP; ++kp)
+#pragma unroll
+              for (int i = 0; i < DL; ++i) {
+                const u32x4 f = value(kp, i, keep);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                  const f32x4 one = kv_mfma16<MT>(f, pf[n][kp], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[n][i][e] += qpos[n] == pos ? one[e] : 0.f;
+                }
+              }
+          }
+        }
+      }
+      fetch_v(next0, pages);
+    }
+
+    // join the waves, 16 queries at a time, through LDS
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float ls = l[n];
+      ls += __shfl_xor(ls, 16, 64);
+      ls += __shfl_xor(ls, 32, 64);
+      __syncthreads();  // the rows of the last round, or sequence, have been read
+      // lane (q = r, g): dims (4 g + e) DL + i
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < DL; i += 4)
+          *reinterpret_cast<f32x4*>(&so[wave][r][(4 * g + e) * DL + i]) =
+              f32x4{o[n][i][e], o[n][i + 1][e], o[n][i + 2][e], o[n][i + 3][e]};
+      if (g == 0) {
+        sm[wave][r] = m[n];
+        sl[wave][r] = ls;
+      }
+      if (lane == 0) se[wave] = ve;
+      __syncthreads();
+      const int row = 16 * n + (int)threadIdx.x / LR, i0 = threadIdx.x % LR;
+      if ((int)threadIdx.x < 16 * LR && row < rows) {
+        const int q = row & 15, tok = row / a.group, head = h * a.group + row % a.group;
+        float mx = KV_NEG_INF;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[w][q]);
+        float sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float f = __builtin_amdgcn_exp2f(sm[w][q] - kv_base(mx));
+          sum += f * sl[w][q];
+          const float fo = INT4 ? f * __builtin_ldexpf(1.f, se[w]) : f;
+          // a wave that saw nothing for this row adds nothing
+          const bool none = sm[w][q] == KV_NEG_INF && sl[w][q] == 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] += none ? 0.f : fo * so[w][q][8 * i0 + e];
+        }
+        if ((uint32_t)(q0 + tok) < (uint64_t)a.q_tokens) {
+          if (whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= inv;
+            if constexpr (INT4) kv_row_rht<D, 8, true>(x, i0, 1, lane, a.c.signs);
+            stg<u32x4>(a.out + (int64_t)(q0 + tok) * a.o_tok + (int64_t)head * a.o_head + 16 * i0, kv_round8<T>(x));
+            if (a.lse && i0 == 0)
+              a.lse[(int64_t)(q0 + tok) * a.heads + head] =
+                  sum == 0.f ? KV_NEG_INF : (mx + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+          } else {
+            const int64_t pr = ((int64_t)(run + b) * a.c.kv_heads + h) * a.rows + row;
+            stg<f32x4>(a.part_o + pr * D + 8 * i0, f32x4{x[0], x[1], x[2], x[3]});
+            stg<f32x4>(a.part_o + pr * D + 8 * i0 + 4, f32x4{x[4], x[5], x[6], x[7]});
+            if (i0 == 0) {
+              a.part_ml[2 * pr] = mx;
+              a.part_ml[2 * pr + 1] = sum;
             }
           }
         }
       }
     }
-    if (more) cur = nxt;
-  }
-
-  // join the four waves: rows of 16 queries at a time through LDS
-  __shared__ __attribute__((aligned(16))) float so[4][16][PAD];
-  __shared__ float sm[4][16], sl[4][16];
-  __shared__ int se[4];
-  constexpr int LR = D / 8;  // lanes of a row in the join
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    float ls = l[n];
-    ls += __shfl_xor(ls, 16, 64);
-    ls += __shfl_xor(ls, 32, 64);
-    if (n) __syncthreads();
-    // lane (q = r, g): dims (4 g + e) DL + i
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int i = 0; i < DL; i += 4)
-        *reinterpret_cast<f32x4*>(&so[wave][r][(4 * g + e) * DL + i]) =
-            f32x4{o[n][i][e], o[n][i + 1][e], o[n][i + 2][e], o[n][i + 3][e]};
-    if (g == 0) {
-      sm[wave][r] = m[n];
-      sl[wave][r] = ls;
+    if (a.blocks == 0) return;
+    if (from == 0 && h == 0 && threadIdx.x == 0) {
+      a.reach[2 * b] = run;
+      a.reach[2 * b + 1] = (int)(((u + sp.units) * runs - 1) / total);  // the run with its last unit
     }
-    if (lane == 0) se[wave] = ve;
-    __syncthreads();
-    const int row = 16 * n + (int)threadIdx.x / LR, i0 = threadIdx.x % LR;
-    if ((int)threadIdx.x < 16 * LR && row < rows) {
-      const int q = row & 15, tok = row / a.group, head = h * a.group + row % a.group;
-      float mx = KV_NEG_INF;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, sm[w][q]);
-      float sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sm[w][q] - kv_base(mx));
-        sum += f * sl[w][q];
-        const float fo = INT4 ? f * __builtin_ldexpf(1.f, se[w]) : f;
-        // a wave that saw nothing for this row adds nothing
-        const bool none = sm[w][q] == KV_NEG_INF && sl[w][q] == 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += none ? 0.f : fo * so[w][q][8 * i0 + e];
-      }
-      if ((uint32_t)(q0 + tok) < (uint64_t)a.q_tokens) {
-        const int64_t gr = (int64_t)(q0 + tok) * a.heads + head;
-        if (a.splits == 1) {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= inv;
-          if constexpr (INT4) kv_row_rht<D, 8, true>(x, i0, 1, lane, a.c.signs);
-          stg<u32x4>(a.out + (int64_t)(q0 + tok) * a.o_tok + (int64_t)head * a.o_head + 16 * i0, kv_round8<T>(x));
-          if (a.lse && i0 == 0)
-            a.lse[gr] = sum == 0.f ? KV_NEG_INF : (mx + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
-        } else {
-          const int64_t pr = (int64_t)split * a.q_tokens * a.heads + gr;
-          stg<f32x4>(a.part_o + pr * D + 8 * i0, f32x4{x[0], x[1], x[2], x[3]});
-          stg<f32x4>(a.part_o + pr * D + 8 * i0 + 4, f32x4{x[4], x[5], x[6], x[7]});
-          if (i0 == 0) {
-            a.part_ml[2 * pr] = mx;
-            a.part_ml[2 * pr + 1] = sum;
-          }
-        }
-      }
-    }
+    u += take;
+    at = 0;
   }
 }
 
-// Adds the splits of each row in order of the keys.  GR groups of D / 8
-// lanes share a row when there are few rows and many splits.
-template <int D, int T, bool INT4>
-__global__ __launch_bounds__(256) void k_kv_join(const KvAttnArgs a, int gr) {
+// Joins the pieces a row's keys were split into, in order of the keys.
+// Pieces of a row are at piece(i), i in [0, n); `gr` groups of D / 8 lanes
+// share a row when there are few rows and many pieces.
+template <int D, int T, bool INT4, typename P>
+__device__ __forceinline__ void kv_join_row(const KvAttnArgs& a, int64_t row, bool live, int n, int gr, P piece) {
   constexpr int LR = D / 8, PAD = D + 4;
   __shared__ __attribute__((aligned(16))) float so[256 / LR][PAD];
   __shared__ float sm[256 / LR], sl[256 / LR];
   const int grp = threadIdx.x / LR, i0 = threadIdx.x % LR, lane = threadIdx.x & 63;
-  const int per = (256 / LR) / gr;  // rows of the block
-  const int64_t rows = a.q_tokens * a.heads;
-  const int64_t row = (int64_t)blockIdx.x * per + grp / gr;
   const int part = grp % gr;
   float mx = KV_NEG_INF, sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   auto add = [&](float m1, float l1, const float* y) {
     const float mn = fmaxf(mx, m1), f0 = __builtin_amdgcn_exp2f(mx - kv_base(mn)), f1 = __builtin_amdgcn_exp2f(m1 - kv_base(mn));
-    const bool none = m1 == KV_NEG_INF && l1 == 0.f;  // its output was not written
-    sum = f0 * sum + (none ? 0.f : f1 * l1);
+    const bool none = m1 == KV_NEG_INF && l1 == 0.f;  // saw nothing
+    const bool old = mx == KV_NEG_INF && sum == 0.f;
+    sum = (old ? 0.f : f0 * sum) + (none ? 0.f : f1 * l1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = f0 * x[e] + (none ? 0.f : f1 * y[e]);
+    for (int e = 0; e < 8; ++e) x[e] = (old ? 0.f : f0 * x[e]) + (none ? 0.f : f1 * y[e]);
     mx = mn;
   };
-  if (row < rows)
-    for (int s = part; s < a.splits; s += gr) {
-      const int64_t pr = (int64_t)s * rows + row;
+  if (live)
+    for (int s = part; s < n; s += gr) {
+      const int64_t pr = piece(s);
+      const float m1 = a.part_ml[2 * pr], l1 = a.part_ml[2 * pr + 1];
       const f32x4 u = ldg<f32x4>(a.part_o + pr * D + 8 * i0), w = ldg<f32x4>(a.part_o + pr * D + 8 * i0 + 4);
       const float y[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
-      add(a.part_ml[2 * pr], a.part_ml[2 * pr + 1], y);
+      add(m1, l1, y);
     }
   if (gr > 1) {
 #pragma unroll
@@ -479,7 +579,7 @@ __global__ __launch_bounds__(256) void k_kv_join(const KvAttnArgs a, int gr) {
       add(sm[grp + p], sl[grp + p], y);
     }
   }
-  if (row >= rows) return;
+  if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] *= inv;
@@ -489,11 +589,45 @@ __global__ __launch_bounds__(256) void k_kv_join(const KvAttnArgs a, int gr) {
   if (a.lse && i0 == 0) a.lse[row] = sum == 0.f ? KV_NEG_INF : (mx + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
+// of the chunk kernel: pieces by split, one row of the call after another
+template <int D, int T, bool INT4>
+__global__ __launch_bounds__(256) void k_kv_join(const KvAttnArgs a, int gr) {
+  const int64_t rows = a.q_tokens * a.heads;
+  const int64_t row = (int64_t)blockIdx.x * (256 / (D / 8) / gr) + threadIdx.x / (D / 8) / gr;
+  kv_join_row<D, T, INT4>(a, row, row < rows, a.splits, gr, [&](int s) { return (int64_t)s * rows + row; });
+}
+// of the step kernel: a block per sequence, head and `16 or 32 / gr` of its rows
+template <int D, int T, bool INT4>
+__global__ __launch_bounds__(256) void k_kv_step_join(const KvAttnArgs a, int gr, int parts) {
+  const int part = blockIdx.x % parts, h = blockIdx.x / parts % a.c.kv_heads, b = blockIdx.x / parts / a.c.kv_heads;
+  const int q0 = a.q_start[b], rows = min((a.q_start[b + 1] - q0) * a.group, a.rows);
+  if (rows <= 0) return;
+  const int i0 = a.reach[2 * b], i1 = a.reach[2 * b + 1];
+  if (i0 == i1) return;
+  const int row = part * (256 / (D / 8) / gr) + threadIdx.x / (D / 8) / gr;
+  const int tok = q0 + row / a.group;
+  const bool live = row < rows && (uint32_t)tok < (uint64_t)a.q_tokens;
+  kv_join_row<D, T, INT4>(a, (int64_t)tok * a.heads + h * a.group + row % a.group, live, i1 - i0 + 1, gr, [&](int s) {
+    return ((int64_t)(i0 + s + b) * a.c.kv_heads + h) * a.rows + row;
+  });
+}
+
 template <int D, int T, bool INT4>
 static hipError_t step_launch(const KvAttnArgs& a, int nq, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)a.seqs * a.c.kv_heads * a.splits));
-  if (nq == 1) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_kv_step<D, T, INT4, 2>), grid, dim3(256), 0, s, a);
+  const dim3 grid((unsigned)((int64_t)a.c.kv_heads * (a.blocks ? a.blocks : a.seqs)));
+  if (nq == 1 && a.blocks == 0) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 8>), grid, dim3(512), 0, s, a);
+  else if (nq == 1) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 4>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_kv_step<D, T, INT4, 2, 4>), grid, dim3(256), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.blocks == 0) return e;
+  // as many groups a row as keep the machine busy
+  int gr = 1;
+  const int most = 256 / (D / 8);
+  const int64_t rows = a.q_tokens * a.heads;
+  while (gr < most && rows * gr < 8192) gr *= 2;
+  const int per = most / gr, parts = (a.rows + per - 1) / per;
+  hipLaunchKernelGGL((k_kv_step_join<D, T, INT4>), dim3((unsigned)((int64_t)a.seqs * a.c.kv_heads * parts)), dim3(256), 0,
+                     s, a, gr, parts);
   return hipGetLastError();
 }
 template <int D, int T, bool INT4>
@@ -512,6 +646,9 @@ static hipError_t join_launch(const KvAttnArgs& a, hipStream_t s) {
                                   : ((INT4) ? F<128, KV_F16, true>(__VA_ARGS__) : F<128, KV_F16, false>(__VA_ARGS__)))  \
                 : ((T) == KV_BF16 ? ((INT4) ? F<64, KV_BF16, true>(__VA_ARGS__) : F<64, KV_BF16, false>(__VA_ARGS__))   \
                                   : ((INT4) ? F<64, KV_F16, true>(__VA_ARGS__) : F<64, KV_F16, false>(__VA_ARGS__))))
+
+// Keys of a unit of the step kernel (one tile for each wave of a block).
+int kv_step_unit(int dim, bool int4, bool whole) { return (dim == 128 && !int4 ? 32 : 64) * (whole ? 8 : 4); }
 
 hipError_t launch_kv_step(const KvAttnArgs& a, int dim, int dt, bool int4, int nq, hipStream_t s) {
   return KV_PICK(step_launch, dim, dt, int4, a, nq, s);

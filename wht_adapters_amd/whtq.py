@@ -7,6 +7,7 @@ is no CPU fallback: importing this module fails if the library is missing.
 """
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -665,18 +666,8 @@ class KVCache:
                 raise ValueError("scales and signs belong to INT4 caches")
             c.dtype = _DT[self.k.dtype]
         self._c = c
-
-    @property
-    def dim(self):
-        return self._c.dim
-
-    @property
-    def kv_heads(self):
-        return self._c.kv_heads
-
-    @property
-    def page_size(self):
-        return self._c.page_size
+        self.dim, self.kv_heads, self.page_size = c.dim, c.kv_heads, c.page_size
+        self._scale, self._dev = c.dim ** -0.5, self.k.get_device()
 
 
 def kv_cache_alloc(num_pages, page_size, kv_heads, dim, *, int4=False, dtype=torch.bfloat16, signs=None, device="cuda"):
@@ -689,27 +680,48 @@ def kv_cache_alloc(num_pages, page_size, kv_heads, dim, *, int4=False, dtype=tor
     return KVCache(*codes, *scales, signs)
 
 
-def _head_rows(name, t, cache, heads=None, dtype=None):
+_pair = functools.lru_cache(maxsize=1024)(lambda a, b: (_i64 * 2)(a, b))  # strides as the library takes them
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on_device(dev, f, *args):
+    """f(*args, stream) on device `dev`'s current stream."""
+    if torch.cuda.current_device() == dev:
+        return f(*args, _raw_stream(dev))
+    with torch.cuda.device(dev):
+        return f(*args, _raw_stream(dev))
+
+
+def _head_rows(name, t, cache, tokens, heads, dtype):
     """Strides of a [tokens, heads, dim] tensor with contiguous head vectors."""
-    _need_cuda(name, t)
-    if t.dim() != 3 or t.shape[2] != cache.dim or t.stride(2) != 1:
+    if not isinstance(t, torch.Tensor) or t.get_device() != cache._dev:
+        raise ValueError(f"{name} must be a tensor on the cache's device")
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != cache.dim or st[2] != 1:
         raise ValueError(f"{name} must be [tokens, heads, {cache.dim}] with a contiguous last dimension")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"{name} must have {heads} heads")
-    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype or 'bfloat16 or float16'}")
-    if not cache.int4 and t.dtype != cache.k.dtype:
-        raise ValueError(f"{name} must have the cache's dtype")
-    if t.device != cache.k.device:
-        raise ValueError(f"{name} must be on the cache's device")
+    if shape[0] != tokens or shape[1] != heads:
+        raise ValueError(f"{name} must have {tokens} tokens and {heads} heads")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}")
     # the stride of a dimension of one entry is meaningless
-    return (_i64 * 2)(t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    return _pair(st[0] if tokens > 1 else 0, st[1] if heads > 1 else 0)
 
 
-def _ints(name, t, dtype, device, shape=None):
-    _need_cuda(name, t)
-    if t.dtype != dtype or not t.is_contiguous() or t.device != device or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be contiguous {dtype} {list(shape) if shape is not None else ''} on the cache's device")
+def _rows_dtype(name, t, cache):
+    """The type of a call's rows: a 16-bit cache's own, or either with INT4."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [tokens, heads, dim] tensor")
+    dtype = t.dtype
+    if dtype is not cache.k.dtype and not (cache.int4 and dtype in (torch.bfloat16, torch.float16)):
+        raise ValueError(f"{name} must be {'bfloat16 or float16' if cache.int4 else cache.k.dtype}")
+    return dtype
+
+
+def _ints(name, t, dtype, dev, n):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != (n,) or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on the cache's device")
+    return t.data_ptr()
 
 
 def kv_append(cache, k, v, slots, *, q=None, cos=None, sin=None, positions=None, rot_dim=None, interleaved=False,
@@ -719,44 +731,40 @@ def kv_append(cache, k, v, slots, *, q=None, cos=None, sin=None, positions=None,
     outside the cache: not written).  cos, sin: float32 [positions, rot_dim /
     2] tables, or None for no rotation; positions: int32 [tokens].  Returns
     the rotated queries (q_out, q's shape; q_out=q rotates in place)."""
-    ks = _head_rows("k", k, cache, cache.kv_heads)
-    vs = _head_rows("v", v, cache, cache.kv_heads, k.dtype)
-    tokens, dev = k.shape[0], k.device
-    if v.shape[0] != tokens:
-        raise ValueError("k and v must have the same number of tokens")
-    _ints("slots", slots, torch.int64, dev, (tokens,))
+    dtype = _rows_dtype("k", k, cache)
+    tokens, dev = k.shape[0], cache._dev
+    ks = _head_rows("k", k, cache, tokens, cache.kv_heads, dtype)
+    vs = _head_rows("v", v, cache, tokens, cache.kv_heads, dtype)
+    slots_p = _ints("slots", slots, torch.int64, dev, tokens)
     rope = None
     if cos is not None or sin is not None or positions is not None:
         for nm, t in (("cos", cos), ("sin", sin)):
-            _need_cuda(nm, t)
-            if t.dtype != torch.float32 or t.dim() != 2 or t.stride(1) != 1 or t.device != dev:
-                raise ValueError(f"{nm} must be float32 [positions, rot_dim / 2] with a contiguous last dimension")
-        if cos.shape != sin.shape or cos.stride() != sin.stride():
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.dim() != 2 or \
+                    t.stride(1) != 1 or t.get_device() != dev:
+                raise ValueError(f"{nm} must be a float32 [positions, rot_dim / 2] tensor with a contiguous last "
+                                 "dimension on the cache's device")
+        rows, half = cos.shape
+        ld = cos.stride(0)
+        if sin.shape != cos.shape or sin.stride(0) != ld:
             raise ValueError("cos and sin must have one shape and layout")
-        _ints("positions", positions, torch.int32, dev, (tokens,))
-        rot = int(rot_dim) if rot_dim is not None else 2 * cos.shape[1]
-        if rot > 2 * cos.shape[1]:
+        rot = 2 * half if rot_dim is None else int(rot_dim)
+        if rot > 2 * half:
             raise ValueError("cos and sin must hold rot_dim / 2 entries a row")
-        ld = cos.stride(0) if cos.shape[0] > 1 else -(-cos.shape[1] // 4) * 4
-        rope = _Rope(cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), ld, cos.shape[0], rot, int(bool(interleaved)))
-    qs = qos = None
+        rope = _Rope(cos.data_ptr(), sin.data_ptr(), _ints("positions", positions, torch.int32, dev, tokens),
+                     ld if rows > 1 else -(-half // 4) * 4, rows, rot, 1 if interleaved else 0)
+    qs = qos = q_p = qo_p = None
     heads = 0
     if q is not None:
-        qs = _head_rows("q", q, cache, None, k.dtype)
-        heads = q.shape[1]
-        if q.shape[0] != tokens:
-            raise ValueError("q and k must have the same number of tokens")
+        heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        qs = _head_rows("q", q, cache, tokens, heads, dtype)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        qos = _head_rows("q_out", q_out, cache, heads, q.dtype)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out shape mismatch")
+            q_out = q.new_empty(q.shape)
+        qos = _head_rows("q_out", q_out, cache, tokens, heads, dtype)
+        q_p, qo_p = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    with torch.cuda.device(dev):
-        _check("kv_append", _lib.kv_append(
-            cache._c, _ptr(k), ks, _ptr(v), vs, _DT[k.dtype], tokens, _ptr(slots), rope, _ptr(q), qs, heads,
-            _ptr(q_out), qos, _stream(k)))
+    _check("kv_append", _on_device(dev, _lib.kv_append, cache._c, k.data_ptr(), ks, v.data_ptr(), vs, _DT[dtype], tokens,
+                                   slots_p, rope, q_p, qs, heads, qo_p, qos))
     return q_out
 
 
@@ -764,26 +772,27 @@ def kv_gather(cache, slots, *, dtype=None, k_out=None, v_out=None):
     """(k, v) [tokens, kv_heads, dim]: what the cache's slots (int64 [tokens])
     stand for; zeros for a slot outside the cache.  dtype: an INT4 cache's
     output type (bfloat16 by default)."""
-    dev = cache.k.device
-    _ints("slots", slots, torch.int64, dev)
-    tokens = slots.numel()
-    dtype = dtype or (torch.bfloat16 if cache.int4 else cache.k.dtype)
-    outs = []
-    for nm, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is None:
-            t = torch.empty((tokens, cache.kv_heads, cache.dim), dtype=dtype, device=dev)
-        outs.append((t, _head_rows(nm, t, cache, cache.kv_heads, dtype)))
-        if t.shape[0] != tokens:
-            raise ValueError(f"{nm} must have one row per slot")
-    (k, ks), (v, vs) = outs
-    with torch.cuda.device(dev):
-        _check("kv_gather", _lib.kv_gather(cache._c, tokens, _ptr(slots), _ptr(k), ks, _ptr(v), vs, _DT[dtype],
-                                           _stream(cache.k)))
-    return k, v
+    dev = cache._dev
+    tokens = slots.numel() if isinstance(slots, torch.Tensor) else 0
+    slots_p = _ints("slots", slots, torch.int64, dev, tokens)
+    if dtype is None:
+        dtype = torch.bfloat16 if cache.int4 else cache.k.dtype
+    elif dtype is not cache.k.dtype and not (cache.int4 and dtype in (torch.bfloat16, torch.float16)):
+        raise ValueError(f"dtype must be {'bfloat16 or float16' if cache.int4 else cache.k.dtype}")
+    heads, shape = cache.kv_heads, (tokens, cache.kv_heads, cache.dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=cache.k.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=cache.k.device)
+    ks = _head_rows("k_out", k_out, cache, tokens, heads, dtype)
+    vs = _head_rows("v_out", v_out, cache, tokens, heads, dtype)
+    _check("kv_gather", _on_device(dev, _lib.kv_gather, cache._c, tokens, slots_p, k_out.data_ptr(), ks, v_out.data_ptr(),
+                                   vs, _DT[dtype]))
+    return k_out, v_out
 
 
 def kv_attention_workspace_bytes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len):
-    with torch.cuda.device(cache.k.device):
+    with torch.cuda.device(cache._dev):
         return int(_lib.kv_attention_workspace_bytes(cache._c, q_tokens, heads, seqs, max_q_len, max_kv_len))
 
 
@@ -796,41 +805,46 @@ def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_le
     default; window: 0, or how many of the latest keys a query sees.  lse: a
     float32 [tokens, heads] tensor to fill.  workspace: a uint8 tensor of
     kv_attention_workspace_bytes, allocated here if not given."""
-    qs = _head_rows("q", q, cache)
-    dev = q.device
-    tokens, heads = q.shape[:2]
+    dtype = _rows_dtype("q", q, cache)
+    dev = cache._dev
+    tokens, heads, _ = q.shape
+    qs = _head_rows("q", q, cache, tokens, heads, dtype)
+    if not isinstance(kv_len, torch.Tensor):
+        raise ValueError("kv_len must be a tensor")
     seqs = kv_len.numel()
-    _ints("q_start", q_start, torch.int32, dev, (seqs + 1,))
-    _ints("kv_len", kv_len, torch.int32, dev, (seqs,))
-    _need_cuda("block_table", block_table)
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != seqs or \
-            block_table.device != dev or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [seqs, width] with a contiguous last dimension")
-    width = block_table.shape[1]
+    start_p = _ints("q_start", q_start, torch.int32, dev, seqs + 1)
+    kv_p = _ints("kv_len", kv_len, torch.int32, dev, seqs)
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32 or block_table.dim() != 2 or \
+            block_table.get_device() != dev:
+        raise ValueError("block_table must be an int32 [seqs, width] tensor on the cache's device")
+    (rows, width), (ts, t1) = block_table.shape, block_table.stride()
+    if rows != seqs or (width > 1 and t1 != 1):
+        raise ValueError("block_table must have a row per sequence and a contiguous last dimension")
     if heads % cache.kv_heads:
         raise ValueError("q's heads must be a multiple of the cache's")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    if out.shape != q.shape:
-        raise ValueError("out shape mismatch")
-    outs = _head_rows("out", out, cache, heads, q.dtype)
+        out = q.new_empty(q.shape)
+    outs = _head_rows("out", out, cache, tokens, heads, dtype)
+    lse_p = None
     if lse is not None:
-        _need_cuda("lse", lse)
-        if lse.dtype != torch.float32 or lse.shape != (tokens, heads) or not lse.is_contiguous() or lse.device != dev:
-            raise ValueError("lse must be contiguous float32 [tokens, heads]")
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = _lib.kv_attention_workspace_bytes(cache._c, tokens, heads, seqs, max_q_len, max_kv_len)
-            if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif not workspace.is_contiguous() or workspace.device != dev:
-            raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check("kv_attention", _lib.kv_attention(
-            cache._c, _ptr(q), qs, _DT[q.dtype], tokens, heads, seqs, _ptr(q_start), _ptr(kv_len),
-            _ptr(block_table), block_table.stride(0) if seqs > 1 else width, width, max_q_len, max_kv_len,
-            cache.dim ** -0.5 if scale is None else scale, int(bool(causal)), window, _ptr(out), outs, _ptr(lse),
-            _ptr(workspace), wbytes, _stream(q)))
+        if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32 or lse.shape != (tokens, heads) or \
+                not lse.is_contiguous() or lse.get_device() != dev:
+            raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor on the cache's device")
+        lse_p = lse.data_ptr()
+    if workspace is None:
+        need = _on_device(dev, lambda *a: _lib.kv_attention_workspace_bytes(*a[:-1]), cache._c, tokens, heads, seqs,
+                          max_q_len, max_kv_len)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    ws_p = wbytes = 0
+    if workspace is not None:
+        ws_p, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check("kv_attention", _on_device(
+        dev, _lib.kv_attention, cache._c, q.data_ptr(), qs, _DT[dtype], tokens, heads, seqs, start_p, kv_p,
+        block_table.data_ptr(), ts if seqs > 1 else width, width, max_q_len, max_kv_len,
+        cache._scale if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), outs, lse_p, ws_p, wbytes))
     return out
 
 
