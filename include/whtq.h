@@ -601,7 +601,8 @@ whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t*
  *   and the value's to the fp32 probability.  Deterministic.
  */
 int64_t kv_attention_workspace_bytes(const whtq_kv_cache* cache, int64_t q_tokens, int64_t heads, int64_t seqs,
-                                     int64_t max_q_len, int64_t max_kv_len); /* -1: invalid sizes or no device */
+                                     int64_t max_q_len, int64_t max_kv_len,
+                                     int64_t window); /* -1: invalid sizes or no device */
 
 whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_t* q_stride, whtq_dtype dtype,
                          int64_t q_tokens, int64_t heads, int64_t seqs, const int32_t* q_start,

@@ -143,9 +143,9 @@ def test_attention_rules():
 
 def test_workspace_of_invalid_sizes():
     f = L.kv_attention_workspace_bytes
-    assert f(cache(dim=96), 1, 4, 1, 1, 1) == -1
-    assert f(cache(), 1, 3, 1, 1, 1) == -1
-    assert f(cache(), -1, 4, 1, 1, 1) == -1
+    assert f(cache(dim=96), 1, 4, 1, 1, 1, 0) == -1
+    assert f(cache(), 1, 3, 1, 1, 1, 0) == -1
+    assert f(cache(), -1, 4, 1, 1, 1, 0) == -1
 
 
 def test_null_cache():

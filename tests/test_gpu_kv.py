@@ -304,6 +304,37 @@ def test_attention(W, case, dtype, int4):
     check(o3, lse, qs, kvs, scale, dtype, int4, sg, causal, window, hk)
 
 
+LONG = [
+    (4, 2, 128, 32, [(260, 1400), (1, 900), (70, 70)], True, 0),
+    (3, 1, 64, 64, [(130, 1100)], False, 0),
+    (4, 1, 128, 16, [(200, 1000)], True, 300),
+    (2, 1, 64, 16, [(300, 700), (33, 640)], True, 0),
+]
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_attention_long(W, case, dtype, int4):
+    """Many whole tiles between the masked ones, with and without a split of the keys."""
+    heads, hk, d, page, seqs, causal, window = LONG[case]
+    rng = np.random.default_rng(200 + case)
+    kls = [b for _, b in seqs]
+    cache, sg = new_cache(W, rng, sum(-(-n // page) for n in kls) + 3, page, hk, d, dtype, int4)
+    table, _, kvs = fill(W, rng, cache, sg, kls, hk, d, dtype, int4, page, 1.5)
+    n = sum(a for a, _ in seqs)
+    q = randn(rng, n, heads, d, dtype=dtype, scale=1.5)
+    qst = np.cumsum([0] + [a for a, _ in seqs]).astype(np.int32)
+    args = (torch.from_numpy(qst).to(DEV), torch.tensor(kls, dtype=torch.int32, device=DEV),
+            torch.from_numpy(table).to(DEV))
+    qs = [host64(q)[a:b] for a, b in zip(qst[:-1], qst[1:])]
+    lse = torch.full((n, heads), 9.0, device=DEV)
+    for most in (64, max(kls)):
+        out = W.kv_attention(cache, q.to(DEV), *args, lse=lse, max_q_len=max(a for a, _ in seqs), max_kv_len=most,
+                             scale=-0.1, causal=causal, window=window)
+        check(out, lse, [-x for x in qs], kvs, 0.1, dtype, int4, sg, causal, window, hk)
+
+
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
 @pytest.mark.parametrize("dtype", DTS)
 @pytest.mark.parametrize("d,n,kv,window", [(64, 5, 50, 0), (128, 5, 50, 0), (128, 90, 150, 0), (64, 90, 150, 40), (128, 6, 200, 9)])

@@ -73,8 +73,7 @@ hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_
                             hipStream_t s);
 hipError_t launch_kv_step(const KvAttnArgs& a, int dim, int dt, bool int4, int nq, hipStream_t s);
 hipError_t launch_kv_join(const KvAttnArgs& a, int dim, int dt, bool int4, hipStream_t s);
-hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int64_t tiles, hipStream_t s);
-int kv_chunk_rows();
+hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int waves, unsigned grid, hipStream_t s);
 int kv_step_unit(int dim, bool int4, bool whole);
 
 static thread_local int g_last_hip = 0;
@@ -782,12 +781,12 @@ bool kv_rows_aligned(const void* p, const int64_t* st) { return aligned16(p) && 
 // how an attention call runs: which kernel, and over how many blocks the keys of a row are split
 struct KvPlan {
   bool step;
-  int nq, blocks, rows, splits, split_keys;
-  int64_t tiles, grid, parts, bytes;  // parts: partial rows kept
+  int nq, blocks, rows, waves, splits;
+  int64_t grid, parts, bytes;  // parts: partial rows kept
 };
 
 KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t seqs, int64_t max_q, int64_t max_kv,
-               int cus) {
+               int64_t window, int cus) {
   KvPlan p{};
   const int64_t group = heads / c->kv_heads, kvh = c->kv_heads;
   const bool int4 = c->format == WHTQ_KV_INT4;
@@ -809,16 +808,24 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
     p.grid = p.blocks * kvh;
     p.parts = (p.blocks + seqs) * kvh * p.rows;
   } else {
-    const int64_t rows = kv_chunk_rows();
-    p.tiles = q_tokens * group / rows + seqs;
-    // blocks without a split, how many are wanted, and the fewest keys worth a block
-    const int64_t blocks = (q_tokens * group + rows - 1) / rows * kvh, want = 2 * cus, least = 512;
-    int64_t splits = std::max<int64_t>(1, std::min((want + blocks - 1) / blocks, max_kv / least));
-    const int64_t keys = std::max<int64_t>(64, ((max_kv + splits - 1) / splits + 63) / 64 * 64);
-    splits = std::max<int64_t>(1, (max_kv + keys - 1) / keys);
+    // INT4 tiles are unpacked once a block: blocks of 8 waves halve that work
+    // where there are rows for them.  16-bit tiles cost a copy, and two blocks
+    // of 4 waves a CU, out of step, run a little faster.
+    p.waves = int4 && max_q * group > 128 ? 8 : 4;
+    const int64_t rows = 32 * p.waves;
+    const int64_t slots = (p.waves == 8 ? 1 : c->dim == 64 ? 3 : 2) * (int64_t)cus;  // blocks at work at a time
+    const int64_t blocks = (q_tokens * group + rows - 1) / rows * kvh;
+    const int64_t keys = window > 0 ? std::min(max_kv, window + rows / group + 64) : max_kv;
+    // split the keys of a block's rows where that shortens the longest chain
+    // of tiles a slot works off; the joining kernel costs about 4 tiles' time
+    const int64_t tiles = (keys + 63) / 64;
+    int64_t best = (blocks + slots - 1) / slots * tiles, splits = 1;
+    for (int64_t n = 2; n <= 64 && 4 * n <= tiles; ++n) {
+      const int64_t cost = (blocks * n + slots - 1) / slots * ((tiles + n - 1) / n) + 4;
+      if (cost < best) best = cost, splits = n;
+    }
     p.splits = (int)splits;
-    p.split_keys = (int)keys;
-    p.grid = p.tiles * kvh * splits;
+    p.grid = (q_tokens * group / rows + seqs) * kvh * splits;
     if (splits > 1) p.parts = splits * q_tokens * heads;
   }
   if (p.parts) p.bytes = (p.parts * (c->dim + 2) * 4 + (p.step ? seqs * 8 : 0) + 15) / 16 * 16;
@@ -900,13 +907,13 @@ whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t*
 }
 
 int64_t kv_attention_workspace_bytes(const whtq_kv_cache* cache, int64_t q_tokens, int64_t heads, int64_t seqs,
-                                     int64_t max_q_len, int64_t max_kv_len) {
+                                     int64_t max_q_len, int64_t max_kv_len, int64_t window) {
   KvCache c;
   if (kv_check(cache, &c) != WHTQ_OK) return -1;
   if (kv_attn_sizes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len) != WHTQ_OK) return -1;
-  if (need_device() != WHTQ_OK) return -1;
+  if (window < 0 || need_device() != WHTQ_OK) return -1;
   if (q_tokens == 0 || seqs == 0) return 0;
-  return kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, kv_cus()).bytes;
+  return kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window, kv_cus()).bytes;
 }
 
 whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_t* q_stride, whtq_dtype dtype,
@@ -933,7 +940,7 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   if (!any) return WHTQ_OK;
   st = need_device();
   if (st != WHTQ_OK) return st;
-  const KvPlan p = kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, kv_cus());
+  const KvPlan p = kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window, kv_cus());
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return WHTQ_EINVAL;
   if (p.grid > INT32_MAX) return WHTQ_EUNSUPPORTED;
   a.q = (const uint8_t*)q;
@@ -955,7 +962,6 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   a.causal = causal;
   a.window = (int)std::min(window, kMost);
   a.splits = p.splits;
-  a.split_keys = p.split_keys;
   a.scale = scale * 1.4426950408889634f;
   a.part_o = (float*)workspace;
   a.part_ml = a.part_o + p.parts * cache->dim;
@@ -965,7 +971,7 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   const bool int4 = cache->format == WHTQ_KV_INT4;
   const hipStream_t s = (hipStream_t)stream;
   const int dim = (int)cache->dim;
-  hipError_t e = p.step ? launch_kv_step(a, dim, dtype, int4, p.nq, s) : launch_kv_chunk(a, dim, dtype, int4, p.tiles, s);
+  hipError_t e = p.step ? launch_kv_step(a, dim, dtype, int4, p.nq, s) : launch_kv_chunk(a, dim, dtype, int4, p.waves, (unsigned)p.grid, s);
   if (e == hipSuccess && !p.step && p.splits > 1) e = launch_kv_join(a, dim, dtype, int4, s);
   return hip_status(e);
 }

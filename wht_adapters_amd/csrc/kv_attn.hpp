@@ -27,7 +27,7 @@ struct KvAttnArgs {
   int* reach;  // step kernel: first and last run of each sequence
   int64_t q_tokens;
   int table_width, heads, group, seqs, causal, window;
-  int splits, split_keys;  // chunk kernel
+  int splits;              // chunk kernel
   int blocks, rows;        // step kernel: runs a head (0: a block per sequence), rows of a sequence and head
   float scale;  // times log2(e)
 };

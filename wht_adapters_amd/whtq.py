@@ -78,7 +78,7 @@ _lib.qwha_grad_values_workspace_bytes.argtypes = [_i64, _i64, _i64]
 _lib.qwha_grad_values_workspace_bytes.restype = _i64
 _lib.qwha_forward_plan_bytes.argtypes = [_i64, _i64, _i64, _i64]
 _lib.qwha_forward_plan_bytes.restype = _i64
-_lib.kv_attention_workspace_bytes.argtypes = [_cache_p, _i64, _i64, _i64, _i64, _i64]
+_lib.kv_attention_workspace_bytes.argtypes = [_cache_p, _i64, _i64, _i64, _i64, _i64, _i64]
 _lib.kv_attention_workspace_bytes.restype = _i64
 _lib.whtq_status_string.argtypes = [_int]
 _lib.whtq_status_string.restype = ctypes.c_char_p
@@ -791,9 +791,9 @@ def kv_gather(cache, slots, *, dtype=None, k_out=None, v_out=None):
     return k_out, v_out
 
 
-def kv_attention_workspace_bytes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len):
+def kv_attention_workspace_bytes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window=0):
     with torch.cuda.device(cache._dev):
-        return int(_lib.kv_attention_workspace_bytes(cache._c, q_tokens, heads, seqs, max_q_len, max_kv_len))
+        return int(_lib.kv_attention_workspace_bytes(cache._c, q_tokens, heads, seqs, max_q_len, max_kv_len, window))
 
 
 def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_len, scale=None, causal=True, window=0,
@@ -833,7 +833,7 @@ def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_le
         lse_p = lse.data_ptr()
     if workspace is None:
         need = _on_device(dev, lambda *a: _lib.kv_attention_workspace_bytes(*a[:-1]), cache._c, tokens, heads, seqs,
-                          max_q_len, max_kv_len)
+                          max_q_len, max_kv_len, window)
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.get_device() != dev:
