@@ -795,10 +795,10 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
   if (p.step) {
     p.nq = max_q * group <= 16 ? 1 : 2;
     p.rows = (int)std::max<int64_t>(1, max_q * group);
-    // A block takes a whole sequence when there is little to share: at most 4
-    // units each, or enough sequences to fill the machine with equal keys
+    // A block takes a whole sequence when there is little to share: at most 2
+    // units each (the joining kernel costs more than a third would)
     const int64_t unit = kv_step_unit((int)c->dim, int4, true), shared = kv_step_unit((int)c->dim, int4, false);
-    if (p.nq == 1 && max_kv <= 4 * unit) {
+    if (p.nq == 1 && max_kv <= 2 * unit) {
       p.grid = seqs * kvh;
       return p;
     }
@@ -817,11 +817,11 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
     const int64_t blocks = (q_tokens * group + rows - 1) / rows * kvh;
     const int64_t keys = window > 0 ? std::min(max_kv, window + rows / group + 64) : max_kv;
     // split the keys of a block's rows where that shortens the longest chain
-    // of tiles a slot works off; the joining kernel costs about 4 tiles' time
+    // of tiles a slot works off; the joining kernel costs about 8 tiles' time
     const int64_t tiles = (keys + 63) / 64;
     int64_t best = (blocks + slots - 1) / slots * tiles, splits = 1;
     for (int64_t n = 2; n <= 64 && 4 * n <= tiles; ++n) {
-      const int64_t cost = (blocks * n + slots - 1) / slots * ((tiles + n - 1) / n) + 4;
+      const int64_t cost = (blocks * n + slots - 1) / slots * ((tiles + n - 1) / n) + 8;
       if (cost < best) best = cost, splits = n;
     }
     p.splits = (int)splits;

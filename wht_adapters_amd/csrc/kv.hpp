@@ -25,13 +25,17 @@ struct KvCache {
   int page_shift, kv_heads;
 };
 
-// Load at a wave-uniform base plus a lane's 32-bit offset: one register pair
-// for the base serves every lane.
+// Load at a wave-uniform base plus a lane's 32-bit offset plus a constant, as
+// a buffer load: the base is in scalar registers and no lane computes a 64-bit
+// address.  (The buffer has no size of its own: offsets are checked by their
+// callers, like any pointer's.)
 template <typename V>
-__device__ __forceinline__ V kv_load(const void* base, uint32_t off) {
-  const __attribute__((address_space(1))) uint8_t* p =
-      reinterpret_cast<const __attribute__((address_space(1))) uint8_t*>(reinterpret_cast<uintptr_t>(base));
-  return *reinterpret_cast<const __attribute__((address_space(1))) V*>(p + off);
+__device__ __forceinline__ V kv_load(const void* base, uint32_t off, int imm = 0) {
+  const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00027000);
+  if constexpr (sizeof(V) == 16) return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(r, off + imm, 0, 0));
+  else if constexpr (sizeof(V) == 8) return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b64(r, off + imm, 0, 0));
+  else if constexpr (sizeof(V) == 4) return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b32(r, off + imm, 0, 0));
+  else return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b16(r, off + imm, 0, 0));
 }
 
 template <int T>

@@ -28,7 +28,7 @@ struct KvAttnArgs {
   int64_t q_tokens;
   int table_width, heads, group, seqs, causal, window;
   int splits;              // chunk kernel
-  int blocks, rows;        // step kernel: runs a head (0: a block per sequence), rows of a sequence and head
+  int blocks, rows;        // step kernel: runs a head (0: a block per sequence), rows of a sequence and head (max_q_len * group)
   float scale;  // times log2(e)
 };
 
@@ -37,11 +37,6 @@ constexpr float KV_NEG_INF = -__builtin_huge_valf();
 // exp2 of a score against the running maximum (a maximum of -inf means that
 // nothing was seen yet: the score is -inf too and gives 0).
 __device__ __forceinline__ float kv_base(float m) { return m == KV_NEG_INF ? 0.f : m; }
-// What sums and outputs are multiplied by when the maximum goes from m to mn.
-__device__ __forceinline__ float kv_alpha(float m, float mn) {
-  return m == KV_NEG_INF ? 0.f : __builtin_amdgcn_exp2f(m - mn);
-}
-
 // Scores are compared with a maximum that may lag behind by up to 2^KV_LAG:
 // the accumulators are rescaled only when a score exceeds it by more.  The
 // probabilities then reach 2^KV_LAG at most (far inside fp16's range) and the

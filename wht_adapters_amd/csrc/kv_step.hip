@@ -57,12 +57,11 @@ __device__ __forceinline__ void kv_row_rht(float* x, int sub, int step, int lane
 struct KvSpan {  // a sequence's share of the work
   int q0, nq, chunk, p0, first, last, units;
 };
-template <int NQ>
 __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, int q0, int q1, int kv_len, int unit) {
   KvSpan s;
   s.q0 = q0;
   s.chunk = q1 - q0;
-  s.nq = min(s.chunk, (16 * NQ) / a.group);
+  s.nq = min(s.chunk, a.rows / a.group);  // at most max_q_len
   const int kv = min(kv_len, (int)min<int64_t>((int64_t)a.table_width << a.c.page_shift, INT32_MAX));
   s.p0 = kv - s.chunk;  // position of the first query
   s.first = a.window > 0 ? max(0, s.p0 - a.window + 1) : 0;  // the keys any of its queries sees
@@ -72,6 +71,21 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, int q0, int q1, i
   return s;
 }
 
+// n runs of a number of units, the first `more` of them one longer.
+struct KvRuns {
+  int64_t each, more;
+  __device__ __forceinline__ KvRuns() {}
+  __device__ __forceinline__ KvRuns(int64_t total, int n) {
+    each = total >> 31 ? total / n : (uint32_t)total / (uint32_t)n;  // (a 64-bit division takes a microsecond)
+    more = total - each * n;
+  }
+  __device__ __forceinline__ int64_t start(int run) const { return run * each + min<int64_t>(run, more); }
+  __device__ __forceinline__ int of(int64_t unit) const {  // the run a unit is in
+    const int64_t big = more * (each + 1), x = unit < big ? unit : unit - big, d = unit < big ? each + 1 : each;
+    return (int)((unit < big ? 0 : more) + (x >> 31 || d >> 31 ? x / d : (int64_t)((uint32_t)x / (uint32_t)d)));
+  }
+};
+
 // Values every lane has alike, kept as such (scalar registers and branches).
 __device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int64_t scalar(int64_t x) {
@@ -79,8 +93,10 @@ __device__ __forceinline__ int64_t scalar(int64_t x) {
 }
 
 // T: type of q and out; the operands of the products are T (dense) or fp16.
-template <int D, int T, bool INT4, int NQ, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
+// MANY: chunks of more than one token (values that are not finite need care
+// there: a kernel of its own keeps its registers out of the single token's).
+template <int D, int T, bool INT4, int NQ, int NW, bool MANY>
+__global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAttnArgs a) {
   constexpr int MT = INT4 ? KV_F16 : T;
   constexpr int KK = D / 32;   // products per 16 keys of S^T
   constexpr int DL = D / 16;   // dims a lane holds of a value row
@@ -92,57 +108,61 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
   constexpr int LR = D / 8;  // lanes of a row in the join
   __shared__ __attribute__((aligned(16))) float so[NW][16][PAD];
   __shared__ float sm[NW][16], sl[NW][16];
-  __shared__ int se[NW];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
 
   // the block's run of units [u, u1), starting `at` units into sequence b
-  int h, b, run = 0, runs = 1;
+  int b, run = 0, runs = 1;
+  const int h = blockIdx.x % a.c.kv_heads;
   int64_t u = 0, u1 = 1, at = 0, total = 1;
+  KvRuns share{};
+  KvSpan sp;
   if (a.blocks == 0) {
-    h = blockIdx.x % a.c.kv_heads;
     b = blockIdx.x / a.c.kv_heads;
+    sp = kv_span(a, scalar(a.q_start[b]), scalar(a.q_start[b + 1]), scalar(a.kv_len[b]), UNIT);
   } else {
-    h = blockIdx.x % a.c.kv_heads;
     run = blockIdx.x / a.c.kv_heads;
-    auto units_of = [&](int s) {
-      return s < a.seqs ? kv_span<NQ>(a, a.q_start[s], a.q_start[s + 1], a.kv_len[s], UNIT).units : 0;
-    };
-    total = 0;
-    for (int s = 0; s < a.seqs; s += 64) {
-      int n = units_of(s + lane);
-#pragma unroll
-      for (int m = 1; m < 64; m *= 2) n += __shfl_xor(n, m, 64);
-      total += n;
-    }
-    total = scalar(total);
-    runs = (int)min<int64_t>(a.blocks, total);
-    if (run >= runs) return;
-    u = run * total / runs;
-    u1 = (run + 1) * total / runs;
-    int64_t before = 0;
-    for (b = 0;; b += 64) {  // ends: u < total
-      const int n = units_of(b + lane);
-      int sum = n;
+    // lane i looks at sequence s + i
+    KvSpan mine;
+    auto look = [&](int s) {
+      const int i = s + lane;
+      mine = i < a.seqs ? kv_span(a, a.q_start[i], a.q_start[i + 1], a.kv_len[i], UNIT) : KvSpan{};
+      int sum = mine.units;  // of the lanes up to this one
 #pragma unroll
       for (int m = 1; m < 64; m *= 2) {
         const int o = __shfl_up(sum, m, 64);
         if (lane >= m) sum += o;
       }
+      return sum;
+    };
+    int sum = look(0);
+    total = scalar(__builtin_amdgcn_readlane(sum, 63));
+    for (int s = 64; s < a.seqs; s += 64) total += scalar(__builtin_amdgcn_readlane(look(s), 63));
+    runs = (int)min<int64_t>(a.blocks, total);
+    if (run >= runs) return;
+    share = KvRuns(total, runs);
+    u = share.start(run);
+    u1 = share.start(run + 1);
+    int64_t before = 0;
+    for (b = 0;; b += 64) {  // ends: u < total
+      if (a.seqs > 64) sum = look(b);
       const uint64_t past = __ballot(before + sum > u);
       if (past) {
         const int i = __builtin_ctzll(past);
-        at = u - before - (__shfl(sum, i, 64) - __shfl(n, i, 64));
+        auto of = [&](int x) { return __builtin_amdgcn_readlane(x, i); };
+        sp = {of(mine.q0), of(mine.nq), of(mine.chunk), of(mine.p0), of(mine.first), of(mine.last), of(mine.units)};
+        at = u - before - (of(sum) - sp.units);
         b += i;
         break;
       }
-      before += scalar(__shfl(sum, 63, 64));
+      before += __builtin_amdgcn_readlane(sum, 63);
     }
+    b = scalar(b);
     at = scalar(at);
   }
 
-  for (; u < u1; ++b) {
-    const KvSpan sp = kv_span<NQ>(a, scalar(a.q_start[b]), scalar(a.q_start[b + 1]), scalar(a.kv_len[b]), UNIT);
+  for (bool one = true; u < u1; ++b, one = false) {
+    if (!one) sp = kv_span(a, scalar(a.q_start[b]), scalar(a.q_start[b + 1]), scalar(a.kv_len[b]), UNIT);
     if (sp.units == 0) {
       if (a.blocks == 0) return;
       continue;
@@ -156,56 +176,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
     const int kfirst = max(sp.first, base_key + from * UNIT);
     const int klast = min(sp.last, base_key + (from + take) * UNIT - 1);
     const int32_t* table = a.table + b * a.table_stride;
-
-    // the lane's queries (column r of each block of 16) and what they see
-    int qpos[NQ];
-    u32x4 qf[NQ][KK];
-    float qs[NQ];  // scale of the scores
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int row = 16 * n + r, tok = row / a.group;
-      const bool live = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
-      qpos[n] = p0 + tok;
-      qs[n] = a.scale;
-      const uint8_t* qp = a.q + (int64_t)(q0 + tok) * a.q_tok + (int64_t)(h * a.group + row % a.group) * a.q_head;
-      if constexpr (!INT4) {
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-          qf[n][kk] = live ? ldg<u32x4>(qp + 64 * kk + 16 * g) : u32x4{0u, 0u, 0u, 0u};
-      } else {
-        float x[D / 4];
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-          kv_widen8<T>(live ? ldg<u32x4>(qp + g * (D / 2) + 16 * kk) : u32x4{0u, 0u, 0u, 0u}, x + 8 * kk);
-        kv_row_rht<D, D / 4, false>(x, g, 16, lane, a.c.signs);
-        float top = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(x[e]));
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        // an exact power of two brings the row's largest value to [1, 2)
-        const int ex = top > 0.f && top < __builtin_huge_valf() ? max(-126, min(126, __builtin_amdgcn_frexp_expf(top) - 1)) : 0;
-        const float down = __builtin_ldexpf(1.f, -ex);
-        qs[n] = a.scale * __builtin_ldexpf(1.f, ex);
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            qf[n][kk][w] = pack_f16(x[8 * kk + kv_perm(2 * w)] * down, x[8 * kk + kv_perm(2 * w + 1)] * down);
-        }
-      }
-    }
-
-    float m[NQ], l[NQ];
-    f32x4 o[NQ][DL];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      m[n] = KV_NEG_INF;
-      l[n] = 0.f;
-#pragma unroll
-      for (int i = 0; i < DL; ++i) o[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    int ve = -30;  // INT4: the outputs are in units of 2^ve (fp16's least scale is 2^-24)
 
     const uint8_t* kbase = a.c.k.p + h * a.c.k.head;
     const uint8_t* vbase = a.c.v.p + h * a.c.v.head;
@@ -232,7 +202,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
         const uint8_t* kp = kbase + (page * a.c.k.page + off * a.c.k.tok);
         if constexpr (!INT4) {
 #pragma unroll
-          for (int kk = 0; kk < KK; ++kk) kr[kb][kk] = kv_load<u32x4>(kp, klane + 64 * kk);
+          for (int kk = 0; kk < KK; ++kk) kr[kb][kk] = ldg_global<u32x4>(kp + (klane + 64 * kk));
         } else if constexpr (D == 128) {
           kr[kb][0] = kv_load<u32x4>(kp, klane);
         } else {
@@ -254,7 +224,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
           const uint32_t p = vlane + j * (uint32_t)a.c.v.tok;
           uint32_t* to = vr[4 * kb + j];
           if constexpr (!INT4 && D == 128) {
-            const u32x4 w = kv_load<u32x4>(vp, p);
+            const u32x4 w = ldg_global<u32x4>(vp + p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) to[i % VW] = w[i];
           } else if constexpr (!INT4) {
@@ -283,6 +253,103 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
       fetch_k(t * TK, pages);
       fetch_v(t * TK, pages);
     }
+    // the lane's queries (column r of each block of 16) and what they see
+    int qpos[NQ];
+    u32x4 qf[NQ][KK];
+    float qs[NQ];  // the scores are kept in units of 1 / qs, qs > 0; a negative scale turns q around
+    const uint32_t turn = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int row = 16 * n + r, tok = row / a.group;
+      const bool live = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
+      qpos[n] = p0 + tok;
+      qs[n] = fmaxf(fabsf(a.scale), 1e-30f);  // 0 would turn a masked -inf into NaN; the results are the same
+      const uint8_t* qp = a.q + (int64_t)(q0 + tok) * a.q_tok + (int64_t)(h * a.group + row % a.group) * a.q_head;
+      if constexpr (!INT4) {
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+          qf[n][kk] = live ? ldg<u32x4>(qp + 64 * kk + 16 * g) ^ turn : u32x4{0u, 0u, 0u, 0u};
+      } else {
+        float x[D / 4];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+          kv_widen8<T>(live ? ldg<u32x4>(qp + g * (D / 2) + 16 * kk) : u32x4{0u, 0u, 0u, 0u}, x + 8 * kk);
+        kv_row_rht<D, D / 4, false>(x, g, 16, lane, a.c.signs);
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(x[e]));
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        // an exact power of two brings the row's largest value to [1, 2)
+        const int ex = top > 0.f && top < __builtin_huge_valf() ? max(-126, min(126, __builtin_amdgcn_frexp_expf(top) - 1)) : 0;
+        const float down = __builtin_ldexpf(1.f, -ex);
+        qs[n] *= __builtin_ldexpf(1.f, ex);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            qf[n][kk][w] = pack_f16(x[8 * kk + kv_perm(2 * w)] * down, x[8 * kk + kv_perm(2 * w + 1)] * down) ^ turn;
+        }
+      }
+    }
+
+    float m[NQ], l[NQ], lag[NQ];
+    f32x4 o[NQ][DL];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      m[n] = KV_NEG_INF;
+      lag[n] = KV_LAG / qs[n];
+      l[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < DL; ++i) o[n][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    // INT4: sums and outputs are in units of 2^ve, 2^ve the power of two below the
+    // largest value scale seen: the products stay inside fp16 (whose least is 2^-24)
+    int ve = -30;
+
+    // Values that are not finite, taken out of a tile that some query does not
+    // see whole: the outputs of the queries that see them become what they are
+    // (the sum's result whatever the probability), 16 keys at a time through
+    // the wave's rows of `so`, and the tile holds 0 in their place.
+    constexpr uint32_t EXPO = T == KV_BF16 ? 0x7f80u : 0x7c00u;
+    auto take_out = [&](int key0) {
+#pragma unroll
+      for (int kb = 0; kb < 2 * KP; ++kb) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            uint32_t& x = vr[4 * kb + j][w];
+            const uint32_t lo = x & 0xffffu, hi = x >> 16;
+            const bool bl = (lo & EXPO) == EXPO, bh = (hi & EXPO) == EXPO;
+            float f[8];
+            kv_widen8<T>(u32x4{x, 0u, 0u, 0u}, f);
+            so[wave][4 * g + j][DL * r + 2 * w] = bl ? f[0] : 0.f;
+            so[wave][4 * g + j][DL * r + 2 * w + 1] = bh ? f[1] : 0.f;
+            x = (bl ? 0u : lo) | (bh ? 0u : hi << 16);
+          }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) {
+          const int key = key0 + 16 * kb + k;
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            const bool in = key >= kfirst && key <= klast && (!a.causal || key <= qpos[n]) &&
+                            (a.window <= 0 || key > qpos[n] - a.window);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int i = 0; i < DL; i += 4) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(&so[wave][k][(4 * g + e) * DL + i]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[n][i + x][e] += in ? v[x] : 0.f;
+                asm volatile("" ::: "memory");
+              }
+          }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      }
+    };
     for (; work && t <= t1; t += NW) {
       // the last tile is loaded again (from near caches) rather than nothing:
       // without branches around the loads each wait is for its own data alone
@@ -321,30 +388,40 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
       const int pages = kv_page(a, entry);
       entry = look_up(next0 + TK * NW);
       fetch_k(next0, pages);
+      const bool inner = key0 >= kfirst && key0 + TK - 1 <= klast;  // wave-uniform
       if constexpr (INT4) {
-        // the largest value scale of the tile, as a power of two, sets the unit
-        float top = 0.f;
+        // the scales' largest, as bits: they are not negative
+        u16x2 big = {0, 0};
+#pragma unroll
+        for (int kb = 0; kb < 2 * KP; ++kb) {
+          const uint32_t w0 = vsr[kb].x, w1 = vsr[kb].y;
+          big = absmax16(absmax16(big, w0), w1);
+        }
 #pragma unroll
         for (int s = 0; s < 8 * KP; ++s) {
           const uint32_t w = vsr[s >> 2][(s >> 1) & 1];
           vs[s] = (float)__builtin_bit_cast(_Float16, (uint16_t)(s & 1 ? w >> 16 : w & 0xffffu));
-          if (key_of(s) >= kfirst && key_of(s) <= klast && vs[s] < 65536.f) top = fmaxf(top, vs[s]);
         }
-        if (__any(top >= __builtin_ldexpf(1.f, ve + 1))) {
+        float top = (float)__builtin_bit_cast(_Float16, (uint16_t)absmax16(big));
+        if (__any(!(top < __builtin_ldexpf(1.f, ve + 1)))) {
+          // of the keys that count, without infinities and NaN
+          top = 0.f;
+#pragma unroll
+          for (int s = 0; s < 8 * KP; ++s)
+            if (key_of(s) >= kfirst && key_of(s) <= klast && vs[s] < 65536.f) top = fmaxf(top, vs[s]);
 #pragma unroll
           for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x, 64));
-          const int e = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top) - 1);
+          const int e = max(ve, __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top) - 1));
           const float f = __builtin_ldexpf(1.f, ve - e);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n)
+          for (int n = 0; n < NQ; ++n) {
+            l[n] *= f;
 #pragma unroll
             for (int i = 0; i < DL; ++i) o[n][i] *= f;
+          }
           ve = e;
         }
-        const float unit = __builtin_ldexpf(1.f, -ve);
-#pragma unroll
-        for (int s = 0; s < 8 * KP; ++s) vs[s] *= unit;
-      } else if (key0 < kfirst || key0 + TK - 1 > klast) {
+      } else if (!inner) {
         // what lies outside [kfirst, klast] may be anything: the values become 0
 #pragma unroll
         for (int s = 0; s < 8 * KP; ++s) {
@@ -359,7 +436,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
         float top = KV_NEG_INF;
 #pragma unroll
         for (int s = 0; s < 8 * KP; ++s) {
-          sc[n][s] *= INT4 ? qs[n] * ks[s] : qs[n];
+          if constexpr (INT4) sc[n][s] *= ks[s];
           if (!full) {
             const int key = key_of(s);
             const bool in = key >= kfirst && key <= klast && (!a.causal || key <= qpos[n]) &&
@@ -368,39 +445,32 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
           }
           top = fmaxf(top, sc[n][s]);
         }
-        if (__any(top > m[n] + KV_LAG)) {
+        if (__any(top > m[n] + lag[n])) {
           top = fmaxf(top, __shfl_xor(top, 16, 64));
           top = fmaxf(top, __shfl_xor(top, 32, 64));
           const float mn = fmaxf(m[n], top);
-          const float al = kv_alpha(m[n], mn);
+          const float al = m[n] == KV_NEG_INF ? 1.f : __builtin_amdgcn_exp2f((m[n] - mn) * qs[n]);  // 1: l and o are 0
           l[n] *= al;
 #pragma unroll
           for (int i = 0; i < DL; ++i) o[n][i] *= al;
           m[n] = mn;
         }
-        const float base = kv_base(m[n]);
+        const float base = -kv_base(m[n]) * qs[n] - (INT4 ? (float)ve : 0.f);
         float p[8 * KP];
 #pragma unroll
         for (int s = 0; s < 8 * KP; ++s) {
-          p[s] = __builtin_amdgcn_exp2f(sc[n][s] - base);
+          p[s] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][s], qs[n], base));
           l[n] += p[s];
-          if constexpr (INT4) p[s] = sc[n][s] == KV_NEG_INF ? 0.f : p[s] * vs[s];
+          if constexpr (INT4) p[s] *= vs[s];
+        }
+        if (INT4 && !full) {  // whatever the scale of a masked place is
+#pragma unroll
+          for (int s = 0; s < 8 * KP; ++s) p[s] = sc[n][s] == KV_NEG_INF ? 0.f : p[s];
         }
 #pragma unroll
         for (int w = 0; w < 4 * KP; ++w) pf[n][w / 4][w % 4] = kv_pack<MT>(p[2 * w], p[2 * w + 1]);
       }
       // O^T: product i yields dim DL r + i
-      auto value = [&](int kp, int i, auto keep) {  // A operand; keep(s): whether slot s counts
-        u32x4 f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int s = 8 * kp + 2 * w;
-          const uint32_t x0 = keep(s) ? vr[s][i / 2 % VW] : 0u;
-          const uint32_t x1 = keep(s + 1) ? vr[s + 1][i / 2 % VW] : 0u;
-          f[w] = __builtin_amdgcn_perm(x1, x0, (i & 1) ? 0x07060302u : 0x05040100u);
-        }
-        return f;
-      };
       if constexpr (INT4) {
 #pragma unroll
         for (int kp = 0; kp < KP; ++kp)
@@ -422,46 +492,28 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
             }
           }
       } else {
-        bool bad = false;
-        if (!full && nq > 1) {
+        if (MANY && !full && nq > 1) {
           // a masked probability of 0 does not hide a value that is not finite
           u16x2 top = {0, 0};
 #pragma unroll
           for (int s = 0; s < 8 * KP; ++s)
 #pragma unroll
             for (int w = 0; w < VW; ++w) top = absmax16(top, vr[s][w]);
-          bad = __any(kv_not_finite<T>(top));
+          if (__any(kv_not_finite<T>(top))) take_out(key0);
         }
-        if (!bad) {
 #pragma unroll
-          for (int kp = 0; kp < KP; ++kp)
+        for (int kp = 0; kp < KP; ++kp)
 #pragma unroll
-            for (int i = 0; i < DL; ++i) {
-              const u32x4 f = value(kp, i, [](int) { return true; });
+          for (int i = 0; i < DL; ++i) {
+            u32x4 f;
 #pragma unroll
-              for (int n = 0; n < NQ; ++n) o[n][i] = kv_mfma16<MT>(f, pf[n][kp], o[n][i]);
+            for (int w = 0; w < 4; ++w) {
+              const int s = 8 * kp + 2 * w;
+              f[w] = __builtin_amdgcn_perm(vr[s + 1][i / 2 % VW], vr[s][i / 2 % VW], (i & 1) ? 0x07060302u : 0x05040100u);
             }
-        } else {
-          // once per token of the chunk, with the keys it does not see cleared
-          for (int tok = 0; tok < nq; ++tok) {
-            const int pos = p0 + tok;
-            auto keep = [&](int s) {
-              return (!a.causal || key_of(s) <= pos) && (a.window <= 0 || key_of(s) > pos - a.window);
-            };
 #pragma unroll
-            for (int kp = 0; kp < KP; ++kp)
-#pragma unroll
-              for (int i = 0; i < DL; ++i) {
-                const u32x4 f = value(kp, i, keep);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                  const f32x4 one = kv_mfma16<MT>(f, pf[n][kp], f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) o[n][i][e] += qpos[n] == pos ? one[e] : 0.f;
-                }
-              }
+            for (int n = 0; n < NQ; ++n) o[n][i] = kv_mfma16<MT>(f, pf[n][kp], o[n][i]);
           }
-        }
       }
       fetch_v(next0, pages);
     }
@@ -481,10 +533,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
           *reinterpret_cast<f32x4*>(&so[wave][r][(4 * g + e) * DL + i]) =
               f32x4{o[n][i][e], o[n][i + 1][e], o[n][i + 2][e], o[n][i + 3][e]};
       if (g == 0) {
-        sm[wave][r] = m[n];
+        sm[wave][r] = m[n] == KV_NEG_INF ? m[n] : m[n] * qs[n] + (INT4 ? (float)ve : 0.f);
         sl[wave][r] = ls;
       }
-      if (lane == 0) se[wave] = ve;
       __syncthreads();
       const int row = 16 * n + (int)threadIdx.x / LR, i0 = threadIdx.x % LR;
       if ((int)threadIdx.x < 16 * LR && row < rows) {
@@ -497,11 +548,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
         for (int w = 0; w < NW; ++w) {
           const float f = __builtin_amdgcn_exp2f(sm[w][q] - kv_base(mx));
           sum += f * sl[w][q];
-          const float fo = INT4 ? f * __builtin_ldexpf(1.f, se[w]) : f;
           // a wave that saw nothing for this row adds nothing
           const bool none = sm[w][q] == KV_NEG_INF && sl[w][q] == 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] += none ? 0.f : fo * so[w][q][8 * i0 + e];
+          for (int e = 0; e < 8; ++e) x[e] += none ? 0.f : f * so[w][q][8 * i0 + e];
         }
         if ((uint32_t)(q0 + tok) < (uint64_t)a.q_tokens) {
           if (whole) {
@@ -528,7 +578,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_step(const KvAttnArgs a) {
     if (a.blocks == 0) return;
     if (from == 0 && h == 0 && threadIdx.x == 0) {
       a.reach[2 * b] = run;
-      a.reach[2 * b + 1] = (int)(((u + sp.units) * runs - 1) / total);  // the run with its last unit
+      a.reach[2 * b + 1] = share.of(u + sp.units - 1);  // the run with its last unit
     }
     u += take;
     at = 0;
@@ -600,10 +650,9 @@ __global__ __launch_bounds__(256) void k_kv_join(const KvAttnArgs a, int gr) {
 template <int D, int T, bool INT4>
 __global__ __launch_bounds__(256) void k_kv_step_join(const KvAttnArgs a, int gr, int parts) {
   const int part = blockIdx.x % parts, h = blockIdx.x / parts % a.c.kv_heads, b = blockIdx.x / parts / a.c.kv_heads;
-  const int q0 = a.q_start[b], rows = min((a.q_start[b + 1] - q0) * a.group, a.rows);
-  if (rows <= 0) return;
-  const int i0 = a.reach[2 * b], i1 = a.reach[2 * b + 1];
-  if (i0 == i1) return;
+  const int q0 = a.q_start[b], q1 = a.q_start[b + 1], i0 = a.reach[2 * b], i1 = a.reach[2 * b + 1];
+  const int rows = min((q1 - q0) * a.group, a.rows);
+  if (rows <= 0 || i0 == i1) return;  // (a sequence without queries has no reach)
   const int row = part * (256 / (D / 8) / gr) + threadIdx.x / (D / 8) / gr;
   const int tok = q0 + row / a.group;
   const bool live = row < rows && (uint32_t)tok < (uint64_t)a.q_tokens;
@@ -615,9 +664,12 @@ __global__ __launch_bounds__(256) void k_kv_step_join(const KvAttnArgs a, int gr
 template <int D, int T, bool INT4>
 static hipError_t step_launch(const KvAttnArgs& a, int nq, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.c.kv_heads * (a.blocks ? a.blocks : a.seqs)));
-  if (nq == 1 && a.blocks == 0) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 8>), grid, dim3(512), 0, s, a);
-  else if (nq == 1) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 4>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_kv_step<D, T, INT4, 2, 4>), grid, dim3(256), 0, s, a);
+  const bool many = !INT4 && a.rows > a.group;
+  if (nq == 2) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 2, 4, true>), grid, dim3(256), 0, s, a);
+  else if (a.blocks == 0 && many) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 8, true>), grid, dim3(512), 0, s, a);
+  else if (a.blocks == 0) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 8, false>), grid, dim3(512), 0, s, a);
+  else if (many) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 4, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 4, false>), grid, dim3(256), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.blocks == 0) return e;
   // as many groups a row as keep the machine busy
