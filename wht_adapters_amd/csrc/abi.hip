@@ -836,6 +836,7 @@ whtq_status kv_attn_sizes(const whtq_kv_cache* c, int64_t q_tokens, int64_t head
                           int64_t max_kv) {
   if (q_tokens < 0 || seqs < 0 || heads < 1 || max_q < 0 || max_kv < 0 || heads % c->kv_heads) return WHTQ_EINVAL;
   if (q_tokens > kMost || seqs > kMost || heads > 65535 || max_q > kMost || max_kv > kMost) return WHTQ_EUNSUPPORTED;
+  if ((q_tokens + seqs) * (heads / c->kv_heads) > kMost) return WHTQ_EUNSUPPORTED;  // rows of a head: 32-bit
   return WHTQ_OK;
 }
 

@@ -85,15 +85,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   for (int step = 1 << (31 - __builtin_clz(a.seqs)); step; step >>= 1)
     if (b + step < a.seqs && (int64_t)a.q_start[b + step] * a.group / ROWS + b + step <= slot) b += step;
   const int q0 = a.q_start[b], chunk = a.q_start[b + 1] - q0;
-  const int64_t row0 = (slot - ((int64_t)q0 * a.group / ROWS + b)) * ROWS;
-  const int64_t rows = (int64_t)chunk * a.group;
+  // (rows of a head are below 2^30, so that these are 32-bit)
+  const int row0 = (int)(slot - ((int64_t)q0 * a.group / ROWS + b)) * ROWS;
+  const int rows = chunk * a.group;
   if (row0 < 0 || row0 >= rows) return;
   const int kv = min(a.kv_len[b], (int)min<int64_t>((int64_t)a.table_width << a.c.page_shift, INT32_MAX));
   const int p0 = kv - chunk;
   const int32_t* table = a.table + b * a.table_stride;
 
   // first and last position among rows [r0, r0 + n) that exist
-  const int tok0 = (int)(row0 / a.group), tok1 = (int)((min<int64_t>(row0 + ROWS, rows) - 1) / a.group);
+  const int tok0 = row0 / a.group, tok1 = (min(row0 + ROWS, rows) - 1) / a.group;
   const int first = a.window > 0 ? max(0, p0 + tok0 - a.window + 1) : 0;
   const int last = a.causal ? min(kv - 1, p0 + tok1) : kv - 1;
   // the split's share of the block's tiles
@@ -103,8 +104,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   // The lane's query.  Its scores are kept in units of 1 / qs, qs > 0 (0 would
   // turn a masked -inf into NaN; 1e-30 gives the same results): a negative
   // scale turns q around.
-  const int64_t row = row0 + 32 * wave + qc;
-  const int tok = (int)(row / a.group), head = h * a.group + (int)(row % a.group);
+  const int row = row0 + 32 * wave + qc;
+  const int tok = row / a.group, head = h * a.group + row % a.group;
   const bool live = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
   const int pos = p0 + tok;
   float qs = fmaxf(fabsf(a.scale), 1e-30f);

@@ -589,7 +589,7 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
 // Pieces of a row are at piece(i), i in [0, n); `gr` groups of D / 8 lanes
 // share a row when there are few rows and many pieces.
 template <int D, int T, bool INT4, typename P>
-__device__ __forceinline__ void kv_join_row(const KvAttnArgs& a, int64_t row, bool live, int n, int gr, P piece) {
+__device__ __forceinline__ void kv_join_row(const KvAttnArgs& a, int64_t tok, int head, bool live, int n, int gr, P piece) {
   constexpr int LR = D / 8, PAD = D + 4;
   __shared__ __attribute__((aligned(16))) float so[256 / LR][PAD];
   __shared__ float sm[256 / LR], sl[256 / LR];
@@ -622,7 +622,7 @@ __device__ __forceinline__ void kv_join_row(const KvAttnArgs& a, int64_t row, bo
     }
     __syncthreads();
     if (part) return;
-    for (int p = 1; p < gr; ++p) {
+    for (int p = 1; p < min(gr, n); ++p) {
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = so[grp + p][8 * i0 + e];
@@ -634,9 +634,8 @@ __device__ __forceinline__ void kv_join_row(const KvAttnArgs& a, int64_t row, bo
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] *= inv;
   if constexpr (INT4) kv_row_rht<D, 8, true>(x, i0, 1, lane, a.c.signs);
-  const int64_t tok = row / a.heads, head = row % a.heads;
   stg<u32x4>(a.out + tok * a.o_tok + head * a.o_head + 16 * i0, kv_round8<T>(x));
-  if (a.lse && i0 == 0) a.lse[row] = sum == 0.f ? KV_NEG_INF : (mx + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+  if (a.lse && i0 == 0) a.lse[tok * a.heads + head] = sum == 0.f ? KV_NEG_INF : (mx + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }
 
 // of the chunk kernel: pieces by split, one row of the call after another
@@ -644,7 +643,10 @@ template <int D, int T, bool INT4>
 __global__ __launch_bounds__(256) void k_kv_join(const KvAttnArgs a, int gr) {
   const int64_t rows = a.q_tokens * a.heads;
   const int64_t row = (int64_t)blockIdx.x * (256 / (D / 8) / gr) + threadIdx.x / (D / 8) / gr;
-  kv_join_row<D, T, INT4>(a, row, row < rows, a.splits, gr, [&](int s) { return (int64_t)s * rows + row; });
+  // (a 64-bit division takes a microsecond)
+  const int64_t tok = rows >> 31 ? row / a.heads : (uint32_t)row / (uint32_t)a.heads;
+  kv_join_row<D, T, INT4>(a, tok, (int)(row - tok * a.heads), row < rows, a.splits, gr,
+                          [&](int s) { return (int64_t)s * rows + row; });
 }
 // of the step kernel: a block per sequence, head and `16 or 32 / gr` of its rows
 template <int D, int T, bool INT4>
@@ -656,7 +658,7 @@ __global__ __launch_bounds__(256) void k_kv_step_join(const KvAttnArgs a, int gr
   const int row = part * (256 / (D / 8) / gr) + threadIdx.x / (D / 8) / gr;
   const int tok = q0 + row / a.group;
   const bool live = row < rows && (uint32_t)tok < (uint64_t)a.q_tokens;
-  kv_join_row<D, T, INT4>(a, (int64_t)tok * a.heads + h * a.group + row % a.group, live, i1 - i0 + 1, gr, [&](int s) {
+  kv_join_row<D, T, INT4>(a, tok, h * a.group + row % a.group, live, i1 - i0 + 1, gr, [&](int s) {
     return ((int64_t)(i0 + s + b) * a.c.kv_heads + h) * a.rows + row;
   });
 }
@@ -676,7 +678,7 @@ static hipError_t step_launch(const KvAttnArgs& a, int nq, hipStream_t s) {
   int gr = 1;
   const int most = 256 / (D / 8);
   const int64_t rows = a.q_tokens * a.heads;
-  while (gr < most && rows * gr < 8192) gr *= 2;
+  while (gr < most && gr < a.blocks && rows * gr < 8192) gr *= 2;
   const int per = most / gr, parts = (a.rows + per - 1) / per;
   hipLaunchKernelGGL((k_kv_step_join<D, T, INT4>), dim3((unsigned)((int64_t)a.seqs * a.c.kv_heads * parts)), dim3(256), 0,
                      s, a, gr, parts);
