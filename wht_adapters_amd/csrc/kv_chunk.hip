@@ -175,26 +175,36 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
     return min(max(key0 + (n * NW + wave) * CR, kfirst & ~(CR - 1)), klast & ~(CR - 1));
   };
   const uint32_t klane = lr * ktok + kswz, vlane = lr * vtok + vswz;
-  // dense: lane n finds the place of copy n (`page` there), the others read it
-  auto copy = [&](auto is_v, auto buf, int key0, int page) KV_INLINE {
-    constexpr bool V = decltype(is_v)::value;
-    const KvSide& c = V ? a.c.v : a.c.k;
-    uint8_t* to = (V ? svb(buf) : skb(buf)) + wave * CR * ROWB;
-    const bool inner = key0 >= kfirst && key0 + KV_TILE - 1 <= klast;
-    const uint64_t at = (uint64_t)(V ? vbase : kbase) + (uint64_t)((int64_t)page * c.page) +
-                        (uint32_t)(copy_key(lane % COPIES, key0) & pmask) * (uint64_t)(V ? vtok : ktok);
+  // dense: lane n finds the places of copy n of K and of V (`page` there), the
+  // others read them
+  auto copy = [&](auto buf, int key0, int page) KV_INLINE {
+    uint64_t from[2][COPIES];
 #pragma unroll
-    for (int n = 0; n < COPIES; ++n) {
-      uint32_t lane_off = V ? vlane : klane;
-      if (!inner) {
+    for (int v = 0; v < 2; ++v) {
+      const uint64_t at = (uint64_t)(v ? vbase : kbase) + (uint64_t)((int64_t)page * (v ? a.c.v.page : a.c.k.page)) +
+                          (uint32_t)(copy_key(lane % COPIES, key0) & pmask) * (uint64_t)(v ? vtok : ktok);
+#pragma unroll
+      for (int n = 0; n < COPIES; ++n)
+        from[v][n] = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(at >> 32), n) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((int)at, n);
+    }
+    auto go = [&](int v, int n, uint32_t off) KV_INLINE {
+      const __attribute__((address_space(1))) uint8_t* g = reinterpret_cast<const __attribute__((address_space(1))) uint8_t*>(from[v][n]);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(g + off),
+                                       (__attribute__((address_space(3))) void*)((v ? svb(buf) : skb(buf)) + (n * NW + wave) * CR * ROWB),
+                                       16, 0, 0);
+    };
+    if (key0 >= kfirst && key0 + KV_TILE - 1 <= klast) {
+#pragma unroll
+      for (int i = 0; i < 2 * COPIES; ++i) go(i / COPIES, i % COPIES, i / COPIES ? vlane : klane);
+    } else {
+#pragma unroll
+      for (int n = 0; n < COPIES; ++n) {
         const int k0 = copy_key(n, key0);
-        lane_off = min(max(lr, kfirst - k0), klast - k0) * (V ? vtok : ktok) + (V ? vswz : kswz);
+        const uint32_t r = min(max(lr, kfirst - k0), klast - k0);
+        go(0, n, r * ktok + kswz);
+        go(1, n, r * vtok + vswz);
       }
-      const uint64_t p = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(at >> 32), n) << 32 |
-                         (uint32_t)__builtin_amdgcn_readlane((int)at, n);
-      const __attribute__((address_space(1))) uint8_t* g = reinterpret_cast<const __attribute__((address_space(1))) uint8_t*>(p);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(g + lane_off),
-                                       (__attribute__((address_space(3))) void*)(to + n * NW * CR * ROWB), 16, 0, 0);
     }
   };
   // INT4: unit u of a tile is 16 bytes (32 codes) of one row of K or V
@@ -230,41 +240,49 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
       asm volatile("" : "+v"(p.at[n]));
     }
   };
-  auto fetch = [&](auto is_v, auto buf, int key0, const Pages& p) KV_INLINE {
-    constexpr bool V = decltype(is_v)::value;
+  auto fetch = [&](auto buf, int key0, const Pages& p) KV_INLINE {
     if constexpr (!INT4) {
-      copy(is_v, buf, key0, p.at[0]);
+      copy(buf, key0, p.at[0]);
     } else {
-      const KvSide& c = V ? a.c.v : a.c.k;
-      const uint8_t* base = V ? vbase : kbase;
 #pragma unroll
-      for (int n = 0; n < UT; ++n)
-        if (has_unit(n))
-          code[V][n] = ldg_global<u32x4>(base + (int64_t)p.at[n] * c.page +
-                                         ((uint32_t)(inside(key0 + unit_row(n)) & pmask) * (V ? vtok : ktok) +
-                                          16 * (threadIdx.x % UR)));
-      if (has_scale)
-        scl[V] = c.scale[p.at[UT] * c.s_page + h * c.s_head + (inside(key0 + (int)threadIdx.x) & pmask)];
+      for (int v = 0; v < 2; ++v) {
+        const KvSide& c = v ? a.c.v : a.c.k;
+#pragma unroll
+        for (int n = 0; n < UT; ++n)
+          if (has_unit(n))
+            code[v][n] = ldg_global<u32x4>((v ? vbase : kbase) + (int64_t)p.at[n] * c.page +
+                                           ((uint32_t)(inside(key0 + unit_row(n)) & pmask) * (v ? vtok : ktok) +
+                                            16 * (threadIdx.x % UR)));
+        if (has_scale)
+          scl[v] = c.scale[p.at[UT] * c.s_page + h * c.s_head + (inside(key0 + (int)threadIdx.x) & pmask)];
+      }
     }
   };
-  auto spread = [&](auto is_v, auto buf) KV_INLINE {  // INT4: the fetched codes to LDS
-    constexpr bool V = decltype(is_v)::value;
+  auto spread = [&](auto buf) KV_INLINE {  // INT4: the fetched codes and scales to LDS
     if constexpr (INT4) {
 #pragma unroll
-      for (int n = 0; n < UT; ++n)
-        if (has_unit(n)) {
-          const int tr = unit_row(n), c = threadIdx.x % UR;
-          uint8_t* rowp = (V ? svb(buf) : skb(buf)) + tr * ROWB;
+      for (int v = 0; v < 2; ++v) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4*>(rowp + 16 * (V ? kv_v_at<D>(tr, 4 * c + j) : kv_k_at<D>(tr, 4 * c + j))) = kv_codes8(code[V][n][j]);
-        }
-      if (has_scale) (V ? svs : sks)[buf][threadIdx.x] = (float)__builtin_bit_cast(_Float16, scl[V]);
+        for (int n = 0; n < UT; ++n)
+          if (has_unit(n)) {
+            const int tr = unit_row(n), c = threadIdx.x % UR;
+            uint8_t* rowp = (v ? svb(buf) : skb(buf)) + tr * ROWB;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<u32x4*>(rowp + 16 * (v ? kv_v_at<D>(tr, 4 * c + j) : kv_k_at<D>(tr, 4 * c + j))) =
+                  kv_codes8(code[v][n][j]);
+          }
+        if (has_scale) (v ? svs : sks)[buf][threadIdx.x] = (float)__builtin_bit_cast(_Float16, scl[v]);
+      }
     }
   };
 
-  auto sees = [&](int key) KV_INLINE {
-    return key >= kfirst && key <= klast && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
-  };
+  // the keys [low, low + span] that the lane's row sees here
+  int low = a.window > 0 ? max(kfirst, pos - a.window + 1) : kfirst;
+  const int high = a.causal ? min(klast, pos) : klast;
+  const uint32_t span = high < low ? 0u : (uint32_t)(high - low);
+  if (high < low) low = INT32_MAX;  // none
+  auto sees = [&](int key) KV_INLINE { return (uint32_t)(key - low) <= span; };
   // A probability of 0 does not hide a value that is not finite, so in a
   // tile that some row does not see whole such values are taken out: the
   // outputs of the rows that see them become what they are (the sum's result
@@ -443,13 +461,24 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
 
   const bool work = kfirst <= klast;
   const int t0 = kfirst / KV_TILE, t1 = klast / KV_TILE;
-  // tiles [f0, f1) that every row of the block sees whole
-  const int bfull0 = a.window > 0 ? max(kfirst, p0 + tok1 - a.window + 1) : kfirst;
-  const int bfull1 = a.causal ? min(klast, p0 + tok0) : klast;
-  const int f0 = (bfull0 + KV_TILE - 1) / KV_TILE, f1 = (bfull1 + 1) / KV_TILE;  // (bfull1 may be negative: none)
-  auto masked = [&](int t) KV_INLINE { return t < f0 || t >= f1; };
-  constexpr std::false_type K{}, B0{};
-  constexpr std::true_type V{}, B1{};
+  // Among tokens [i0, i1]: tiles [f0, f1) that every one sees whole, and tiles
+  // [n0, n1] that one of them sees any of.
+  struct Range {
+    int f0, f1, n0, n1;
+  };
+  auto range = [&](int i0, int i1) KV_INLINE {
+    const int w0 = a.window > 0 ? max(kfirst, p0 + i1 - a.window + 1) : kfirst, w1 = a.causal ? min(klast, p0 + i0) : klast;
+    const int s0 = a.window > 0 ? max(kfirst, p0 + i0 - a.window + 1) : kfirst, s1 = a.causal ? min(klast, p0 + i1) : klast;
+    // (w1 and s1 may be negative: none)
+    return Range{(w0 + KV_TILE - 1) / KV_TILE, (w1 + 1) / KV_TILE, s0 / KV_TILE, s1 < s0 ? -1 : s1 / KV_TILE};
+  };
+  const Range br = range(tok0, tok1);
+  const int wrow = row0 + 32 * wave;
+  Range wr = range(wrow / a.group, (min(wrow + 32, rows) - 1) / a.group);
+  if (wrow >= rows) wr.n1 = -1;
+  auto masked = [&](const Range& r, int t) KV_INLINE { return t < r.f0 || t >= r.f1; };
+  constexpr std::false_type B0{};
+  constexpr std::true_type B1{};
   f32x16 s[KB];
   u32x4 pf[2 * KB];
   // Tiles go to the two buffers in turn; the next one is asked for before
@@ -459,8 +488,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
     Pages now = later;
     check(now);
     look_up(later, (t + 1) * KV_TILE);
-    fetch(K, buf, t * KV_TILE, now);
-    fetch(V, buf, t * KV_TILE, now);
+    fetch(buf, t * KV_TILE, now);
   };
   auto visit = [&](int t, auto buf, auto other) KV_INLINE {
     // this tile has landed, and every wave is done with the other buffer
@@ -468,21 +496,19 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if (t < t1) ask(t + 1, other);
-    if (masked(t) && __syncthreads_or(wild(buf))) take_out(buf, t * KV_TILE);
-    scores(s, buf);
-    settle(s, buf, t * KV_TILE, masked(t));
-    probs(s, pf, buf);
-    outputs(pf, buf);
-    if (t < t1) {
-      spread(K, other);
-      spread(V, other);
+    if (masked(br, t) && __syncthreads_or(wild(buf))) take_out(buf, t * KV_TILE);
+    if (t >= wr.n0 && t <= wr.n1) {
+      scores(s, buf);
+      settle(s, buf, t * KV_TILE, masked(wr, t));
+      probs(s, pf, buf);
+      outputs(pf, buf);
     }
+    if (t < t1) spread(other);
   };
   if (work) {
     look_up(later, t0 * KV_TILE);
     ask(t0, B0);
-    spread(K, B0);
-    spread(V, B0);
+    spread(B0);
     for (int t = t0; t <= t1; t += 2) {
       visit(t, B0, B1);
       if (t < t1) visit(t + 1, B1, B0);
@@ -490,7 +516,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   }
 
   // lane (qc, hf): o[d][4 j + e] is position 32 d + 8 j + 4 hf + e of its row
-{
+  {
     l += __shfl_xor(l, 32, 64);
     const bool one = a.splits == 1;
     const float inv = one ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -558,12 +584,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
 
 template <int D, int T, bool INT4>
 static hipError_t chunk_launch(const KvAttnArgs& a, int waves, unsigned grid, hipStream_t s) {
-  if (waves == 8) hipLaunchKernelGGL((k_kv_chunk<D, T, INT4, 8>), dim3(grid), dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((k_kv_chunk<D, T, INT4, 4>), dim3(grid), dim3(256), 0, s, a);
+  if constexpr (INT4)
+    if (waves == 8) {
+      hipLaunchKernelGGL((k_kv_chunk<D, T, INT4, 8>), dim3(grid), dim3(512), 0, s, a);
+      return hipGetLastError();
+    }
+  hipLaunchKernelGGL((k_kv_chunk<D, T, INT4, 4>), dim3(grid), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-// waves: 4 or 8, 32 rows each
+// waves: 4, or for INT4 8; 32 rows each
 hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int waves, unsigned grid, hipStream_t s) {
   if (dim == 128) {
     if (dt == KV_BF16) return int4 ? chunk_launch<128, KV_BF16, true>(a, waves, grid, s) : chunk_launch<128, KV_BF16, false>(a, waves, grid, s);
