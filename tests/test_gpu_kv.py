@@ -335,6 +335,30 @@ def test_attention_long(W, case, dtype, int4):
         check(out, lse, [-x for x in qs], kvs, 0.1, dtype, int4, sg, causal, window, hk)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,hk", [(1, 4), (5, 2), (40, 1), (150, 4)])
+def test_int4_fp16_keeps_the_precision_of_its_outputs(W, d, n, hk):
+    """Scores of deviation 3: rounding the rotated query to fp16 alone would leave an error of 3 2^-11 / sqrt(3) and more
+    in the probabilities.  What may stay is one rounding of each probability's product with its value scale and one of
+    the result, each at most 2^-10 / sqrt(12) of its value in the root mean square, independent of each other; 10 % for
+    the sample (about 2000 values or more), and fp32 sums far below."""
+    rng = np.random.default_rng(17 + d + n)
+    heads, page, kls = 8, 16, [700, 331]
+    cache, sg = new_cache(W, rng, sum(-(-m // page) for m in kls) + 3, page, hk, d, torch.float16, True)
+    table, _, kvs = fill(W, rng, cache, sg, kls, hk, d, torch.float16, True, page)
+    q = randn(rng, 2 * n, heads, d, dtype=torch.float16, scale=3.0)
+    args = (torch.tensor([0, n, 2 * n], dtype=torch.int32, device=DEV), torch.tensor(kls, dtype=torch.int32, device=DEV),
+            torch.from_numpy(table).to(DEV))
+    lse = torch.empty(2 * n, heads, device=DEV)
+    got = host64(W.kv_attention(cache, q.to(DEV), *args, lse=lse, max_q_len=n, max_kv_len=max(kls), scale=d ** -0.5))
+    pairs = [K.attention(host64(q)[b * n:b * n + n], k, v, d ** -0.5, True, 0) for b, (k, v) in enumerate(kvs)]
+    want, wl = (np.concatenate([p[i] for p in pairs]) for i in (0, 1))
+    assert np.linalg.norm(got - want) <= 1.1 * math.sqrt(2) * 2.0 ** -10 / math.sqrt(12) * np.linalg.norm(want)
+    # sums of d products in fp32, the two parts of the query good to 2^-22 of its largest value
+    size = d ** -0.5 * 3 * 4.5 * d
+    assert np.abs(host64(lse) - wl).max() <= (E32 * (d + 4) + 2.0 ** -22) * size + 2.0 ** -20 + 4 * E32 * np.abs(wl).max()
+
+
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
 @pytest.mark.parametrize("dtype", DTS)
 @pytest.mark.parametrize("d,n,kv,window", [(64, 5, 50, 0), (128, 5, 50, 0), (128, 90, 150, 0), (64, 90, 150, 40), (128, 6, 200, 9)])

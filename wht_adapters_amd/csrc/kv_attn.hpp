@@ -65,6 +65,12 @@ __device__ __forceinline__ f32x16 kv_mfma32(u32x4 x, u32x4 y, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, x), __builtin_bit_cast(f16x8_t, y), c, 0, 0, 0);
 }
 
+// What rounding x0, x1 to the fp16 pair hi dropped, as a pair.
+__device__ __forceinline__ uint32_t kv_low(uint32_t hi, float x0, float x1) {
+  const f16x2_t h = __builtin_bit_cast(f16x2_t, hi);
+  return pack_f16(x0 - (float)h[0], x1 - (float)h[1]);
+}
+
 // Whether any 16-bit float among the words folded into m (absmax16) is an
 // infinity or NaN.
 template <int T>

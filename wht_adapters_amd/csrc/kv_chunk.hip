@@ -48,6 +48,7 @@ __device__ __forceinline__ int kv_v_at(int row, int c) {
 template <int D, int T, bool INT4, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   constexpr int MT = INT4 ? KV_F16 : T;
+  constexpr bool LOW = INT4 && T == KV_F16;  // the queries' low parts count, see qf
   constexpr int ROWS = 32 * NW, CH = D / 8, ROWB = 2 * D;  // 16-byte chunks and bytes of a tile row
   constexpr int KK = D / 16, DB = D / 32;
   constexpr int TILEB = KV_TILE * ROWB;
@@ -56,6 +57,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   // otherwise it waits for the copies of the next tile before it reads this one.
   __shared__ __attribute__((aligned(16))) uint8_t sk0[TILEB], sk1[TILEB], sv0[TILEB], sv1[TILEB];
   __shared__ __attribute__((aligned(16))) float sks[2][INT4 ? KV_TILE : 1], svs[2][INT4 ? KV_TILE : 1];
+  __shared__ u32x4 sql[NW][LOW ? D / 16 : 1][64];
   auto skb = [&](auto buf) KV_INLINE -> uint8_t* { return buf.value ? sk1 : sk0; };
   auto svb = [&](auto buf) KV_INLINE -> uint8_t* { return buf.value ? sv1 : sv0; };
 
@@ -108,6 +110,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   const int tok = row / a.group, head = h * a.group + row % a.group;
   const bool live = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
   const int pos = p0 + tok;
+  // INT4: the rotated query is rounded to fp16 for its product, 2^-12 of each
+  // value.  bf16 outputs hide that (it adds 1 % to their own 2^-9); fp16
+  // outputs would be off by twice their own rounding, so there what the
+  // rounding dropped goes into a second product, from LDS.
   float qs = fmaxf(fabsf(a.scale), 1e-30f);
   u32x4 qf[KK];
   {
@@ -142,10 +148,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
       const float down = __builtin_ldexpf(1.f, -ex);
       qs *= __builtin_ldexpf(1.f, ex);
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
+      for (int kk = 0; kk < KK; ++kk) {
+        u32x4 low;
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          qf[kk][w] = pack_f16(x[8 * kk + kv_perm(2 * w)] * down, x[8 * kk + kv_perm(2 * w + 1)] * down) ^ turn;
+        for (int w = 0; w < 4; ++w) {
+          const float x0 = x[8 * kk + kv_perm(2 * w)] * down, x1 = x[8 * kk + kv_perm(2 * w + 1)] * down;
+          const uint32_t hi = pack_f16(x0, x1);
+          qf[kk][w] = hi ^ turn;
+          if constexpr (LOW) low[w] = kv_low(hi, x0, x1) ^ turn;
+        }
+        if constexpr (LOW) sql[wave][kk][lane] = low;
+      }
     }
   }
   const float lag = KV_LAG / qs;
@@ -348,11 +361,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   auto scores = [&](f32x16 (&s)[KB], auto buf) KV_INLINE {
     // S^T: lane (qc, hf), s[kb][4 j + e] is key 32 kb + 8 j + 4 hf + e.  Reads
     // run AHEAD products before their use, the order laid down.
-    constexpr int AHEAD = 8;
-    u32x4 f[KB][KK];
+    constexpr int AHEAD = LOW ? 4 : 8;
+    u32x4 f[KB][KK], low[LOW ? KK : 1];
     auto read = [&](int i) KV_INLINE {
       const int kb = i % KB, kk = i / KB, tr = 32 * kb + qc;
       f[kb][kk] = *reinterpret_cast<const u32x4*>(skb(buf) + tr * ROWB + 16 * kv_k_at<D>(tr, 2 * kk + hf));
+      if constexpr (LOW)
+        if (kb == 0) low[kk] = sql[wave][kk][lane];
     };
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) read(i);
@@ -364,6 +379,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
 #pragma unroll
     for (int i = 0; i < KB * KK; ++i) {
       s[i % KB] = kv_mfma32<MT>(f[i % KB][i / KB], qf[i / KB], s[i % KB]);
+      if constexpr (LOW) s[i % KB] = kv_mfma32<MT>(f[i % KB][i / KB], low[i / KB], s[i % KB]);
       if (i + AHEAD < KB * KK) read(i + AHEAD);
       __builtin_amdgcn_sched_barrier(0);
     }

@@ -98,6 +98,7 @@ __device__ __forceinline__ int64_t scalar(int64_t x) {
 template <int D, int T, bool INT4, int NQ, int NW, bool MANY>
 __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAttnArgs a) {
   constexpr int MT = INT4 ? KV_F16 : T;
+  constexpr bool LOW = INT4 && T == KV_F16;  // the queries' low parts count, see qf
   constexpr int KK = D / 32;   // products per 16 keys of S^T
   constexpr int DL = D / 16;   // dims a lane holds of a value row
   constexpr int VW = INT4 ? 1 : DL / 2;  // words of a value row in a lane
@@ -254,8 +255,12 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
       fetch_v(t * TK, pages);
     }
     // the lane's queries (column r of each block of 16) and what they see
+    // INT4: the rotated query is rounded to fp16 for its product, 2^-12 of each
+    // value.  bf16 outputs hide that (it adds 1 % to their own 2^-9); fp16
+    // outputs would be off by twice their own rounding, so there what the
+    // rounding dropped goes into a second product.
     int qpos[NQ];
-    u32x4 qf[NQ][KK];
+    u32x4 qf[NQ][KK], ql[NQ][LOW ? KK : 1];
     float qs[NQ];  // the scores are kept in units of 1 / qs, qs > 0; a negative scale turns q around
     const uint32_t turn = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
@@ -287,8 +292,12 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            qf[n][kk][w] = pack_f16(x[8 * kk + kv_perm(2 * w)] * down, x[8 * kk + kv_perm(2 * w + 1)] * down) ^ turn;
+          for (int w = 0; w < 4; ++w) {
+            const float x0 = x[8 * kk + kv_perm(2 * w)] * down, x1 = x[8 * kk + kv_perm(2 * w + 1)] * down;
+            const uint32_t hi = pack_f16(x0, x1);
+            qf[n][kk][w] = hi ^ turn;
+            if constexpr (LOW) ql[n][kk][w] = kv_low(hi, x0, x1) ^ turn;
+          }
         }
       }
     }
@@ -380,7 +389,10 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
         for (int n = 0; n < NQ; ++n) {
           f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int kk = 0; kk < KK; ++kk) acc = kv_mfma16<MT>(kf[kk], qf[n][kk], acc);
+          for (int kk = 0; kk < KK; ++kk) {
+            acc = kv_mfma16<MT>(kf[kk], qf[n][kk], acc);
+            if constexpr (LOW) acc = kv_mfma16<MT>(kf[kk], ql[n][kk], acc);
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[n][4 * kb + e] = acc[e];
         }
