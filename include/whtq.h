@@ -537,10 +537,10 @@ typedef struct {
  *   k, v: rows k + token * k_stride[0] + head * k_stride[1] (elements) of dim
  *   contiguous values in `dtype` (bf16 or fp16; a DENSE cache has the same
  *   dtype).  slots: device int64[tokens]; a token whose slot lies outside
- *   [0, num_pages * page_size) (-1 for padding) leaves the cache alone; two
- *   tokens with one slot leave either's entry.  rope: NULL for no rotation; a
- *   token whose position lies outside [0, max_position) leaves the cache and
- *   its q_out rows alone.
+ *   [0, num_pages * page_size) (-1 for padding) leaves the cache alone; the
+ *   entry of a slot that two tokens name is undefined.  rope: NULL for no
+ *   rotation; a token whose position lies outside [0, max_position) leaves the
+ *   cache and its q_out rows alone.
  *   q (may be NULL): `heads` rows per token, written rotated to q_out (q_out
  *   == q with equal strides is allowed).
  *   Arithmetic: fp32, rounded once to the stored type.  INT4: y = Hn S k' of
@@ -597,8 +597,11 @@ whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t*
  *   softmax statistics, sums and the joining of splits in fp32; the
  *   probabilities are rounded to the 16-bit type for the second product.
  *   INT4: queries rotated in fp32 and rounded to fp16 under a power of two
- *   per row, codes exact in fp16, the key's scale applied to the fp32 score
+ *   per row (fp16 rows: kept as the sum of two fp16 values), codes exact in fp16, the key's scale applied to the fp32 score
  *   and the value's to the fp32 probability.  Deterministic.
+ *   EUNSUPPORTED beyond 2^30 query tokens, sequences, lengths or table
+ *   entries a row, heads above 65535, and (q_tokens + seqs) * heads / kv_heads
+ *   above 2^30.
  */
 int64_t kv_attention_workspace_bytes(const whtq_kv_cache* cache, int64_t q_tokens, int64_t heads, int64_t seqs,
                                      int64_t max_q_len, int64_t max_kv_len,
