@@ -45,6 +45,13 @@ __device__ __forceinline__ int kv_v_at(int row, int c) {
   return D == 128 ? c ^ (4 * (row & 3)) ^ (2 * ((row >> 2) & 1)) : c ^ (4 * ((row >> 1) & 1));
 }
 
+// INT4: the order in which the lane that unpacks unit c (32 codes, 4 chunks) of
+// a row stores them: chunk j ^ this at step j.
+template <int D>
+__device__ __forceinline__ int kv_turn(bool v, int row, int c) {
+  return (D == 128 ? c & 2 : 2 * (row & 1)) | (v ? c & 1 : 0);
+}
+
 template <int D, int T, bool INT4, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   constexpr int MT = INT4 ? KV_F16 : T;
@@ -220,15 +227,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
       }
     }
   };
-  // INT4: unit u of a tile is 16 bytes (32 codes) of one row of K or V
+  // INT4: unit u of a tile is 16 bytes (32 codes) of one row, first K's units,
+  // then V's; wave 0 holds the keys' scales, wave 1 the values'
   constexpr int UR = D / 32;                   // units of a row
-  constexpr int UNITS = KV_TILE * UR, UT = (UNITS + 64 * NW - 1) / (64 * NW);
-  u32x4 code[2][INT4 ? UT : 1];
-  uint16_t scl[2] = {0, 0};
-  auto unit_row = [&](int n) KV_INLINE { return (n * 64 * NW + (int)threadIdx.x) / UR; };
+  constexpr int UNITS = KV_TILE * UR, UT = (2 * UNITS + 64 * NW - 1) / (64 * NW);
+  u32x4 code[INT4 ? UT : 1];
+  uint16_t scl = 0;
+  auto unit_row = [&](int n) KV_INLINE { return (n * 64 * NW + (int)threadIdx.x) / UR % KV_TILE; };
+  auto unit_of_v = [&](int n) KV_INLINE { return n * NW + wave >= UNITS / 64; };  // wave-uniform
+  auto has_unit = [&](int n) KV_INLINE { return n * NW + wave < UNITS / 32; };
   auto inside = [&](int key) KV_INLINE { return min(max(key, kfirst), klast); };
-  auto has_unit = [&](int n) KV_INLINE { return UNITS % (64 * NW) == 0 || n * 64 * NW + (int)threadIdx.x < UNITS; };
-  const bool has_scale = threadIdx.x < KV_TILE;
+  const bool has_scale = wave < 2;
   // Table entries of a tile, held by the lanes that need them: dense, copy n's
   // in lane n; INT4, of the thread's units and of its scale.  Memory answers
   // in order: they are asked for before the copies of the tile before.
@@ -239,7 +248,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
     if constexpr (INT4) {
 #pragma unroll
       for (int n = 0; n < UT; ++n) p.at[n] = table[inside(key0 + unit_row(n)) >> a.c.page_shift];
-      p.at[UT] = table[inside(key0 + (int)(threadIdx.x % KV_TILE)) >> a.c.page_shift];
+      p.at[UT] = table[inside(key0 + lane) >> a.c.page_shift];
     } else {
       p.at[0] = table[copy_key(lane % COPIES, key0) >> a.c.page_shift];
     }
@@ -258,35 +267,41 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
       copy(buf, key0, p.at[0]);
     } else {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const KvSide& c = v ? a.c.v : a.c.k;
-#pragma unroll
-        for (int n = 0; n < UT; ++n)
-          if (has_unit(n))
-            code[v][n] = ldg_global<u32x4>((v ? vbase : kbase) + (int64_t)p.at[n] * c.page +
-                                           ((uint32_t)(inside(key0 + unit_row(n)) & pmask) * (v ? vtok : ktok) +
-                                            16 * (threadIdx.x % UR)));
-        if (has_scale)
-          scl[v] = c.scale[p.at[UT] * c.s_page + h * c.s_head + (inside(key0 + (int)threadIdx.x) & pmask)];
+      for (int n = 0; n < UT; ++n)
+        if (has_unit(n)) {
+          const bool v = unit_of_v(n);
+          code[n] = ldg_global<u32x4>((v ? vbase : kbase) + (int64_t)p.at[n] * (v ? a.c.v.page : a.c.k.page) +
+                                      ((uint32_t)(inside(key0 + unit_row(n)) & pmask) * (v ? vtok : ktok) +
+                                       16 * (threadIdx.x % UR)));
+        }
+      if (has_scale) {
+        const KvSide& c = wave ? a.c.v : a.c.k;
+        scl = c.scale[p.at[UT] * c.s_page + h * c.s_head + (inside(key0 + lane) & pmask)];
       }
     }
   };
-  auto spread = [&](auto buf) KV_INLINE {  // INT4: the fetched codes and scales to LDS
+  // INT4: the fetched codes and scales to LDS.  Stores of 16 bytes go 8 lanes
+  // at a time, here 8 units of a row or two, in an order of its own each: they
+  // fall on different banks.
+  auto spread = [&](auto buf) KV_INLINE {
     if constexpr (INT4) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
+      for (int n = 0; n < UT; ++n)
+        if (has_unit(n)) {
+          const bool v = unit_of_v(n);
+          const int tr = unit_row(n), c = threadIdx.x % UR;
+          const int turn = kv_turn<D>(v, tr, c);
+          uint8_t* rowp = (v ? svb(buf) : skb(buf)) + tr * ROWB;
+          u32x4 w = code[n];
+          if (turn & 2) w = u32x4{w[2], w[3], w[0], w[1]};
+          if (turn & 1) w = u32x4{w[1], w[0], w[3], w[2]};
 #pragma unroll
-        for (int n = 0; n < UT; ++n)
-          if (has_unit(n)) {
-            const int tr = unit_row(n), c = threadIdx.x % UR;
-            uint8_t* rowp = (v ? svb(buf) : skb(buf)) + tr * ROWB;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<u32x4*>(rowp + 16 * (v ? kv_v_at<D>(tr, 4 * c + j) : kv_k_at<D>(tr, 4 * c + j))) =
-                  kv_codes8(code[v][n][j]);
+          for (int j = 0; j < 4; ++j) {
+            const int at = 4 * c + (j ^ turn);
+            *reinterpret_cast<u32x4*>(rowp + 16 * (v ? kv_v_at<D>(tr, at) : kv_k_at<D>(tr, at))) = kv_codes8(w[j]);
           }
-        if (has_scale) (v ? svs : sks)[buf][threadIdx.x] = (float)__builtin_bit_cast(_Float16, scl[v]);
-      }
+        }
+      if (has_scale) (wave ? svs : sks)[buf][lane] = (float)__builtin_bit_cast(_Float16, scl);
     }
   };
 
@@ -303,7 +318,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   auto wild = [&](auto buf) KV_INLINE {  // whether this thread's part of the V tile holds any
     bool any = false;
     if constexpr (INT4) {
-      any = has_scale && !(svs[buf][threadIdx.x % KV_TILE] < 65536.f);
+      any = wave == 0 && !(svs[buf][lane] < 65536.f);
     } else {
       for (int i = threadIdx.x; i < TILEB / 16; i += 64 * NW) {
         const u32x4 w = *reinterpret_cast<const u32x4*>(svb(buf) + 16 * i);
@@ -347,7 +362,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
     }
     __syncthreads();
     if constexpr (INT4) {
-      if (has_scale && !(svs[buf][threadIdx.x] < 65536.f)) svs[buf][threadIdx.x] = 0.f;
+      if (wave == 0 && !(svs[buf][lane] < 65536.f)) svs[buf][lane] = 0.f;
     } else {
       for (int i = threadIdx.x; i < TILEB / 4; i += 64 * NW) {
         uint32_t* p = reinterpret_cast<uint32_t*>(svb(buf)) + i;
