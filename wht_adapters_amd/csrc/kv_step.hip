@@ -678,12 +678,16 @@ __global__ __launch_bounds__(256) void k_kv_step_join(const KvAttnArgs a, int gr
 template <int D, int T, bool INT4>
 static hipError_t step_launch(const KvAttnArgs& a, int nq, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.c.kv_heads * (a.blocks ? a.blocks : a.seqs)));
+  // 16-bit pages: at most 16 rows, INT4: at most 32 and one kernel for single tokens and chunks
   const bool many = !INT4 && a.rows > a.group;
-  if (nq == 2) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 2, 4, true>), grid, dim3(256), 0, s, a);
-  else if (a.blocks == 0 && many) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 8, true>), grid, dim3(512), 0, s, a);
-  else if (a.blocks == 0) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 8, false>), grid, dim3(512), 0, s, a);
-  else if (many) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 4, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 4, false>), grid, dim3(256), 0, s, a);
+  if (nq == 1 && !many && a.blocks == 0) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 8, false>), grid, dim3(512), 0, s, a);
+  else if (nq == 1 && !many) hipLaunchKernelGGL((k_kv_step<D, T, INT4, 1, 4, false>), grid, dim3(256), 0, s, a);
+  if constexpr (INT4) {
+    if (nq == 2) hipLaunchKernelGGL((k_kv_step<D, T, true, 2, 4, false>), grid, dim3(256), 0, s, a);
+  } else {
+    if (many && a.blocks == 0) hipLaunchKernelGGL((k_kv_step<D, T, false, 1, 8, true>), grid, dim3(512), 0, s, a);
+    else if (many) hipLaunchKernelGGL((k_kv_step<D, T, false, 1, 4, true>), grid, dim3(256), 0, s, a);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.blocks == 0) return e;
   // as many groups a row as keep the machine busy
