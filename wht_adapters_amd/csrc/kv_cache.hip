@@ -8,8 +8,19 @@
 //
 // Both kernels move bytes: what bounds them is memory (and, for a few
 // tokens, the latency of the chain slot / position -> table row -> store).
+// Rows of one token follow each other in the grid, so that a token's cos, sin
+// and slot come from near caches.
+//
+// Measured (kernel times): a prompt of 8192 tokens, 32 + 2 x 8 heads of 128,
+// bf16 pages: 205 MB in 41 us, 5.0 TB/s (a large copy moves 4.75).  4093
+// tokens, 3 x 24 heads of 64, fp16 into INT4: 57 MB in 21 us, the vector
+// pipes half busy with the transform, the rest latency of the one row a group
+// of lanes has.  30011 entries of 8 INT4 heads of 128 read back: 155 MB in
+// 33 us, 4.7 TB/s.  One token: 2.6 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "kv.hpp"
 #include "launch.hpp"
@@ -81,11 +92,25 @@ __device__ __forceinline__ void kv_rotate(float (&x)[16], const KvAppendArgs& a,
   }
 }
 
+template <int M>  // the value of the lane that differs in lane bit M = 1, 2, 4
+__device__ __forceinline__ uint32_t kv_lane_xor(uint32_t x) {
+  constexpr int QUAD = M == 1 ? 0xb1 : M == 2 ? 0x4e : 0x1b;  // quad_perm: lane ^ 1, ^ 2, ^ 3
+  if constexpr (M == 4) x = __builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true);  // row_half_mirror: lane ^ 7
+  return __builtin_amdgcn_mov_dpp(x, QUAD, 0xf, 0xf, true);
+}
+// Butterflies between lanes whose values differ in lane bit M.
+template <int M>
+__device__ __forceinline__ void kv_near_bfly(float (&x)[16], int i) {
+  const float sg = i & M ? -1.f : 1.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = __builtin_fmaf(x[e], sg, as_f(kv_lane_xor<M>(as_u(x[e]))));
+}
+
 template <int D, int T, bool INT4>
 __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
   constexpr int L = D / 16, RB = 256 / L;
   const uint32_t r = blockIdx.x * RB + threadIdx.x / L;
-  const int i = threadIdx.x % L, lane = threadIdx.x & 63;
+  const int i = threadIdx.x % L;
   const uint32_t per = a.heads + 2 * a.c.kv_heads;
   const bool live = r < a.rows;
   const uint32_t t = live ? r / per : 0, hs = live ? r % per : 0;
@@ -125,8 +150,9 @@ __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
     }
     kv_bfly<8>(x);
     kv_bfly<8>(x + 8);
-#pragma unroll
-    for (int m = 1; m < L; m *= 2) kv_lane_bfly<16>(x, m, lane);
+    kv_near_bfly<1>(x, i);
+    kv_near_bfly<2>(x, i);
+    if constexpr (D == 128) kv_near_bfly<4>(x, i);
 #pragma unroll
     for (int e = 0; e < 8; ++e) bfly(x[e], x[8 + e]);
     float top = 0.f;
@@ -136,7 +162,7 @@ __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
       top = fmaxf(top, fabsf(x[e]));
     }
 #pragma unroll
-    for (int m = 1; m < L; m *= 2) top = fmaxf(top, __shfl_xor(top, m, 64));
+    for (int m = 1; m < L; m *= 2) top = fmaxf(top, as_f(m == 1 ? kv_lane_xor<1>(as_u(top)) : m == 2 ? kv_lane_xor<2>(as_u(top)) : kv_lane_xor<4>(as_u(top))));
     const _Float16 s16 = (_Float16)(top / 7.0f);
     const float s = (float)s16, inv = s > 0.f ? 1.0f / s : 0.f;
     uint32_t w[2] = {0u, 0u};
@@ -153,68 +179,120 @@ __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
   }
 }
 
+// The unscaled transform of a row's codes, as whole numbers: at most 8 D = 1024
+// in size, so fp16 holds every step exactly and two values go in one
+// operation (in fp32 they kept the vector pipes 90 % busy over a long prefix).
+// Lane i's words are its chunks' codes, pairs (j, j + 4).
+template <int D>
+__device__ __forceinline__ void kv_rht_codes(uint32_t c0, uint32_t c1, int i, float* x) {
+  f16x2_t p[8];
+  const u32x4 a = kv_codes8(c0), b = kv_codes8(c1);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t aw = a[w], bw = b[w];
+    p[w] = __builtin_bit_cast(f16x2_t, aw);
+    p[4 + w] = __builtin_bit_cast(f16x2_t, bw);
+  }
+#pragma unroll
+  for (int h = 1; h < 8; h *= 2)  // index bits 0 and 1, and the chunks' bit
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+      if (!(w & h)) {
+        const f16x2_t u = p[w], v = p[w + h];
+        p[w] = u + v;
+        p[w + h] = u - v;
+      }
+  auto lanes = [&](auto m) {
+    constexpr int M = decltype(m)::value;
+    const _Float16 one = (_Float16)(i & M ? -1.f : 1.f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+      p[w] = __builtin_elementwise_fma(p[w], f16x2_t{one, one},
+                                       __builtin_bit_cast(f16x2_t, kv_lane_xor<M>(__builtin_bit_cast(uint32_t, p[w]))));
+  };
+  lanes(std::integral_constant<int, 1>{});
+  lanes(std::integral_constant<int, 2>{});
+  if constexpr (D == 128) lanes(std::integral_constant<int, 4>{});
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {  // index bit 2, inside the pairs
+    const _Float16 u = p[w][0], v = p[w][1];
+    const f16x2_t y = __builtin_elementwise_fma(f16x2_t{v, v}, f16x2_t{(_Float16)1.f, (_Float16)-1.f}, f16x2_t{u, u});
+    x[8 * (w >> 2) + (w & 3)] = (float)y[0];
+    x[8 * (w >> 2) + (w & 3) + 4] = (float)y[1];
+  }
+}
+// The signs of eight 16-bit floats in pairs turned by bits 0 .. 7 of b.
+__device__ __forceinline__ void kv_sign_words(u32x4& w, uint32_t b) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w[q] ^= (b << (15 - 2 * q) & 0x8000u) | (b << (30 - 2 * q) & 0x80000000u);
+}
+
 struct KvGatherArgs {
   KvCache c;
   KvRows k, v;
   const int64_t* slots;
   int64_t capacity;
-  uint32_t rows;  // tokens * kv_heads * sides
-  int sides;      // bit 0: keys, bit 1: values
+  uint32_t rows;  // tokens * kv_heads
+  int first, last;  // sides: 0 keys, 1 values
 };
 
+// A group of lanes has a token's key and value of one head: one slot is looked
+// up for both and their loads are in flight together (30011 entries of 8 INT4
+// heads of 128: 33 us against 39 with a group for each; 61 tokens: 5 against 4).
+// A slot outside the cache reads slot 0, whose place there is.
 template <int D, int T, bool INT4>
 __global__ __launch_bounds__(256) void k_kv_gather(const KvGatherArgs a) {
   constexpr int L = D / 16, RB = 256 / L;
   const uint32_t r = blockIdx.x * RB + threadIdx.x / L;
-  const int i = threadIdx.x % L, lane = threadIdx.x & 63;
-  const uint32_t per = a.c.kv_heads * (a.sides == 3 ? 2 : 1);
+  const int i = threadIdx.x % L;
   const bool live = r < a.rows;
-  const uint32_t t = live ? r / per : 0, hs = live ? r % per : 0;
-  const bool is_k = a.sides == 3 ? hs < (uint32_t)a.c.kv_heads : a.sides == 1;
-  const int h = hs < (uint32_t)a.c.kv_heads ? hs : hs - a.c.kv_heads;
+  const uint32_t t = live ? r / a.c.kv_heads : 0, h = live ? r % a.c.kv_heads : 0;
   const int64_t slot = a.slots[t];
   const bool ok = slot >= 0 && slot < a.capacity;
-  const KvSide& c = is_k ? a.c.k : a.c.v;
-  const KvRows& out = is_k ? a.k : a.v;
   const int64_t page = ok ? slot >> a.c.page_shift : 0, off = ok ? slot & ((1 << a.c.page_shift) - 1) : 0;
-  const uint8_t* e0 = c.p + page * c.page + h * c.head + off * c.tok;
-  uint8_t* o = const_cast<uint8_t*>(out.p) + t * out.tok + h * out.head;
-  u32x4 w0 = {0u, 0u, 0u, 0u}, w1 = w0;
-  if constexpr (!INT4) {
-    if (ok) {
-      w0 = ldg<u32x4>(e0 + 16 * i);
-      w1 = ldg<u32x4>(e0 + 16 * (i + L));
-    }
-  } else {
-    const uint32_t c0 = ldg<uint32_t>(e0 + 4 * i), c1 = ldg<uint32_t>(e0 + 4 * (i + L));
-    const uint16_t sb = c.scale[page * c.s_page + h * c.s_head + off];
-    const float s = (float)__builtin_bit_cast(_Float16, sb);
-    float x[16];
+  u32x4 w[2][2];
+  uint32_t codes[2][2];
+  uint16_t sb[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = (float)((int)(c0 << (28 - 4 * e)) >> 28) * s;
-      x[8 + e] = (float)((int)(c1 << (28 - 4 * e)) >> 28) * s;
-    }
-    kv_bfly<8>(x);
-    kv_bfly<8>(x + 8);
-#pragma unroll
-    for (int m = 1; m < L; m *= 2) kv_lane_bfly<16>(x, m, lane);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) bfly(x[e], x[8 + e]);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] *= D == 64 ? 0.125f : 0.08838834764831845f;  // 1 / sqrt(D)
-    if (a.c.signs) {
-      kv_sign8(x, (a.c.signs[i >> 2] >> (8 * (i & 3))) & 255u);
-      kv_sign8(x + 8, (a.c.signs[(i + L) >> 2] >> (8 * ((i + L) & 3))) & 255u);
-    }
-    if (ok) {
-      w0 = kv_round8<T>(x);
-      w1 = kv_round8<T>(x + 8);
+  for (int v = 0; v < 2; ++v) {
+    if (v < a.first || v > a.last) continue;
+    const KvSide& c = v ? a.c.v : a.c.k;
+    const uint8_t* e0 = c.p + page * c.page + h * c.head + off * c.tok;
+    if constexpr (INT4) {
+      codes[v][0] = ldg<uint32_t>(e0 + 4 * i);
+      codes[v][1] = ldg<uint32_t>(e0 + 4 * (i + L));
+      sb[v] = c.scale[page * c.s_page + h * c.s_head + off];
+    } else {
+      w[v][0] = ldg<u32x4>(e0 + 16 * i);
+      w[v][1] = ldg<u32x4>(e0 + 16 * (i + L));
     }
   }
-  if (!live) return;
-  stg<u32x4>(o + 16 * i, w0);
-  stg<u32x4>(o + 16 * (i + L), w1);
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    if (v < a.first || v > a.last) continue;
+    if constexpr (INT4) {
+      float x[16];
+      kv_rht_codes<D>(codes[v][0], codes[v][1], i, x);
+      // of a scale that is not finite nothing is left
+      const float s = (float)__builtin_bit_cast(_Float16, sb[v]);
+      const float f = s < 65536.f ? s * (D == 64 ? 0.125f : 0.08838834764831845f) : __builtin_nanf("");  // s / sqrt(D)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] *= f;
+      w[v][0] = kv_round8<T>(x);
+      w[v][1] = kv_round8<T>(x + 8);
+      if (a.c.signs) {
+        kv_sign_words(w[v][0], a.c.signs[i >> 2] >> (8 * (i & 3)));
+        kv_sign_words(w[v][1], a.c.signs[(i + L) >> 2] >> (8 * ((i + L) & 3)));
+      }
+    }
+    if (!ok) w[v][0] = w[v][1] = u32x4{0u, 0u, 0u, 0u};
+    if (live) {
+      const KvRows& out = v ? a.v : a.k;
+      uint8_t* o = const_cast<uint8_t*>(out.p) + t * out.tok + h * out.head;
+      stg<u32x4>(o + 16 * i, w[v][0]);
+      stg<u32x4>(o + 16 * (i + L), w[v][1]);
+    }
+  }
 }
 
 // Tokens go in launches of at most 2^30 rows (32-bit row numbers in the
@@ -278,8 +356,7 @@ hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_
                             int64_t capacity, void* ko, const int64_t* ks, void* vo, const int64_t* vs,
                             hipStream_t s) {
   const int rb = 256 / (dim / 16);
-  const int sides = (ko ? 1 : 0) | (vo ? 2 : 0);
-  const int64_t per = (int64_t)c.kv_heads * (sides == 3 ? 2 : 1);
+  const int64_t per = c.kv_heads;
   return by_tokens(tokens, per, [&](int64_t t0, int64_t n) {
     KvGatherArgs a{};
     a.c = c;
@@ -287,7 +364,8 @@ hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_
     if (vo) a.v = {(const uint8_t*)vo + t0 * vs[0] * 2, vs[0] * 2, vs[1] * 2};
     a.slots = slots + t0;
     a.capacity = capacity;
-    a.sides = sides;
+    a.first = ko ? 0 : 1;
+    a.last = vo ? 1 : 0;
     a.rows = (uint32_t)(n * per);
     const dim3 grid((unsigned)((n * per + rb - 1) / rb));
     KV_DISPATCH(k_kv_gather, dim, dt, int4, grid, s, a);

@@ -11,6 +11,18 @@
 // Tiles are swizzled (16-byte chunk index XOR row) so that the row reads and
 // the transposing reads spread over the banks.  16-bit pages are copied to
 // LDS directly; INT4 codes go through registers and are stored as exact fp16.
+// Softmax in one pass: a row's maximum may lag (KV_LAG), sums are fp32 of the
+// unrounded probabilities.  32 rows a wave, because 64 (half the LDS reads)
+// need more registers than there are at two waves a SIMD.
+//
+// Measured (kernel times): a prompt of 8192 tokens, 32 heads of 128, bf16:
+// 550 GFLOP in 610 us, 900 TFLOP/s (a large bf16 product of the library: 1300);
+// the matrix pipes are busy half the time and the vector pipes (32 exp2 and
+// about 170 other operations a tile and lane) the other half, the two blocks of
+// a CU overlapping little, at about 1.9 GHz.  512 tokens over 33000 INT4 keys,
+// 64 heads on 8 of 128: 549 GFLOP in 635 us and 9.6 us for the join.  Six
+// fp16 chunks of 5 to 1500 tokens under a window of 1000, 24 heads on 8 of
+// 64: 34 us, 1.25 us a tile of two waves a SIMD, about 10 us before and after.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

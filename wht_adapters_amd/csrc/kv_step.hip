@@ -3,7 +3,7 @@
 //
 // The rows of one key/value head (chunk tokens x the head's query group, at
 // most 16 NQ) share every byte of cache read, so what bounds this kernel is
-// reading the cache once.  A wave takes tiles of 32 keys straight from
+// reading the cache once.  A wave takes tiles of 32 or 64 keys straight from
 // memory into registers, in the MFMA operand layouts (16 x 16 x 32):
 //   S^T = K Q^T   A: lane (r, g) key r of 16, dims 8g .. 8g + 7 of each 32
 //                 (INT4: dims gD/4 .. of the row, one 16-byte load);
@@ -12,10 +12,19 @@
 //                 lane: lane (r, g) loads dims r D/16 .. of the 8 keys (whole
 //                 rows, 16 lanes x 16 bytes) and one v_perm a word pairs two
 //                 keys' values: product i then yields dim r D/16 + i.
-// Nothing goes through LDS until the four waves' results are joined at the
-// end.  The keys are split over blocks until the grid covers the machine a
-// few times; splits leave (maximum, sum, output) in fp32 and k_kv_join adds
-// them in order.
+// Softmax in one pass: a row's maximum may lag (KV_LAG), sums are fp32 of the
+// unrounded probabilities.  An operand register is loaded again for the next
+// tile as soon as its product has used it; nothing goes through LDS until the
+// waves' results are joined at the end.  The keys of all sequences are dealt
+// to the blocks in equal runs (see the comment below), so ragged lengths cost
+// nothing: pieces of a sequence leave (maximum, sum, output) in fp32 and
+// k_kv_step_join adds them in the order of the keys.
+//
+// Measured (kernel times): 64 sequences of 17 to 8191 keys, 32 heads on 8 of
+// 128, bf16: 363 MB in 80 us, 4.5 TB/s (a large copy moves 4.75), and 4.7 us
+// for the join.  Two INT4 contexts of 100003 and 131072 keys, 64 heads on 8:
+// 244 MB in 61 us, 4.0 TB/s, the vector pipes 56 % busy unpacking codes, and
+// 7.4 us for the join.  One token over 777 keys: 8.6 + 4 us, all latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
