@@ -238,8 +238,10 @@ struct KvGatherArgs {
 
 // A group of lanes has a token's key and value of one head: one slot is looked
 // up for both and their loads are in flight together (30011 entries of 8 INT4
-// heads of 128: 33 us against 39 with a group for each; 61 tokens: 5 against 4).
-// A slot outside the cache reads slot 0, whose place there is.
+// heads of 128: 33 us against 39 with a group for each).  Where the machine
+// holds a group for each at once, the two go apart (a grid of two rows; 61
+// tokens of 8 INT4 heads of 128: 4 us against 5).  A slot outside the cache
+// reads slot 0, whose place there is.
 template <int D, int T, bool INT4>
 __global__ __launch_bounds__(256) void k_kv_gather(const KvGatherArgs a) {
   constexpr int L = D / 16, RB = 256 / L;
@@ -250,12 +252,13 @@ __global__ __launch_bounds__(256) void k_kv_gather(const KvGatherArgs a) {
   const int64_t slot = a.slots[t];
   const bool ok = slot >= 0 && slot < a.capacity;
   const int64_t page = ok ? slot >> a.c.page_shift : 0, off = ok ? slot & ((1 << a.c.page_shift) - 1) : 0;
+  const int first = a.first + blockIdx.y, last = gridDim.y == 2 ? first : a.last;
   u32x4 w[2][2];
   uint32_t codes[2][2];
   uint16_t sb[2];
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
-    if (v < a.first || v > a.last) continue;
+    if (v < first || v > last) continue;
     const KvSide& c = v ? a.c.v : a.c.k;
     const uint8_t* e0 = c.p + page * c.page + h * c.head + off * c.tok;
     if constexpr (INT4) {
@@ -269,7 +272,7 @@ __global__ __launch_bounds__(256) void k_kv_gather(const KvGatherArgs a) {
   }
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
-    if (v < a.first || v > a.last) continue;
+    if (v < first || v > last) continue;
     if constexpr (INT4) {
       float x[16];
       kv_rht_codes<D>(codes[v][0], codes[v][1], i, x);
@@ -367,7 +370,10 @@ hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_
     a.first = ko ? 0 : 1;
     a.last = vo ? 1 : 0;
     a.rows = (uint32_t)(n * per);
-    const dim3 grid((unsigned)((n * per + rb - 1) / rb));
+    int dev = 0;
+    (void)hipGetDevice(&dev);
+    const bool apart = ko && vo && 2 * n * per * (dim / 16) <= 2048 * (int64_t)device_cu_count(dev);
+    const dim3 grid((unsigned)((n * per + rb - 1) / rb), apart ? 2 : 1);
     KV_DISPATCH(k_kv_gather, dim, dt, int4, grid, s, a);
   });
 }
