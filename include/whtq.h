@@ -585,9 +585,10 @@ whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t*
  *   there a value that is not finite reaches only the queries that see it.
  *   Device values are not read on the host: max_q_len and max_kv_len bound
  *   the chunk and key counts.  They choose the kernel and the split of the
- *   keys; with max_q_len too small the results of queries beyond it
- *   are undefined, any max_kv_len gives right results; so are the rows of
- *   tokens that belong to no sequence.  kv_len is held to [0, table_width *
+ *   keys; max_q_len is at least 1 where there are tokens and sequences.  With
+ *   max_q_len too small the results of queries beyond it are undefined, and
+ *   so are the rows of tokens that belong to no sequence; any max_kv_len
+ *   gives right results.  kv_len is held to [0, table_width *
  *   page_size]; a table entry outside the cache reads page 0 (no access
  *   outside the cache, a meaningless result).
  *   workspace: device memory of kv_attention_workspace_bytes(...), 16-byte

@@ -151,3 +151,16 @@ def test_workspace_of_invalid_sizes():
 def test_null_cache():
     assert L.kv_append(None, P, st(0, 0), P, st(0, 0), W.BF16, 1, P, None, None, None, 0, None, None, None) == EINVAL
     assert L.kv_gather(None, 1, P, P, st(0, 0), P, st(0, 0), W.BF16, None) == EINVAL
+
+
+@pytest.mark.parametrize("heads", [2, 8])
+@pytest.mark.parametrize("mk", [0, 100, 1 << 20])
+def test_a_chunk_bound_of_zero_is_refused(heads, mk):
+    """Tokens under a bound of no tokens would leave the joining kernel nothing to read but a workspace nobody wrote."""
+    f = L.kv_attention_workspace_bytes
+    for fmt in (0, 1):
+        assert attend(cache(fmt), heads=heads, mq=0, mk=mk) == EINVAL
+        assert attend(cache(fmt), heads=heads, mq=0, mk=mk, ws=P, wb=1 << 40) == EINVAL
+        assert f(cache(fmt), 3, heads, 1, 0, mk, 0) == -1
+        assert attend(cache(fmt), heads=heads, n=0, mq=0, mk=mk) == OK
+        assert attend(cache(fmt), heads=heads, seqs=0, mq=0, mk=mk) == OK

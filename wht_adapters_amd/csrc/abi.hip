@@ -800,7 +800,7 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
   p.step = max_q * group <= (int4 ? 32 : 16);
   if (p.step) {
     p.nq = max_q * group <= 16 ? 1 : 2;
-    p.rows = (int)std::max<int64_t>(1, max_q * group);
+    p.rows = (int)(max_q * group);
     // A block of 8 waves takes a whole sequence, which saves the joining
     // kernel, when every block has a CU at once and its sequence is short, the
     // shorter the fewer blocks there are.  One token, 8 heads of 16-bit 128 (a
@@ -852,6 +852,7 @@ whtq_status kv_attn_sizes(const whtq_kv_cache* c, int64_t q_tokens, int64_t head
                           int64_t max_kv) {
   if (q_tokens < 0 || seqs < 0 || heads < 1 || max_q < 0 || max_kv < 0 || heads % c->kv_heads) return WHTQ_EINVAL;
   if (q_tokens > kMost || seqs > kMost || heads > 65535 || max_q > kMost || max_kv > kMost) return WHTQ_EUNSUPPORTED;
+  if (q_tokens > 0 && seqs > 0 && max_q < 1) return WHTQ_EINVAL;  // no row would have a place
   if ((q_tokens + seqs) * (heads / c->kv_heads) > kMost) return WHTQ_EUNSUPPORTED;  // rows of a head: 32-bit
   return WHTQ_OK;
 }

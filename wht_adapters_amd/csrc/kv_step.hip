@@ -674,8 +674,8 @@ template <int D, int T, bool INT4>
 __global__ __launch_bounds__(256) void k_kv_step_join(const KvAttnArgs a, int gr, int parts) {
   const int part = blockIdx.x % parts, h = blockIdx.x / parts % a.c.kv_heads, b = blockIdx.x / parts / a.c.kv_heads;
   const int q0 = a.q_start[b], q1 = a.q_start[b + 1], i0 = a.reach[2 * b], i1 = a.reach[2 * b + 1];
-  const int rows = min((q1 - q0) * a.group, a.rows);
-  if (rows <= 0 || i0 == i1) return;  // (a sequence without queries has no reach)
+  const int rows = min(q1 - q0, a.rows / a.group) * a.group;  // as kv_span counts them: with none there is no reach
+  if (rows <= 0 || i0 == i1) return;
   const int row = part * (256 / (D / 8) / gr) + threadIdx.x / (D / 8) / gr;
   const int tok = q0 + row / a.group;
   const bool live = row < rows && (uint32_t)tok < (uint64_t)a.q_tokens;
