@@ -1,0 +1,106 @@
+"""The paged key/value cache at its edges, against fp64: runs that cross
+sequences, values and scales that are not finite, tiny queries, tiny
+probabilities, lengths and grids out of the ordinary."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import rtn
+from tests.gpu_util import DEV, host64
+from tests.test_gpu_kv import DTS, E32, U, check, fill, new_cache, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def W():
+    from wht_adapters_amd import whtq
+    return whtq
+
+
+def ints(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x), dtype=dtype).to(DEV)
+
+
+def starts(counts):
+    return ints(np.cumsum([0] + list(counts)))
+
+
+def stored(cache, sg, slots, d):
+    """fp64 (k, v) [slots, kv_heads, d] of an INT4 cache, from its codes and scales."""
+    page, out = cache.page_size, []
+    for codes, scales in ((cache.k, cache.k_scales), (cache.v, cache.v_scales)):
+        c = codes.cpu().numpy()[slots // page, :, slots % page]
+        s = scales.cpu().numpy()[slots // page, :, slots % page]
+        out.append(rtn.dequantize_inverse(c.reshape(-1, d // 2), s.reshape(-1, 1), sg, 4, d, d).reshape(*s.shape, d))
+    return out
+
+
+def reference(q, k, v, scale, window, low):
+    """out, lse [n, heads, ..] in fp64, causal, and a bound on the 2-norm of an output row's error.  Norms bound sums of
+    products in any rotated basis: a score is off by ds = (E32 (d + 8) + low) scale |q| |k|, low for a rotated query's
+    rounding to fp16; u is the probabilities' rounding."""
+    n, heads, d = q.shape
+    group = heads // k.shape[1]
+    kk, vv = (np.repeat(t, group, 1) for t in (k, v))
+    s = scale * np.einsum("ihd,jhd->ihj", q, kk)
+    p, j = len(k) - n + np.arange(n)[:, None, None], np.arange(len(k))
+    s = np.where((j <= p) & ((j > p - window) | (window == 0)), s, -np.inf)
+    top = np.where(np.isfinite(s.max(-1, initial=-np.inf)), s.max(-1, initial=-np.inf), 0.0)
+    w = np.exp(s - top[..., None])
+    total = w.sum(-1)
+    w /= np.where(total == 0, 1.0, total)[..., None]
+    with np.errstate(divide="ignore"):
+        lse = top + np.log(total)
+    norm = lambda t: np.linalg.norm(t, axis=-1)  # noqa: E731
+    ds = (E32 * (d + 8) + low) * scale * norm(q).max(-1, initial=0) * norm(kk).max(initial=0)
+    mean = np.einsum("ihj,jh->ih", w, norm(vv))
+    return np.einsum("ihj,jhd->ihd", w, vv), lse, ds, mean
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,int4,top,window,poison", [
+    (dtype, int4, *rest) for dtype in DTS for int4 in (False, True)
+    for rest in ((1, 0, False), (4, 0, False), (4, 50, False), (4, 0, True)) if not (int4 and rest[2])])
+def test_runs_over_many_sequences(W, d, dtype, int4, top, window, poison):
+    """70 ragged sequences on 32 key heads (a few blocks a head): a block's run of keys goes through many sequences, the
+    runs are of two lengths, some begin after the 64th sequence, and long sequences reach over several.  Poisoned: the
+    last value of every second sequence is not finite on every head, which only its last query sees."""
+    rng = np.random.default_rng(91)
+    hk, heads, page, seqs = 32, 64, 16, 70
+    counts = [0 if b % 11 == 10 else 1 + b % top for b in range(seqs)]
+    lens = [int(x) for x in rng.integers(1, 60, seqs)]
+    lens[3], lens[30], lens[31], lens[66], lens[68] = 1700, 0, 900, 2, 1100
+    cache, sg = new_cache(W, rng, sum(-(-n // page) for n in lens) + 3, page, hk, d, dtype, int4)
+    table, slots, kvs = fill(W, rng, cache, sg, lens, hk, d, dtype, int4, page)
+    bad = [b for b in range(0, seqs, 2) if poison and lens[b] > 4 and counts[b] > 1]
+    for b in bad:
+        s = int(slots[b][-1])
+        cache.v[s // page, :, s % page, :] = (float("nan"), float("inf"))[b % 8 // 4]
+    q = randn(rng, sum(counts), heads, d, dtype=dtype)
+    lse = torch.empty(sum(counts), heads, device=DEV)
+    args = (q.to(DEV), starts(counts), ints(lens), ints(table))
+    out = W.kv_attention(cache, *args, max_q_len=top, max_kv_len=max(lens), scale=0.1, window=window, lse=lse)
+    got, gl, q64, at = host64(out), host64(lse), host64(q), 0
+    um, low = (2.0 ** -11 if int4 else U[dtype]), (2.0 ** -11 if int4 and dtype == torch.bfloat16 else 0.0)
+    for b, n in enumerate(counts):
+        want, wl, ds, mean = reference(q64[at:at + n], *kvs[b], 0.1, window, low)
+        tiny = 0.0 if um > 2.0 ** -9 else lens[b] * 2.0 ** -25
+        bound = ((np.expm1(2 * ds)[:, None] + um + 2.0 ** -20) * mean + tiny * np.abs(kvs[b][1]).max(initial=0) * math.sqrt(d) +
+                 U[dtype] * np.linalg.norm(want, axis=-1) + 2.0 ** -24 * math.sqrt(d))
+        err = np.linalg.norm(got[at:at + n] - want, axis=-1)
+        sees = np.ones(n, bool)
+        if b in bad:
+            sees[-1] = False
+            assert not np.isfinite(got[at + n - 1]).any(), b
+        assert (err <= bound)[sees].all(), (b, err.max(), bound.max())
+        fine = np.isfinite(wl)
+        assert np.array_equal(np.isfinite(gl[at:at + n]), fine)
+        gl0, wl0 = (np.where(fine, t, 0.0) for t in (gl[at:at + n], wl))
+        assert (np.abs(gl0 - wl0) <= ds[:, None] + 2.0 ** -20 + 4 * E32 * np.abs(wl0)).all(), b
+        at += n
+    if not poison:  # the same bytes again
+        again = W.kv_attention(cache, *args, max_q_len=top, max_kv_len=max(lens), scale=0.1, window=window)
+        assert torch.equal(again, out)

@@ -603,6 +603,8 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
     }
     u += take;
     at = 0;
+    // `so` has been read: the next sequence's take_out writes it before its first barrier
+    if (MANY && u < u1) __syncthreads();
   }
 }
 
