@@ -589,7 +589,7 @@ whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t*
  *   max_q_len too small the results of queries beyond it are undefined, and
  *   so are the rows of tokens that belong to no sequence; any max_kv_len
  *   gives right results.  kv_len is held to [0, table_width *
- *   page_size]; a table entry outside the cache reads page 0 (no access
+ *   page_size] and to 2^30; a table entry outside the cache reads page 0 (no access
  *   outside the cache, a meaningless result).
  *   workspace: device memory of kv_attention_workspace_bytes(...), 16-byte
  *   aligned, overwritten (fp32 partial results where the keys are split

@@ -104,3 +104,26 @@ def test_runs_over_many_sequences(W, d, dtype, int4, top, window, poison):
     if not poison:  # the same bytes again
         again = W.kv_attention(cache, *args, max_q_len=top, max_kv_len=max(lens), scale=0.1, window=window)
         assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("mq,most", [(4, 64), (4, 1 << 16), (4096, 64), (4096, 1 << 16)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 5), (False, 7)])
+def test_lengths_are_held_to_the_table(W, int4, mq, most, causal, window):
+    """Lengths below 0 count as 0, lengths beyond the table as its width."""
+    rng = np.random.default_rng(81)
+    hk, heads, d, page, width = 2, 4, 64, 16, 3
+    dtype = torch.bfloat16
+    cache, sg = new_cache(W, rng, 9, page, hk, d, dtype, int4)
+    table, _, kvs = fill(W, rng, cache, sg, [48, 48], hk, d, dtype, int4, page)
+    table = np.concatenate([table[:, :width], np.zeros((4, width), np.int32)])
+    lens = [48, 2 ** 31 - 1, -1, -2 ** 31, -2 ** 31 + 2, 0]
+    none = (np.zeros((0, hk, d)),) * 2
+    counts = [4, 3, 2, 4, 1, 3]
+    q = randn(rng, sum(counts), heads, d, dtype=dtype)
+    lse = torch.empty(sum(counts), heads, device=DEV)
+    out = W.kv_attention(cache, q.to(DEV), starts(counts), ints(lens), ints(table), max_q_len=mq, max_kv_len=most,
+                         scale=0.1, causal=causal, window=window, lse=lse)
+    cut = np.cumsum([0] + counts)
+    check(out, lse, [host64(q)[a:b] for a, b in zip(cut[:-1], cut[1:])], kvs + [none] * 4, 0.1, dtype, int4, sg, causal,
+          window, hk)

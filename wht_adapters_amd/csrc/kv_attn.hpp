@@ -50,6 +50,12 @@ __device__ __forceinline__ int kv_page(const KvAttnArgs& a, int entry) {
   return (uint32_t)entry < (uint64_t)a.c.num_pages ? entry : 0;
 }
 
+// A sequence's length, held to [0, what its row of the table covers] and to
+// 2^30 keys: sums of a position, a window and a tile stay inside 32 bits.
+__device__ __forceinline__ int kv_held(const KvAttnArgs& a, int len) {
+  return max(0, min(len, (int)min<int64_t>((int64_t)a.table_width << a.c.page_shift, 1 << 30)));
+}
+
 template <int T>
 __device__ __forceinline__ f32x4 kv_mfma16(u32x4 x, u32x4 y, f32x4 c) {
   if constexpr (T == KV_BF16)

@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   const int row0 = (int)(slot - ((int64_t)q0 * a.group / ROWS + b)) * ROWS;
   const int rows = chunk * a.group;
   if (row0 < 0 || row0 >= rows) return;
-  const int kv = min(a.kv_len[b], (int)min<int64_t>((int64_t)a.table_width << a.c.page_shift, INT32_MAX));
+  const int kv = kv_held(a, a.kv_len[b]);
   const int p0 = kv - chunk;
   const int32_t* table = a.table + b * a.table_stride;
 

@@ -71,7 +71,7 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, int q0, int q1, i
   s.q0 = q0;
   s.chunk = q1 - q0;
   s.nq = min(s.chunk, a.rows / a.group);  // at most max_q_len
-  const int kv = min(kv_len, (int)min<int64_t>((int64_t)a.table_width << a.c.page_shift, INT32_MAX));
+  const int kv = kv_held(a, kv_len);
   s.p0 = kv - s.chunk;  // position of the first query
   s.first = a.window > 0 ? max(0, s.p0 - a.window + 1) : 0;  // the keys any of its queries sees
   s.last = a.causal ? min(kv - 1, s.p0 + s.nq - 1) : kv - 1;
