@@ -127,3 +127,43 @@ def test_lengths_are_held_to_the_table(W, int4, mq, most, causal, window):
     cut = np.cumsum([0] + counts)
     check(out, lse, [host64(q)[a:b] for a, b in zip(cut[:-1], cut[1:])], kvs + [none] * 4, 0.1, dtype, int4, sg, causal,
           window, hk)
+
+
+def test_more_threads_than_one_launch_takes(W):
+    """2^29 and more rows of 8 lanes: several launches, all of them there."""
+    n, hk, d = (1 << 26) + 3, 4, 128
+    cache = W.kv_cache_alloc(1, 16, hk, d, device=DEV)
+    k, v = (torch.randn(1, hk, d, device=DEV).bfloat16() for _ in range(2))
+    slots = torch.full((n,), -1, dtype=torch.int64, device=DEV)
+    at = [0, (1 << 25) - 1, 1 << 25, n - 1]
+    slots[at] = torch.arange(4, device=DEV)
+    W.kv_append(cache, k.expand(n, hk, d), v.expand(n, hk, d), slots)
+    for c, x in ((cache.k, k), (cache.v, v)):
+        assert torch.equal(c[0, :, :4], x[0][:, None].expand(hk, 4, d)) and not c[0, :, 4:].any()
+    cache = W.kv_cache_alloc(1, 16, 8, d, device=DEV)
+    out = [torch.ones(1, 8, d, device=DEV).bfloat16().expand(n, 8, d) for _ in range(2)]
+    slots.fill_(-1)
+    W.kv_gather(cache, slots, k_out=out[0], v_out=out[1])
+    assert not out[0][0].any() and not out[1][0].any()
+
+
+@pytest.mark.parametrize("mq", [1, 4096])
+def test_more_sequences_than_one_launch_takes(W, mq):
+    """2^21 sequences on 8 key heads, nearly all of them empty: more blocks than one launch has threads for, of the
+    kernel that joins the split keys of a step and of the chunk kernel."""
+    rng = np.random.default_rng(71)
+    seqs, hk, d, page = (1 << 21) + 5, 8, 64, 2048
+    where, lens = [0, 7, 1 << 20, seqs - 1], [2000, 3, 900, 1500]
+    cache, _ = new_cache(W, rng, 5, page, hk, d, torch.bfloat16, False)
+    small, _, kvs = fill(W, rng, cache, None, lens, hk, d, torch.bfloat16, False, page)
+    count = np.zeros(seqs, np.int64)
+    count[where] = 1
+    kv = np.zeros(seqs, np.int32)
+    kv[where] = lens
+    table = np.zeros((seqs, 1), np.int32)
+    table[where, 0] = small[:, 0]
+    q = randn(rng, 4, hk, d, dtype=torch.bfloat16)
+    lse = torch.empty(4, hk, device=DEV)
+    out = W.kv_attention(cache, q.to(DEV), starts(count), ints(kv), ints(table), max_q_len=mq, max_kv_len=2000,
+                         scale=0.125, lse=lse)
+    check(out, lse, [host64(q)[i:i + 1] for i in range(4)], kvs, 0.125, torch.bfloat16, False, None, True, 0, hk)

@@ -13,6 +13,7 @@
 
 #include "../../include/whtq.h"
 #include "kv_attn.hpp"
+#include "launch.hpp"
 
 namespace whtq {
 
@@ -73,7 +74,7 @@ hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_
                             hipStream_t s);
 hipError_t launch_kv_step(const KvAttnArgs& a, int dim, int dt, bool int4, int nq, hipStream_t s);
 hipError_t launch_kv_join(const KvAttnArgs& a, int dim, int dt, bool int4, hipStream_t s);
-hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int waves, unsigned grid, hipStream_t s);
+hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int waves, hipStream_t s);
 int kv_step_unit(int dim, bool int4, bool whole);
 
 static thread_local int g_last_hip = 0;
@@ -836,7 +837,8 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
     // 64 over 8000: 30 against 158)
     const int64_t tiles = (keys + 63) / 64;
     int64_t best = (blocks + slots - 1) / slots * tiles, splits = 1;
-    for (int64_t n = 2; n <= 64 && 4 * n <= tiles; ++n) {
+    const bool joins = q_tokens * heads * (c->dim / 8) <= kLaunchThreads;  // the joining kernel's threads
+    for (int64_t n = 2; joins && n <= 64 && 4 * n <= tiles; ++n) {
       const int64_t cost = (blocks * n + slots - 1) / slots * ((tiles + n - 1) / n) + 8;
       if (cost < best) best = cost, splits = n;
     }
@@ -980,6 +982,7 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   a.causal = causal;
   a.window = (int)std::min(window, kMost);
   a.splits = p.splits;
+  a.grid = (int)p.grid;
   a.scale = scale * 1.4426950408889634f;
   a.part_o = (float*)workspace;
   a.part_ml = a.part_o + p.parts * cache->dim;
@@ -989,7 +992,7 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   const bool int4 = cache->format == WHTQ_KV_INT4;
   const hipStream_t s = (hipStream_t)stream;
   const int dim = (int)cache->dim;
-  hipError_t e = p.step ? launch_kv_step(a, dim, dtype, int4, p.nq, s) : launch_kv_chunk(a, dim, dtype, int4, p.waves, (unsigned)p.grid, s);
+  hipError_t e = p.step ? launch_kv_step(a, dim, dtype, int4, p.nq, s) : launch_kv_chunk(a, dim, dtype, int4, p.waves, s);
   if (e == hipSuccess && !p.step && p.splits > 1) e = launch_kv_join(a, dim, dtype, int4, s);
   return hip_status(e);
 }

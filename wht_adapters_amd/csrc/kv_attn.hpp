@@ -27,8 +27,9 @@ struct KvAttnArgs {
   int* reach;  // step kernel: first and last run of each sequence
   int64_t q_tokens;
   int table_width, heads, group, seqs, causal, window;
-  int splits;              // chunk kernel
+  int splits, grid;        // chunk kernel: splits of the keys, blocks in all
   int blocks, rows;        // step kernel: runs a head (0: a block per sequence), rows of a sequence and head (max_q_len * group)
+  int launched;            // blocks (chunk kernel) or sequences (joining of steps) in the launches before this one
   float scale;  // times log2(e)
 };
 

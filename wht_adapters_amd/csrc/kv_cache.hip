@@ -298,11 +298,11 @@ __global__ __launch_bounds__(256) void k_kv_gather(const KvGatherArgs a) {
   }
 }
 
-// Tokens go in launches of at most 2^30 rows (32-bit row numbers in the
-// kernels); one launch in any ordinary call.
+// Tokens of `per` rows of `lanes` threads, in as many launches as it takes; one
+// in any ordinary call.  (A token is at most 3 x 65535 rows.)
 template <typename F>
-static hipError_t by_tokens(int64_t tokens, int64_t per, F launch) {
-  const int64_t most = std::max<int64_t>(1, (int64_t(1) << 30) / per);
+static hipError_t by_tokens(int64_t tokens, int64_t per, int lanes, F launch) {
+  const int64_t most = kLaunchThreads / (per * lanes);
   for (int64_t t = 0; t < tokens; t += most) {
     launch(t, std::min(most, tokens - t));
     const hipError_t e = hipGetLastError();
@@ -330,7 +330,7 @@ hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_
                             void* qo, const int64_t* qos, hipStream_t s) {
   const int rb = 256 / (dim / 16);
   const int64_t per = (q ? heads : 0) + 2 * (int64_t)c.kv_heads;
-  return by_tokens(tokens, per, [&](int64_t t0, int64_t n) {
+  return by_tokens(tokens, per, dim / 16, [&](int64_t t0, int64_t n) {
     KvAppendArgs a{};
     a.c = c;
     a.k = {(const uint8_t*)k + t0 * ks[0] * 2, ks[0] * 2, ks[1] * 2};
@@ -360,7 +360,7 @@ hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_
                             hipStream_t s) {
   const int rb = 256 / (dim / 16);
   const int64_t per = c.kv_heads;
-  return by_tokens(tokens, per, [&](int64_t t0, int64_t n) {
+  return by_tokens(tokens, per, dim / 16, [&](int64_t t0, int64_t n) {
     KvGatherArgs a{};
     a.c = c;
     if (ko) a.k = {(const uint8_t*)ko + t0 * ks[0] * 2, ks[0] * 2, ks[1] * 2};

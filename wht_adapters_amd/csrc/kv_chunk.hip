@@ -87,14 +87,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   // turn; whole groups of one head and split go to one XCD each, so that its
   // L2 holds their keys (groups beyond a multiple of 8 are spread over all).
   // Later tiles of a causal chunk are longer and go first.
-  const int groups = a.c.kv_heads * a.splits, per = gridDim.x / groups, whole = groups / 8 * 8;
+  const int groups = a.c.kv_heads * a.splits, per = a.grid / groups, whole = groups / 8 * 8;
+  const int block = a.launched + blockIdx.x;
   int hs, slot;
-  if ((int)blockIdx.x < whole * per) {
-    const int i = blockIdx.x >> 3;
-    hs = i / per * 8 + (blockIdx.x & 7);
+  if (block < whole * per) {
+    const int i = block >> 3;
+    hs = i / per * 8 + (block & 7);
     slot = i % per;
   } else {
-    const int i = blockIdx.x - whole * per;
+    const int i = block - whole * per;
     hs = whole + i / per;
     slot = i % per;
   }
@@ -626,24 +627,26 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
 }
 
 template <int D, int T, bool INT4>
-static hipError_t chunk_launch(const KvAttnArgs& a, int waves, unsigned grid, hipStream_t s) {
-  if constexpr (INT4)
-    if (waves == 8) {
-      hipLaunchKernelGGL((k_kv_chunk<D, T, INT4, 8>), dim3(grid), dim3(512), 0, s, a);
-      return hipGetLastError();
-    }
-  hipLaunchKernelGGL((k_kv_chunk<D, T, INT4, 4>), dim3(grid), dim3(256), 0, s, a);
-  return hipGetLastError();
+static hipError_t chunk_launch(KvAttnArgs a, int waves, hipStream_t s) {
+  const int most = (int)(kLaunchThreads / (64 * waves));  // (a multiple of 8: blocks keep their XCDs)
+  for (a.launched = 0;;) {
+    const int n = std::min(a.grid - a.launched, most);
+    if (INT4 && waves == 8) hipLaunchKernelGGL((k_kv_chunk<D, T, INT4, INT4 ? 8 : 4>), dim3(n), dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((k_kv_chunk<D, T, INT4, 4>), dim3(n), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || n == a.grid - a.launched) return e;
+    a.launched += n;
+  }
 }
 
 // waves: 4, or for INT4 8; 32 rows each
-hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int waves, unsigned grid, hipStream_t s) {
+hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int waves, hipStream_t s) {
   if (dim == 128) {
-    if (dt == KV_BF16) return int4 ? chunk_launch<128, KV_BF16, true>(a, waves, grid, s) : chunk_launch<128, KV_BF16, false>(a, waves, grid, s);
-    return int4 ? chunk_launch<128, KV_F16, true>(a, waves, grid, s) : chunk_launch<128, KV_F16, false>(a, waves, grid, s);
+    if (dt == KV_BF16) return int4 ? chunk_launch<128, KV_BF16, true>(a, waves, s) : chunk_launch<128, KV_BF16, false>(a, waves, s);
+    return int4 ? chunk_launch<128, KV_F16, true>(a, waves, s) : chunk_launch<128, KV_F16, false>(a, waves, s);
   }
-  if (dt == KV_BF16) return int4 ? chunk_launch<64, KV_BF16, true>(a, waves, grid, s) : chunk_launch<64, KV_BF16, false>(a, waves, grid, s);
-  return int4 ? chunk_launch<64, KV_F16, true>(a, waves, grid, s) : chunk_launch<64, KV_F16, false>(a, waves, grid, s);
+  if (dt == KV_BF16) return int4 ? chunk_launch<64, KV_BF16, true>(a, waves, s) : chunk_launch<64, KV_BF16, false>(a, waves, s);
+  return int4 ? chunk_launch<64, KV_F16, true>(a, waves, s) : chunk_launch<64, KV_F16, false>(a, waves, s);
 }
 
 }  // namespace whtq

@@ -674,7 +674,7 @@ __global__ __launch_bounds__(256) void k_kv_join(const KvAttnArgs a, int gr) {
 // of the step kernel: a block per sequence, head and `16 or 32 / gr` of its rows
 template <int D, int T, bool INT4>
 __global__ __launch_bounds__(256) void k_kv_step_join(const KvAttnArgs a, int gr, int parts) {
-  const int part = blockIdx.x % parts, h = blockIdx.x / parts % a.c.kv_heads, b = blockIdx.x / parts / a.c.kv_heads;
+  const int part = blockIdx.x % parts, h = blockIdx.x / parts % a.c.kv_heads, b = a.launched + blockIdx.x / parts / a.c.kv_heads;
   const int q0 = a.q_start[b], q1 = a.q_start[b + 1], i0 = a.reach[2 * b], i1 = a.reach[2 * b + 1];
   const int rows = min(q1 - q0, a.rows / a.group) * a.group;  // as kv_span counts them: with none there is no reach
   if (rows <= 0 || i0 == i1) return;
@@ -687,7 +687,7 @@ __global__ __launch_bounds__(256) void k_kv_step_join(const KvAttnArgs a, int gr
 }
 
 template <int D, int T, bool INT4>
-static hipError_t step_launch(const KvAttnArgs& a, int nq, hipStream_t s) {
+static hipError_t step_launch(KvAttnArgs a, int nq, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.c.kv_heads * (a.blocks ? a.blocks : a.seqs)));
   // 16-bit pages: at most 16 rows, INT4: at most 32 and one kernel for single tokens and chunks
   const bool many = !INT4 && a.rows > a.group;
@@ -707,9 +707,13 @@ static hipError_t step_launch(const KvAttnArgs& a, int nq, hipStream_t s) {
   const int64_t rows = a.q_tokens * a.heads;
   while (gr < most && gr < a.blocks && rows * gr < 8192) gr *= 2;
   const int per = most / gr, parts = (a.rows + per - 1) / per;
-  hipLaunchKernelGGL((k_kv_step_join<D, T, INT4>), dim3((unsigned)((int64_t)a.seqs * a.c.kv_heads * parts)), dim3(256), 0,
-                     s, a, gr, parts);
-  return hipGetLastError();
+  const int most_seqs = (int)std::min<int64_t>(a.seqs, kLaunchThreads / 256 / ((int64_t)a.c.kv_heads * parts));
+  for (a.launched = 0; e == hipSuccess && a.launched < a.seqs; a.launched += most_seqs) {
+    const int n = std::min(a.seqs - a.launched, most_seqs);
+    hipLaunchKernelGGL((k_kv_step_join<D, T, INT4>), dim3((unsigned)(n * a.c.kv_heads * parts)), dim3(256), 0, s, a, gr, parts);
+    e = hipGetLastError();
+  }
+  return e;
 }
 template <int D, int T, bool INT4>
 static hipError_t join_launch(const KvAttnArgs& a, hipStream_t s) {

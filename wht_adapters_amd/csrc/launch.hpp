@@ -20,6 +20,10 @@ int blocks_per_cu(K kernel, int block, size_t dyn_lds) {
   return nb;
 }
 
+// Threads of one launch at most: HIP counts a grid's threads in 32 bits, and a
+// launch of more runs a part of them and reports nothing.
+constexpr int64_t kLaunchThreads = int64_t(1) << 31;
+
 // Grid of min(groups, CUs * resident blocks) for a grid-stride kernel.
 // `nb` is the kernel's resident blocks per CU (callers cache it per instance).
 inline unsigned persistent_grid(int64_t groups, int nb) {
