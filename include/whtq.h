@@ -545,7 +545,8 @@ typedef struct {
  *   == q with equal strides is allowed).
  *   Arithmetic: fp32, rounded once to the stored type.  INT4: y = Hn S k' of
  *   the unrounded rotated key, s = fp16_rne(max|y| / 7), code = rint(y * (1 /
- *   s)) held to [-7, 7] (s = 0 gives 0).
+ *   s)) held to [-7, 7] (s = 0 gives 0).  A row with a NaN or an infinity, or one
+ *   whose s exceeds fp16, gets a scale that is not finite and stands for NaN.
  *   Alignment: rows 16-byte aligned (pointers and strides); slots 8 bytes.
  */
 whtq_status kv_append(const whtq_kv_cache* cache, const void* k, const int64_t* k_stride, const void* v,

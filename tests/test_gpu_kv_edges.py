@@ -167,3 +167,57 @@ def test_more_sequences_than_one_launch_takes(W, mq):
     out = W.kv_attention(cache, q.to(DEV), starts(count), ints(kv), ints(table), max_q_len=mq, max_kv_len=2000,
                          scale=0.125, lse=lse)
     check(out, lse, [host64(q)[i:i + 1] for i in range(4)], kvs, 0.125, torch.bfloat16, False, None, True, 0, hk)
+
+
+@pytest.mark.parametrize("bad", [float("nan")])
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("d,n,kv,window", [(64, 5, 50, 0), (128, 5, 700, 0), (64, 1, 700, 0), (128, 90, 150, 0),
+                                           (64, 90, 600, 40)])
+def test_rows_not_finite_in_int4_pages(W, bad, dtype, d, n, kv, window):
+    """A key or value with one value that is not finite: what its entry stands for is NaN all over (the transform
+    spreads it), for gather and for the queries that see it, and for nobody else."""
+    rng = np.random.default_rng(41)
+    hk, heads, page = 2, 4, 16
+    cache, sg = new_cache(W, rng, -(-kv // page) + 2, page, hk, d, dtype, True)
+    table, slots, _ = fill(W, rng, cache, sg, [kv], hk, d, dtype, True, page)
+    slots = slots[0]
+    q = randn(rng, n, heads, d, dtype=dtype)
+    args = (starts([n]), ints([kv]), ints(table))
+
+    def run(mq, most):
+        lse = torch.empty(n, heads, device=DEV)
+        out = W.kv_attention(cache, q.to(DEV), *args, max_q_len=mq, max_kv_len=most, scale=0.1, window=window, lse=lse)
+        return host64(out), host64(lse)
+
+    calls = [(n, kv), (4096, kv), (n, 0), (4096, 1 << 16)]
+    clean = [run(*c) for c in calls]
+    before = [host64(t) for t in W.kv_gather(cache, ints(slots, torch.int64), dtype=dtype)]
+    j = kv - n // 2 - 1  # in the middle of the chunk (its last key where that is one token)
+    rows = ints(slots[j:j + 1], torch.int64)
+    for side in (0, 1):
+        kept = [t.clone() for t in (cache.k, cache.v, cache.k_scales, cache.v_scales)]
+        x = [t.to(dtype).to(DEV) for t in (randn(rng, 1, hk, d), randn(rng, 1, hk, d))]
+        x[side][0, 1, d // 2 + 3] = bad
+        W.kv_append(cache, x[0], x[1], rows)
+        assert not torch.isfinite((cache.k_scales, cache.v_scales)[side][slots[j] // page, 1, slots[j] % page])
+        got = host64(W.kv_gather(cache, ints(slots, torch.int64), dtype=dtype)[side])
+        assert np.isnan(got[j, 1]).all() and np.isfinite(got[j, 0]).all()
+        assert np.array_equal(np.delete(got, j, 0), np.delete(before[side], j, 0))
+        # as it was, with the entry not finite: key head 0's row must not have changed either
+        for new, old in zip((cache.k, cache.v, cache.k_scales, cache.v_scales), kept):
+            new[slots[j] // page, 0, slots[j] % page] = old[slots[j] // page, 0, slots[j] % page]
+            if new.data_ptr() not in ((cache.k, cache.v)[side].data_ptr(), (cache.k_scales, cache.v_scales)[side].data_ptr()):
+                new.copy_(old)
+        p = kv - n + np.arange(n)
+        hit = np.zeros((n, heads), bool)
+        hit[:, 2:] = ((p >= j) & ((p - window < j) | (window == 0)))[:, None]
+        for c, (out0, lse0) in zip(calls, clean):
+            out, lse = run(*c)
+            assert not np.isfinite(out[hit]).any(), (side, c)
+            # two results of the same sums, each good to 2 U of values of size about 1
+            assert np.all(np.abs(out - out0)[~hit] <= 4 * U[dtype]), (side, c)
+            if side == 0:
+                assert np.isnan(lse[hit]).all()
+            assert np.abs(lse - lse0)[~hit].max(initial=0) <= 2.0 ** -18
+        for new, old in zip((cache.k, cache.v, cache.k_scales, cache.v_scales), kept):
+            new.copy_(old)

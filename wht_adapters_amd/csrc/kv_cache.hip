@@ -155,14 +155,15 @@ __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
     if constexpr (D == 128) kv_near_bfly<4>(x, i);
 #pragma unroll
     for (int e = 0; e < 8; ++e) bfly(x[e], x[8 + e]);
+    // NaN stays the maximum: the row's scale is then NaN, and so is what it stands for
     float top = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       x[e] *= D == 64 ? 0.125f : 0.08838834764831845f;  // 1 / sqrt(D)
-      top = fmaxf(top, fabsf(x[e]));
+      top = __builtin_elementwise_maximum(top, fabsf(x[e]));
     }
 #pragma unroll
-    for (int m = 1; m < L; m *= 2) top = fmaxf(top, as_f(m == 1 ? kv_lane_xor<1>(as_u(top)) : m == 2 ? kv_lane_xor<2>(as_u(top)) : kv_lane_xor<4>(as_u(top))));
+    for (int m = 1; m < L; m *= 2) top = __builtin_elementwise_maximum(top, as_f(m == 1 ? kv_lane_xor<1>(as_u(top)) : m == 2 ? kv_lane_xor<2>(as_u(top)) : kv_lane_xor<4>(as_u(top))));
     const _Float16 s16 = (_Float16)(top / 7.0f);
     const float s = (float)s16, inv = s > 0.f ? 1.0f / s : 0.f;
     uint32_t w[2] = {0u, 0u};
