@@ -169,7 +169,7 @@ def test_more_sequences_than_one_launch_takes(W, mq):
     check(out, lse, [host64(q)[i:i + 1] for i in range(4)], kvs, 0.125, torch.bfloat16, False, None, True, 0, hk)
 
 
-@pytest.mark.parametrize("bad", [float("nan")])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("dtype", DTS)
 @pytest.mark.parametrize("d,n,kv,window", [(64, 5, 50, 0), (128, 5, 700, 0), (64, 1, 700, 0), (128, 90, 150, 0),
                                            (64, 90, 600, 40)])

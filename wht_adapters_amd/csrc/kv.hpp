@@ -112,4 +112,17 @@ __device__ __forceinline__ u32x4 kv_codes8(uint32_t w) {
   return u32x4{kv_code_lo(a), kv_code_hi(a), kv_code_lo(b), kv_code_hi(b)};
 }
 
+// The scale of an INT4 entry, from its bits.  An entry whose scale is not finite
+// stands for NaN: an infinite scale must not make a score of -inf, which would
+// hide its key.
+__device__ __forceinline__ float kv_scale(uint16_t b) {
+  const float s = (float)__builtin_bit_cast(_Float16, b);
+  return fabsf(s) < 65536.f ? s : __builtin_nanf("");
+}
+// Two of them in a word, still fp16: x + 0 x.
+__device__ __forceinline__ f16x2_t kv_scale2(uint32_t w) {
+  const f16x2_t h = __builtin_bit_cast(f16x2_t, w), z = {(_Float16)0.f, (_Float16)0.f};
+  return __builtin_elementwise_fma(h, z, h);
+}
+
 }  // namespace whtq

@@ -277,9 +277,7 @@ __global__ __launch_bounds__(256) void k_kv_gather(const KvGatherArgs a) {
     if constexpr (INT4) {
       float x[16];
       kv_rht_codes<D>(codes[v][0], codes[v][1], i, x);
-      // of a scale that is not finite nothing is left
-      const float s = (float)__builtin_bit_cast(_Float16, sb[v]);
-      const float f = s < 65536.f ? s * (D == 64 ? 0.125f : 0.08838834764831845f) : __builtin_nanf("");  // s / sqrt(D)
+      const float f = kv_scale(sb[v]) * (D == 64 ? 0.125f : 0.08838834764831845f);  // s / sqrt(D)
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] *= f;
       w[v][0] = kv_round8<T>(x);

@@ -314,7 +314,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
             *reinterpret_cast<u32x4*>(rowp + 16 * (v ? kv_v_at<D>(tr, at) : kv_k_at<D>(tr, at))) = kv_codes8(w[j]);
           }
         }
-      if (has_scale) (wave ? svs : sks)[buf][lane] = (float)__builtin_bit_cast(_Float16, scl);
+      if (has_scale) (wave ? svs : sks)[buf][lane] = kv_scale(scl);
     }
   };
 

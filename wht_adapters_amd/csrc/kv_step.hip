@@ -379,9 +379,11 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
       float ks[8 * KP], vs[8 * KP];
       if constexpr (INT4) {
 #pragma unroll
-        for (int s = 0; s < 8 * KP; ++s) {
+        for (int s = 0; s < 8 * KP; s += 2) {
           const uint32_t w = ksr[s >> 2][(s >> 1) & 1];
-          ks[s] = (float)__builtin_bit_cast(_Float16, (uint16_t)(s & 1 ? w >> 16 : w & 0xffffu));
+          const f16x2_t h = kv_scale2(w);
+          ks[s] = (float)h[0];
+          ks[s + 1] = (float)h[1];
         }
       }
       // S^T: sc[n][4 kb + e] is key 16 kb + 4 g + e
