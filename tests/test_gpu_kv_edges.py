@@ -221,3 +221,23 @@ def test_rows_not_finite_in_int4_pages(W, bad, dtype, d, n, kv, window):
             assert np.abs(lse - lse0)[~hit].max(initial=0) <= 2.0 ** -18
         for new, old in zip((cache.k, cache.v, cache.k_scales, cache.v_scales), kept):
             new.copy_(old)
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("most", [0, 1 << 16])
+@pytest.mark.parametrize("n,mq", [(1, 1), (5, 5), (5, 4096)])
+@pytest.mark.parametrize("dtype,size,scale", [(torch.bfloat16, 1e-37, 0.1), (torch.bfloat16, 1e-9, 0.0),
+                                              (torch.bfloat16, 1e-20, 1e-20), (torch.bfloat16, 1e-20, 0.0),
+                                              (torch.bfloat16, 2e-38, 1e-30), (torch.float16, 1e-7, 0.0),
+                                              (torch.float16, 1e-7, 1e-38)])
+def test_tiny_queries_give_the_mean(W, int4, n, mq, most, dtype, size, scale):
+    """Scores that are all but 0: the mean of the values seen, lse the logarithm of their number."""
+    rng = np.random.default_rng(31)
+    d, hk, page, kv = 64, 1, 16, 700
+    cache, sg = new_cache(W, rng, 46, page, hk, d, dtype, int4)
+    table, _, kvs = fill(W, rng, cache, sg, [kv], hk, d, dtype, int4, page)
+    q = (randn(rng, n, 2, d) * size).to(dtype)
+    lse = torch.empty(n, 2, device=DEV)
+    out = W.kv_attention(cache, q.to(DEV), starts([n]), ints([kv]), ints(table), max_q_len=mq, max_kv_len=most,
+                         scale=scale, lse=lse)
+    check(out, lse, [host64(q)], kvs, scale, dtype, int4, sg, True, 0, hk)

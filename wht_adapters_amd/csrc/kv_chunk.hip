@@ -124,8 +124,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   const int kfirst = max(first, (b0 + (int)((int64_t)bn * split / a.splits)) * KV_TILE);
   const int klast = min(last, (b0 + (int)((int64_t)bn * (split + 1) / a.splits)) * KV_TILE - 1);
   // The lane's query.  Its scores are kept in units of 1 / qs, qs > 0 (0 would
-  // turn a masked -inf into NaN; 1e-30 gives the same results): a negative
-  // scale turns q around.
+  // turn a masked -inf into NaN; 1e-30 gives the same results, for INT4, whose
+  // power of two takes part, because a score is below 2^27): a negative scale
+  // turns q around.
   const int row = row0 + 32 * wave + qc;
   const int tok = row / a.group, head = h * a.group + row % a.group;
   const bool live = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
       // an exact power of two brings the row's largest value to [1, 2)
       const int ex = top > 0.f && top < __builtin_huge_valf() ? max(-126, min(126, __builtin_amdgcn_frexp_expf(top) - 1)) : 0;
       const float down = __builtin_ldexpf(1.f, -ex);
-      qs *= __builtin_ldexpf(1.f, ex);
+      qs = fmaxf(qs * __builtin_ldexpf(1.f, ex), 1e-30f);
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
         u32x4 low;

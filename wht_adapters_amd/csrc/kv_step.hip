@@ -277,7 +277,9 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
       const int row = 16 * n + r, tok = row / a.group;
       const bool live = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
       qpos[n] = p0 + tok;
-      qs[n] = fmaxf(fabsf(a.scale), 1e-30f);  // 0 would turn a masked -inf into NaN; the results are the same
+      // 0 would turn a masked -inf into NaN; the results are the same (a score in
+      // these units is below 2^27 where INT4's power of two takes part)
+      qs[n] = fmaxf(fabsf(a.scale), 1e-30f);
       const uint8_t* qp = a.q + (int64_t)(q0 + tok) * a.q_tok + (int64_t)(h * a.group + row % a.group) * a.q_head;
       if constexpr (!INT4) {
 #pragma unroll
@@ -297,7 +299,7 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
         // an exact power of two brings the row's largest value to [1, 2)
         const int ex = top > 0.f && top < __builtin_huge_valf() ? max(-126, min(126, __builtin_amdgcn_frexp_expf(top) - 1)) : 0;
         const float down = __builtin_ldexpf(1.f, -ex);
-        qs[n] *= __builtin_ldexpf(1.f, ex);
+        qs[n] = fmaxf(qs[n] * __builtin_ldexpf(1.f, ex), 1e-30f);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
 #pragma unroll
