@@ -241,3 +241,38 @@ def test_tiny_queries_give_the_mean(W, int4, n, mq, most, dtype, size, scale):
     out = W.kv_attention(cache, q.to(DEV), starts([n]), ints([kv]), ints(table), max_q_len=mq, max_kv_len=most,
                          scale=scale, lse=lse)
     check(out, lse, [host64(q)], kvs, scale, dtype, int4, sg, True, 0, hk)
+
+
+@pytest.mark.parametrize("most", [0, 1 << 16])
+def test_zero_values_beside_large_ones_out_of_sight(W, most):
+    """The first tile in the window holds values of 0 and, before the window, large ones; the weight lies on keys of the
+    same wave whose values are the least that INT4 scales hold.  What is out of sight leaves their bits alone."""
+    rng = np.random.default_rng(61)
+    d, page, kv, window, dtype = 64, 64, 1280, 1034, torch.bfloat16
+    cache, sg = new_cache(W, rng, 20, page, 1, d, dtype, True)
+    j = np.arange(kv)
+    # tiles of 64 keys; the window begins inside tile 3; the weight is on the wave's next ones
+    heavy = np.isin(j // 64, [7, 11, 15, 19])
+    q = randn(rng, 1, 4, d, dtype=dtype)
+    k = randn(rng, kv, 1, d)
+    k[~heavy] -= 8.0 * q[0].sum(0)
+    v = randn(rng, kv, 1, d) * 2.0 ** -21
+    v[j < kv - window] = 1e4
+    v[(j >= kv - window) & (j < 256)] = 0.0
+    W.kv_append(cache, k.to(dtype).to(DEV), v.to(dtype).to(DEV), torch.arange(kv, device=DEV))
+    kvs = [stored(cache, sg, j, d)]
+    lse = torch.empty(1, 4, device=DEV)
+    out = W.kv_attention(cache, q.to(DEV), starts([1]), ints([kv]), ints(np.arange(20)[None]), max_q_len=1,
+                         max_kv_len=most, scale=0.125, window=window, lse=lse)
+    # relative to the output: 2^-8 for its rounding and 2^-11 for the probabilities' (keys of one size, so their errors
+    # add up as their values do), 2^-11 |q| |k| / 8 = 0.004 for the rotated query's; together below 0.01, held to 0.03
+    want = check_rel(host64(q), kvs[0], 0.125, kv - window)
+    err = np.linalg.norm(host64(out)[0] - want, axis=-1) / np.linalg.norm(want, axis=-1)
+    assert err.max() <= 0.03, err
+
+
+def check_rel(q, kv, scale, first):
+    k, v = (t[first:, 0] for t in kv)
+    s = scale * (q[0] @ k.T)
+    p = np.exp(s - s.max(-1, keepdims=True))
+    return (p @ v) / p.sum(-1, keepdims=True)

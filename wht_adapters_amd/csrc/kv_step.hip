@@ -436,7 +436,8 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
             if (key_of(s) >= kfirst && key_of(s) <= klast && vs[s] < 65536.f) top = fmaxf(top, vs[s]);
 #pragma unroll
           for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x, 64));
-          const int e = max(ve, __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top) - 1));
+          // (of 0 the exponent would be 0: the largest may be that of a key which does not count)
+          const int e = top > 0.f ? max(ve, __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(top) - 1)) : ve;
           const float f = __builtin_ldexpf(1.f, ve - e);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
