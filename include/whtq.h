@@ -597,10 +597,12 @@ whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t*
  *   across blocks); may be NULL when that is 0.
  *   Arithmetic: 16-bit products on the matrix cores with fp32 accumulation,
  *   softmax statistics, sums and the joining of splits in fp32; the
- *   probabilities are rounded to the 16-bit type for the second product.
- *   INT4: queries rotated in fp32 and rounded to fp16 under a power of two
- *   per row (fp16 rows: kept as the sum of two fp16 values), codes exact in fp16, the key's scale applied to the fp32 score
- *   and the value's to the fp32 probability.  Deterministic.
+ *   probabilities are rounded to the 16-bit type for the second product
+ *   (fp16: with the row's maximum near 2^8, so that they keep their bits down
+ *   to 2^-22 of it and are 0 below 2^-33).  INT4: queries rotated in fp32 and
+ *   rounded to fp16 under a power of two per row (fp16 rows: kept as the sum
+ *   of two fp16 values), codes exact in fp16, the key's scale applied to the
+ *   fp32 score and the value's to the fp32 probability.  Deterministic.
  *   EUNSUPPORTED beyond 2^30 query tokens, sequences, lengths or table
  *   entries a row, heads above 65535, and (q_tokens + seqs) * heads / kv_heads
  *   above 2^30.

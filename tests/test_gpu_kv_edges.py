@@ -276,3 +276,35 @@ def check_rel(q, kv, scale, first):
     s = scale * (q[0] @ k.T)
     p = np.exp(s - s.max(-1, keepdims=True))
     return (p @ v) / p.sum(-1, keepdims=True)
+
+
+@pytest.mark.parametrize("mq", [1, 4096])
+@pytest.mark.parametrize("dtype,int4", [(torch.float16, False), (torch.float16, True), (torch.bfloat16, True),
+                                        (torch.bfloat16, False)])
+def test_many_tiny_probabilities(W, dtype, int4, mq):
+    """Eight keys (one in the first tile of each wave) with value 0 take nearly all the weight; 131064 others, 2^-25.1
+    of theirs each, make the whole result.  A probability has a rounding of u and, in fp16, an absolute one of 2^-25
+    beside a largest one that may stand at 2^8.  A lane adds up to half the keys to its fp32 sum."""
+    rng = np.random.default_rng(51)
+    d, page, kv, lead = 64, 65536, 131072, 64 * np.arange(8)
+    cache, sg = new_cache(W, rng, 2, page, 1, d, dtype, int4)
+    k, v = torch.zeros(kv, 1, d), torch.ones(kv, 1, d)
+    k[lead], v[lead] = 1.0, 0.0
+    W.kv_append(cache, k.to(dtype).to(DEV), v.to(dtype).to(DEV), torch.arange(kv, device=DEV))
+    k64, v64 = stored(cache, sg, np.arange(kv), d) if int4 else (k.double().numpy(), v.double().numpy())
+    gap = float(np.float32(25.1 * math.log(2) / k64[0].sum()))
+    q = torch.ones(1, 1, d, dtype=dtype)
+    lse = torch.empty(1, 1, device=DEV)
+    out = W.kv_attention(cache, q.to(DEV), starts([1]), ints([kv]), ints([[0, 1]]), max_q_len=mq, max_kv_len=64,
+                         scale=gap, lse=lse)
+    s = gap * k64[:, 0].sum(-1)
+    w = np.exp(s - s.max())
+    want = (w @ v64[:, 0]) / w.sum()
+    um = 2.0 ** -11 if int4 else U[dtype]
+    # scores: fp32 sums of d products and the scale's product with log2(e), the rotated query's fp16 rounding
+    ds = (E32 * (d + 8) + (2.0 ** -11 if int4 else 0.0)) * s.max()
+    sums = kv / 2 * E32
+    rel = np.expm1(2 * ds) + um + sums + U[dtype]
+    tiny = 0.0 if dtype == torch.bfloat16 and not int4 else kv * 2.0 ** -25 * 2.0 ** -8 / w.sum() * 1.25
+    assert np.all(np.abs(host64(out)[0, 0] - want) <= rel * np.abs(want).max() + tiny)
+    assert abs(float(lse) - (s.max() + math.log(w.sum()))) <= ds + sums

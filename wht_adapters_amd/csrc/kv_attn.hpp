@@ -40,9 +40,17 @@ constexpr float KV_NEG_INF = -__builtin_huge_valf();
 __device__ __forceinline__ float kv_base(float m) { return m == KV_NEG_INF ? 0.f : m; }
 // Scores are compared with a maximum that may lag behind by up to 2^KV_LAG:
 // the accumulators are rescaled only when a score exceeds it by more.  The
-// probabilities then reach 2^KV_LAG at most (far inside fp16's range) and the
 // final division by the sum makes the result the same.
 constexpr float KV_LAG = 6.f;
+// Probabilities that become fp16 operands are kept times 2^8: with the lag and
+// INT4's value scale (below 2 in the outputs' unit) they stay below 2^15, and
+// their least is 2^-32 of the maximum's instead of 2^-24, so that a hundred
+// thousand keys of small weight beside one of large weight keep theirs (131064
+// keys of 2^-25.1: they were all 0, 0.05 % of the weight and the whole result
+// where the heavy keys' values are 0).  Sums and outputs are in the same unit,
+// maxima leave the kernel in it.  bf16 has fp32's range and needs none of it.
+template <int MT>
+constexpr float KV_UP = MT == KV_F16 ? 8.f : 0.f;
 
 // The page a table entry names; entries outside the cache read page 0.  The
 // kernels load entries one tile of keys ahead of the keys themselves, so that

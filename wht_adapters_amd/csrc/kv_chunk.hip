@@ -466,7 +466,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
         ve = e;
       }
     }
-    const float base = -kv_base(m) * qs - (INT4 ? (float)ve : 0.f);
+    const float base = -kv_base(m) * qs - (INT4 ? (float)ve : 0.f) + KV_UP<MT>;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -609,7 +609,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
             stg<u32x2>(op + 2 * (32 * d + 8 * j + 4 * hf), u32x2{kv_pack<T>(o[d][4 * j], o[d][4 * j + 1]),
                                                                  kv_pack<T>(o[d][4 * j + 2], o[d][4 * j + 3])});
         if (a.lse && hf == 0)
-          a.lse[gr] = l == 0.f ? KV_NEG_INF : (m * qs + (INT4 ? (float)ve : 0.f) + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+          a.lse[gr] = l == 0.f ? KV_NEG_INF : (m * qs + (INT4 ? (float)ve : 0.f) - KV_UP<MT> + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
       } else {
         const int64_t pr = (int64_t)split * a.q_tokens * a.heads + gr;
 #pragma unroll
@@ -619,7 +619,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
             stg<f32x4>(a.part_o + pr * D + 32 * d + 8 * j + 4 * hf,
                        f32x4{o[d][4 * j], o[d][4 * j + 1], o[d][4 * j + 2], o[d][4 * j + 3]});
         if (hf == 0) {
-          a.part_ml[2 * pr] = m == KV_NEG_INF ? m : m * qs + (INT4 ? (float)ve : 0.f);
+          a.part_ml[2 * pr] = m == KV_NEG_INF ? m : m * qs + (INT4 ? (float)ve : 0.f) - KV_UP<MT>;
           a.part_ml[2 * pr + 1] = l;
         }
       }

@@ -481,7 +481,7 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
           for (int i = 0; i < DL; ++i) o[n][i] *= al;
           m[n] = mn;
         }
-        const float base = -kv_base(m[n]) * qs[n] - (INT4 ? (float)ve : 0.f);
+        const float base = -kv_base(m[n]) * qs[n] - (INT4 ? (float)ve : 0.f) + KV_UP<MT>;
         float p[8 * KP];
 #pragma unroll
         for (int s = 0; s < 8 * KP; ++s) {
@@ -559,7 +559,7 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
           *reinterpret_cast<f32x4*>(&so[wave][r][(4 * g + e) * DL + i]) =
               f32x4{o[n][i][e], o[n][i + 1][e], o[n][i + 2][e], o[n][i + 3][e]};
       if (g == 0) {
-        sm[wave][r] = m[n] == KV_NEG_INF ? m[n] : m[n] * qs[n] + (INT4 ? (float)ve : 0.f);
+        sm[wave][r] = m[n] == KV_NEG_INF ? m[n] : m[n] * qs[n] + (INT4 ? (float)ve : 0.f) - KV_UP<MT>;
         sl[wave][r] = ls;
       }
       __syncthreads();
