@@ -308,3 +308,12 @@ def test_many_tiny_probabilities(W, dtype, int4, mq):
     tiny = 0.0 if dtype == torch.bfloat16 and not int4 else kv * 2.0 ** -25 * 2.0 ** -8 / w.sum() * 1.25
     assert np.all(np.abs(host64(out)[0, 0] - want) <= rel * np.abs(want).max() + tiny)
     assert abs(float(lse) - (s.max() + math.log(w.sum()))) <= ds + sums
+
+
+def test_a_window_beyond_all_keys_plans_like_none(W):
+    cache = W.kv_cache_alloc(2, 16, 1, 64, device=DEV)
+    for n in (1, 64):
+        want = W.kv_attention_workspace_bytes(cache, n, 8, 1, n, 8000)
+        assert want > 0
+        for window in (8000, 1 << 40, 2 ** 63 - 1):
+            assert W.kv_attention_workspace_bytes(cache, n, 8, 1, n, 8000, window) == want

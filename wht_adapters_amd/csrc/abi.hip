@@ -830,7 +830,7 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
     // evens out ragged lengths: 64 sequences of 17 to 8191 keys, 2 x 4 rows, 121
     // us against 180 counting a tile for each; 128 of 1000 to 1500: 152 and 127)
     const int64_t blocks = (q_tokens * group + rows - 1) / rows * kvh;
-    const int64_t keys = window > 0 ? std::min(max_kv, window + rows / group + 64) : max_kv;
+    const int64_t keys = window > 0 ? std::min(max_kv, std::min(window, kMost) + rows / group + 64) : max_kv;
     // split the keys of a block's rows where that shortens the longest chain
     // of tiles a slot works off; the joining kernel costs about 8 tiles' time
     // (512 tokens over 33000 keys: 303 us against 632 unsplit and 351 in 16;
