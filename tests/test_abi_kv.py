@@ -164,3 +164,12 @@ def test_a_chunk_bound_of_zero_is_refused(heads, mk):
         assert f(cache(fmt), 3, heads, 1, 0, mk, 0) == -1
         assert attend(cache(fmt), heads=heads, n=0, mq=0, mk=mk) == OK
         assert attend(cache(fmt), heads=heads, seqs=0, mq=0, mk=mk) == OK
+
+
+@pytest.mark.parametrize("call", [append, gather, attend])
+def test_offsets_inside_a_page_stay_below_2_31(call):
+    """Strides whose product with the element's size or the page's would pass 64 bits too."""
+    for fmt in (0, 1):
+        for far in (1 << 27, 1 << 32, 1 << 59, 1 << 62, (1 << 62) + (1 << 61)):
+            assert call(cache(fmt, k_stride=(0, 0, far))) == EUNSUP
+            assert call(cache(fmt, v_stride=(0, 0, far))) == EUNSUP

@@ -753,7 +753,7 @@ whtq_status kv_check(const whtq_kv_cache* c, KvCache* out) {
   if (c->dim != 64 && c->dim != 128) return WHTQ_EUNSUPPORTED;
   if (shift < 4 || shift > 16 || c->num_pages > kMost || c->kv_heads > 65535) return WHTQ_EUNSUPPORTED;
   // offsets inside a page of one head are 32-bit
-  if (std::max(c->k_stride[2], c->v_stride[2]) * esz >= (int64_t(1) << 31) / c->page_size) return WHTQ_EUNSUPPORTED;
+  if (std::max(c->k_stride[2], c->v_stride[2]) >= (int64_t(1) << 31) / c->page_size / esz) return WHTQ_EUNSUPPORTED;
   if (!aligned16(c->k) || !aligned16(c->v)) return WHTQ_EALIGN;
   for (int i = 0; i < 3; ++i)
     if ((c->k_stride[i] * esz & 15) || (c->v_stride[i] * esz & 15)) return WHTQ_EALIGN;
