@@ -618,7 +618,7 @@ def qwha_initialize(w, codes, scales, signs, bits, group, x, total, floor, cap):
 
 # ------------------------------------------------------------ paged key/value cache
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True, eq=False)
 class KVCache:
     """A paged cache of keys and values (include/whtq.h, whtq_kv_cache).
 
@@ -627,8 +627,9 @@ class KVCache:
     v_scales [pages, kv_heads, page_size] and a sign bitmask (dim / 32 words,
     or None).  Any strides with a contiguous last dimension that the header's
     alignment allows (a transposed [pages, page_size, kv_heads, dim] too).
-    The tensors stay the caller's; their addresses are read when the cache is
-    first used, so give a changed tensor to a new KVCache."""
+    The tensors stay the caller's.  Their addresses are read when the KVCache
+    is made: other tensors need a new one (dataclasses.replace), and these must
+    keep their storage (no resize_ or set_)."""
     k: torch.Tensor
     v: torch.Tensor
     k_scales: Optional[torch.Tensor] = None
@@ -643,14 +644,14 @@ class KVCache:
         if self.k.shape != self.v.shape or self.k.dtype != self.v.dtype or self.k.device != self.v.device:
             raise ValueError("k and v must have one shape, dtype and device")
         c = _Cache()
-        self.int4 = self.k.dtype == torch.uint8
-        if not self.int4 and self.k.dtype not in (torch.bfloat16, torch.float16):
+        int4 = self.k.dtype == torch.uint8
+        if not int4 and self.k.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("k and v must be bfloat16, float16 or uint8 (INT4 codes)")
         c.num_pages, c.kv_heads, c.page_size, c.dim = self.k.shape
         c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
         c.k_stride[:], c.v_stride[:] = self.k.stride()[:3], self.v.stride()[:3]
-        c.format = int(self.int4)
-        if self.int4:
+        c.format = int(int4)
+        if int4:
             c.dim = 2 * self.k.shape[3]
             for nm, t in (("k_scales", self.k_scales), ("v_scales", self.v_scales)):
                 _need_cuda(nm, t)
@@ -665,9 +666,8 @@ class KVCache:
             if self.k_scales is not None or self.v_scales is not None or self.signs is not None:
                 raise ValueError("scales and signs belong to INT4 caches")
             c.dtype = _DT[self.k.dtype]
-        self._c = c
-        self.dim, self.kv_heads, self.page_size = c.dim, c.kv_heads, c.page_size
-        self._scale, self._dev = c.dim ** -0.5, self.k.get_device()
+        self.__dict__.update(_c=c, int4=int4, dim=c.dim, kv_heads=c.kv_heads, page_size=c.page_size,
+                             _scale=c.dim ** -0.5, _dev=self.k.get_device())
 
 
 def kv_cache_alloc(num_pages, page_size, kv_heads, dim, *, int4=False, dtype=torch.bfloat16, signs=None, device="cuda"):
