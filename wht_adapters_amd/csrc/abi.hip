@@ -792,22 +792,23 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
   const int64_t group = heads / c->kv_heads, kvh = c->kv_heads;
   const bool int4 = c->format == WHTQ_KV_INT4;
   p.splits = 1;
-  // The step kernel reads an INT4 row once for up to 32 rows (32 sequences of
-  // 4 x 4 rows, 1000 to 1500 keys: 74 us against the chunk kernel's 277) and
-  // shares ragged sequences evenly (64 of 17 to 8191 keys, 4 x 4 rows, 16-bit
-  // pages: 100 to 111 us against 111 to 133).  With 17 to 32 rows of 16-bit
-  // pages it would hold 300 registers: 58 us against the chunk kernel's 30 (128
-  // sequences of 1000 to 1500 keys, one key head).
+  // Figures here are of bf16 rows, 32 heads on 8 of 128 unless said.  The step
+  // kernel reads an INT4 row once for up to 32 rows (32 sequences of 1000 to
+  // 1500 keys, 4 tokens each: 27 us against the chunk kernel's 93, 8 tokens: 77
+  // against 99) and shares ragged sequences evenly (64 of 17 to 8191 keys, 16-bit
+  // pages, 2 tokens each: 110 us against 121, 4 tokens: 114 against 111).  With 17
+  // to 32 rows of 16-bit pages it would hold 300 registers: 58 us against the
+  // chunk kernel's 30 (128 sequences of 1000 to 1500 keys, 32 heads on one).
   p.step = max_q * group <= (int4 ? 32 : 16);
   if (p.step) {
     p.nq = max_q * group <= 16 ? 1 : 2;
     p.rows = (int)(max_q * group);
     // A block of 8 waves takes a whole sequence, which saves the joining
     // kernel, when every block has a CU at once and its sequence is short, the
-    // shorter the fewer blocks there are.  One token, 8 heads of 16-bit 128 (a
-    // unit is 256 keys), whole against shared, us: 64 keys 7.7 and 9.2; 32
-    // sequences (256 blocks) of 1024 keys 27.1 and 28.9; 16 of 512 keys 14.8
-    // and 16.2; but 4 of 512 keys 13.7 and 11.8, 64 of 256 keys 26.4 and 19.2.
+    // shorter the fewer blocks there are.  One token, 16-bit pages (a unit is
+    // 256 keys), whole against shared, us: 64 keys 7.5 and 9.1; 32 sequences
+    // (256 blocks) of 1024 keys 26.6 and 28.8; 16 of 512 keys 14.4 and 16.1; but
+    // 4 of 512 keys 13.7 and 11.6, 64 of 256 keys 26.0 and 19.0.
     const int64_t unit = kv_step_unit((int)c->dim, int4, true), shared = kv_step_unit((int)c->dim, int4, false);
     if (p.nq == 1 && seqs * kvh <= cus && max_kv <= std::max<int64_t>(1, 4 * seqs * kvh / cus) * unit) {
       p.grid = seqs * kvh;
@@ -820,21 +821,29 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
     p.parts = (p.blocks + seqs) * kvh * p.rows;
   } else {
     // INT4 tiles are unpacked once a block: blocks of 8 waves halve that work
-    // where there are rows for them (512 x 8 rows over 20000 keys: 419 us
-    // against 471 with 4 waves; 40 x 8 rows: 72 against 70).  16-bit tiles
+    // where there are rows for them (64 heads on 8, 512 tokens over 20000 keys:
+    // 420 us against 470 with 4 waves; 40 tokens: 75 against 71).  16-bit tiles
     // cost a copy, and blocks of 4 waves wait for fewer others.
     p.waves = int4 && max_q * group > 128 ? 8 : 4;
     const int64_t rows = 32 * p.waves;
-    const int64_t slots = (p.waves == 8 ? 1 : c->dim == 64 ? 3 : 2) * (int64_t)cus;  // blocks at work at a time
+    // Blocks at work at a time, as a CU holds them with 16-bit pages.  INT4 blocks
+    // of 4 waves need more: 2 are held at 64 dims and, with fp16 rows, 1 at 128
+    // dims.  Counting those instead helps as often as it hurts, because blocks
+    // that sequences do not fill are not counted either (INT4, fp16 rows, 128
+    // dims: 12 x 8 rows on 8 key heads over 33000 keys 72 -> 59 us, 100 rows on
+    // 32 over 4000 53 -> 41, but 24 sequences of 16 x 4 rows on 8 over 4000 160
+    // -> 196; 64 dims: the last 81 -> 71, 4 sequences of 100 rows on 32 61 -> 67).
+    const int64_t slots = (p.waves == 8 ? 1 : c->dim == 64 ? 3 : 2) * (int64_t)cus;
     // (as if sequences filled their tiles: many short chunks split more, which
-    // evens out ragged lengths: 64 sequences of 17 to 8191 keys, 2 x 4 rows, 121
-    // us against 180 counting a tile for each; 128 of 1000 to 1500: 152 and 127)
+    // evens out ragged lengths: 64 sequences of 17 to 8191 keys, 16-bit pages, 2
+    // tokens each, 121 us against 180 counting a tile for each; 128 of 1000 to
+    // 1500: 152 and 127)
     const int64_t blocks = (q_tokens * group + rows - 1) / rows * kvh;
     const int64_t keys = window > 0 ? std::min(max_kv, std::min(window, kMost) + rows / group + 64) : max_kv;
     // split the keys of a block's rows where that shortens the longest chain
     // of tiles a slot works off; the joining kernel costs about 8 tiles' time
-    // (512 tokens over 33000 keys: 303 us against 632 unsplit and 351 in 16;
-    // 64 over 8000: 30 against 158)
+    // (16-bit pages, 512 tokens over 33000 keys: 328 us against 626 unsplit and
+    // 353 in 16; 64 over 8000: 31 against 156 and 33)
     const int64_t tiles = (keys + 63) / 64;
     int64_t best = (blocks + slots - 1) / slots * tiles, splits = 1;
     const bool joins = q_tokens * heads * (c->dim / 8) <= kLaunchThreads;  // the joining kernel's threads
