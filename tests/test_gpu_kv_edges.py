@@ -61,15 +61,16 @@ def reference(q, k, v, scale, window, low):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("dtype,int4,top,window,poison", [
+@pytest.mark.parametrize("dtype,int4,top,window,poison,group", [
     (dtype, int4, *rest) for dtype in DTS for int4 in (False, True)
-    for rest in ((1, 0, False), (4, 0, False), (4, 50, False), (4, 0, True)) if not (int4 and rest[2])])
-def test_runs_over_many_sequences(W, d, dtype, int4, top, window, poison):
+    for rest in ((1, 0, False, 2), (4, 0, False, 2), (4, 50, False, 2), (4, 0, True, 2), (4, 0, False, 5))
+    if not (rest[2] if int4 else rest[3] > 4)])  # 20 rows a key head: INT4 alone has a step kernel for them
+def test_runs_over_many_sequences(W, d, dtype, int4, top, window, poison, group):
     """70 ragged sequences on 32 key heads (a few blocks a head): a block's run of keys goes through many sequences, the
     runs are of two lengths, some begin after the 64th sequence, and long sequences reach over several.  Poisoned: the
     last value of every second sequence is not finite on every head, which only its last query sees."""
     rng = np.random.default_rng(91)
-    hk, heads, page, seqs = 32, 64, 16, 70
+    hk, heads, page, seqs = 32, 32 * group, 16, 70
     counts = [0 if b % 11 == 10 else 1 + b % top for b in range(seqs)]
     lens = [int(x) for x in rng.integers(1, 60, seqs)]
     lens[3], lens[30], lens[31], lens[66], lens[68] = 1700, 0, 900, 2, 1100
