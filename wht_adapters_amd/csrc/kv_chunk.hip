@@ -16,13 +16,14 @@
 // need more registers than there are at two waves a SIMD.
 //
 // Measured (kernel times): a prompt of 8192 tokens, 32 heads of 128, bf16:
-// 550 GFLOP in 610 us, 900 TFLOP/s (a large bf16 product of the library: 1300);
+// 550 GFLOP in 580 to 620 us in a row, 660 among other kernels, 835 to 950
+// TFLOP/s (a large bf16 product of the library: 1300);
 // the matrix pipes are busy half the time and the vector pipes (32 exp2 and
 // about 170 other operations a tile and lane) the other half, the two blocks of
 // a CU overlapping little, at about 1.9 GHz.  512 tokens over 33000 INT4 keys,
-// 64 heads on 8 of 128: 549 GFLOP in 635 us and 9.6 us for the join.  Six
+// 64 heads on 8 of 128: 549 GFLOP in 600 to 675 us and 10 us for the join.  Six
 // fp16 chunks of 5 to 1500 tokens under a window of 1000, 24 heads on 8 of
-// 64: 34 us, 1.25 us a tile of two waves a SIMD, about 10 us before and after.
+// 64: 35 us, 1.25 us a tile of two waves a SIMD, about 10 us before and after.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

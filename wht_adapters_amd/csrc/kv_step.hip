@@ -16,15 +16,20 @@
 // unrounded probabilities.  An operand register is loaded again for the next
 // tile as soon as its product has used it; nothing goes through LDS until the
 // waves' results are joined at the end.  The keys of all sequences are dealt
-// to the blocks in equal runs (see the comment below), so ragged lengths cost
-// nothing: pieces of a sequence leave (maximum, sum, output) in fp32 and
-// k_kv_step_join adds them in the order of the keys.
+// to the blocks in equal runs (see the comment below), so that ragged lengths
+// keep all of them busy; the price is the join: pieces of a sequence leave
+// (maximum, sum, output) in fp32 and k_kv_step_join adds them in the order of
+// the keys.
 //
 // Measured (kernel times): 64 sequences of 17 to 8191 keys, 32 heads on 8 of
-// 128, bf16: 363 MB in 80 us, 4.5 TB/s (a large copy moves 4.75), and 4.7 us
+// 128, bf16: 363 MB in 80 us, 4.6 TB/s (a large copy moves 4.75), and 4.7 us
 // for the join.  Two INT4 contexts of 100003 and 131072 keys, 64 heads on 8:
-// 244 MB in 61 us, 4.0 TB/s, the vector pipes 56 % busy unpacking codes, and
-// 7.4 us for the join.  One token over 777 keys: 8.6 + 4 us, all latency.
+// 244 MB in 62 us, 3.9 TB/s, the vector pipes 55 % busy unpacking codes, and
+// 7.1 us for the join.  One token over 777 keys: 8.6 + 4.1 us, all latency.
+// Registers: the INT4 builds keep about 100 scalars in vector lanes, two column
+// blocks (17 to 32 rows) leave one wave a SIMD, and the 16-bit build for several
+// tokens has up to 24 vector registers in scratch (take_out, unrolled over the
+// tile): the 64 sequences with 4 tokens each take 114 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
