@@ -602,7 +602,9 @@ whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t*
  *   to 2^-22 of it and are 0 below 2^-33).  INT4: queries rotated in fp32 and
  *   rounded to fp16 under a power of two per row (fp16 rows: kept as the sum
  *   of two fp16 values), codes exact in fp16, the key's scale applied to the
- *   fp32 score and the value's to the fp32 probability.  Deterministic.
+ *   fp32 score and the value's to the fp32 probability (their product is what
+ *   is rounded: it keeps its bits down to 2^-22 of the largest value scale
+ *   among the keys a wave works on).  Deterministic.
  *   EUNSUPPORTED beyond 2^30 query tokens, sequences, lengths or table
  *   entries a row, heads above 65535, and (q_tokens + seqs) * heads / kv_heads
  *   above 2^30.
