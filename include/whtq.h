@@ -532,6 +532,21 @@ typedef struct {
 } whtq_rope;
 
 /*
+ * Norms of head vectors: x becomes x r w, r = (mean of x^2 over the vector +
+ * eps)^-1/2, before it is rotated.  q and k are weights of dim contiguous
+ * values in `dtype` (fp32, bf16 or fp16; 16-byte aligned): one vector for all
+ * heads with a head stride of 0, or one a head (strides in elements, 16-byte
+ * aligned in bytes).  eps >= 0.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  int64_t q_head, k_head;
+  int32_t dtype;
+  float eps;
+} whtq_qk_norm;
+
+/*
  * kv_append -- rotates `tokens` new keys (and queries, if q is given) and
  * writes keys and values into their cache slots.
  *   k, v: rows k + token * k_stride[0] + head * k_stride[1] (elements) of dim
@@ -553,6 +568,51 @@ whtq_status kv_append(const whtq_kv_cache* cache, const void* k, const int64_t* 
                       const int64_t* v_stride, whtq_dtype dtype, int64_t tokens, const int64_t* slots,
                       const whtq_rope* rope, const void* q, const int64_t* q_stride, int64_t heads, void* q_out,
                       const int64_t* q_out_stride, void* stream);
+
+/*
+ * kv_append_norm -- kv_append with norms of keys (norm->k) and queries
+ *   (norm->q) before the rotation, in the same pass; a NULL weight leaves its
+ *   side as it is, norm NULL both.  Values are never normed.  Norm, weight and
+ *   rotation are fp32, rounded once to the stored type (INT4: not before the
+ *   transform).  Squares of values above 2^63 overflow: such a row gives 0.
+ */
+whtq_status kv_append_norm(const whtq_kv_cache* cache, const void* k, const int64_t* k_stride, const void* v,
+                           const int64_t* v_stride, whtq_dtype dtype, int64_t tokens, const int64_t* slots,
+                           const whtq_qk_norm* norm, const whtq_rope* rope, const void* q, const int64_t* q_stride,
+                           int64_t heads, void* q_out, const int64_t* q_out_stride, void* stream);
+
+/*
+ * qk_norm_rope -- the same norms and rotation on dense rows, for training and
+ *   for prompts that need no cache: y = R(position) (x r w).
+ *   q, k (rows and strides as in kv_append; heads or kv_heads 0 with NULL
+ *   pointers: that side is absent), weights of both sides, rope NULL for no
+ *   rotation.  dim 64 or 128, dtype bf16 or fp16.  Output rows may be the
+ *   input's own (equal pointer and strides).  A token whose position lies
+ *   outside [0, max_position) leaves its output rows alone.
+ * qk_norm_rope_backward -- from the gradients of the outputs (dq_out, dk_out)
+ *   and the same inputs, the rows' gradients
+ *     dx = r (u - x r^2 mean(u x)),  u = w g,  g = R(position)^T dy
+ *   in `dtype`, and the weights' sum g x r over the tokens (and heads that
+ *   share them) as fp32 dq_norm, dk_norm [dim], or [heads][dim] where the
+ *   weights have a head stride.  dq, dk may be dq_out's, dk_out's or q's, k's
+ *   own rows.  A token outside the positions leaves its rows alone and adds
+ *   nothing; no tokens give weights' gradients of 0.
+ *   workspace: device memory of ..._workspace_bytes (16-byte aligned; may be
+ *   NULL when that is 0), overwritten.  fp32 sums; deterministic.
+ */
+whtq_status qk_norm_rope(const void* q, const int64_t* q_stride, int64_t heads, const void* k, const int64_t* k_stride,
+                         int64_t kv_heads, whtq_dtype dtype, int64_t dim, int64_t tokens, const whtq_qk_norm* norm,
+                         const whtq_rope* rope, void* q_out, const int64_t* q_out_stride, void* k_out,
+                         const int64_t* k_out_stride, void* stream);
+int64_t qk_norm_rope_backward_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t tokens,
+                                              const whtq_qk_norm* norm); /* -1: invalid sizes or no device */
+whtq_status qk_norm_rope_backward(const void* dq_out, const int64_t* dq_out_stride, const void* q,
+                                  const int64_t* q_stride, int64_t heads, const void* dk_out,
+                                  const int64_t* dk_out_stride, const void* k, const int64_t* k_stride, int64_t kv_heads,
+                                  whtq_dtype dtype, int64_t dim, int64_t tokens, const whtq_qk_norm* norm,
+                                  const whtq_rope* rope, void* dq, const int64_t* dq_stride, void* dk,
+                                  const int64_t* dk_stride, float* dq_norm, float* dk_norm, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
 
 /*
  * kv_gather -- the keys and values that `tokens` slots stand for, as dense
@@ -619,6 +679,49 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
                          int64_t table_width, int64_t max_q_len, int64_t max_kv_len, float scale, int causal,
                          int64_t window, void* out, const int64_t* out_stride, float* lse, void* workspace,
                          int64_t workspace_bytes, void* stream);
+
+/*
+ * ---- Log probabilities.  How far a quantised model or an adapter is from
+ * the original is judged by the log probabilities that it gives to a text,
+ * and an adapter trains on them.
+ *
+ * token_logprobs -- for rows of `vocab` logits x (fp32, bf16 or fp16, row
+ *   stride ld in elements, no alignment beyond an element's), z = scale x
+ *   (scale > 0: 1 / temperature) and p = softmax(z):
+ *     lse = log sum e^z             (lse_low: what rounding it to fp32 dropped)
+ *     logprob = z[targets[row]] - lse   (a target outside [0, vocab): 0)
+ *     entropy = -sum p log p
+ *     top_id, top_logprob [rows][top]: the `top` largest logits, largest first,
+ *       equal ones by index (the order is that of x), and their z - lse.
+ *   Any of lse, lse_low, entropy may be NULL; targets and logprob both or
+ *   neither.  top: 0 to WHTQ_TOP_MOST and at most vocab.  vocab: up to 2^20.
+ *   Logits of -inf have probability 0 and take part in nothing else; a row of
+ *   only those has lse = logprob = top_logprob = -inf and entropy 0.  A row
+ *   with a NaN or +inf gives NaN for lse, logprob, entropy and top_logprob (a
+ *   NaN counts as -inf in the order of top_id).
+ *   workspace: device memory of token_logprobs_workspace_bytes(...), 16-byte
+ *   aligned, overwritten; may be NULL when that is 0.
+ *   Arithmetic: fp32 over the row, relative to a maximum; deterministic.
+ * token_logprobs_backward -- the gradient of the logits for gradients
+ *   dlogprob and dentropy (fp32 [rows]; either may be NULL, not both),
+ *     dlogits = scale (dlogprob (onehot - p) - dentropy p (log p + entropy)),
+ *   rounded once to the logits' type.  lse, lse_low (NULL: 0) and entropy (for
+ *   dentropy) are token_logprobs's of the same logits and scale.  A target
+ *   outside [0, vocab) makes its row's dlogprob count as 0, whatever it holds.
+ *   A row of only -inf gets zeros.  dlogits == logits (equal strides) is
+ *   allowed.
+ */
+#define WHTQ_TOP_MOST 32
+
+int64_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top); /* -1: invalid sizes or no device */
+whtq_status token_logprobs(const void* logits, whtq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld, float scale,
+                           const int64_t* targets, float* logprob, float* lse, float* lse_low, float* entropy,
+                           int64_t top, float* top_logprob, int64_t* top_id, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+whtq_status token_logprobs_backward(const void* logits, whtq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                    float scale, const int64_t* targets, const float* lse, const float* lse_low,
+                                    const float* entropy, const float* dlogprob, const float* dentropy, void* dlogits,
+                                    int64_t ldd, void* stream);
 
 /*
  * whtq_stream_probe -- measurement helper, not part of the transform path:

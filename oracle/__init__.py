@@ -35,6 +35,8 @@ says so in the docstring ("reading: ...").  Modules:
   harp      dense HARP stage matrices and rotation, block parametrisation
   gemv      low-bit weight x activation product with the rotation online
   qwha_init QWHA initialisation: error coefficients, AdaAlloc, refinement
+  kv        rotary positions, attention over cached keys and values
+  lm        norms of head vectors and log probabilities, with their gradients
   compare   parity rules used to compare a device result with the oracle
 """
 

@@ -11,7 +11,8 @@ input generators in ``wht_adapters_amd.synth`` import without the library.
 
 _API = ("wht_batched", "rht_quantize_rtn", "rht_dequantize_inverse",
         "qwha_adapter_forward", "harp_rotate", "KVCache", "kv_cache_alloc",
-        "kv_append", "kv_gather", "kv_attention", "WhtqError", "lib_path",
+        "kv_append", "kv_gather", "kv_attention", "qk_norm_rope",
+        "qk_norm_rope_backward", "token_logprobs", "token_logprobs_backward", "WhtqError", "lib_path",
         "abi_version")
 
 

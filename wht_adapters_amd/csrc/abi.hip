@@ -14,6 +14,8 @@
 #include "../../include/whtq.h"
 #include "kv_attn.hpp"
 #include "launch.hpp"
+#include "logprob.hpp"
+#include "qk_norm.hpp"
 
 namespace whtq {
 
@@ -66,9 +68,8 @@ hipError_t launch_qi_refine(const float* g, int64_t n, const float* p, int64_t r
 
 hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const void* k,
                             const int64_t* ks, const void* v, const int64_t* vs, const int64_t* slots,
-                            int64_t capacity, const float* cos, const float* sin, const int32_t* pos, int64_t ld_cs,
-                            int64_t max_pos, int rot, int interleaved, const void* q, const int64_t* qs, int heads,
-                            void* qo, const int64_t* qos, hipStream_t s);
+                            int64_t capacity, const KvTurn& turn, const KvNorm& norm, const void* q,
+                            const int64_t* qs, int heads, void* qo, const int64_t* qos, hipStream_t s);
 hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const int64_t* slots,
                             int64_t capacity, void* ko, const int64_t* ks, void* vo, const int64_t* vs,
                             hipStream_t s);
@@ -76,6 +77,11 @@ hipError_t launch_kv_step(const KvAttnArgs& a, int dim, int dt, bool int4, int n
 hipError_t launch_kv_join(const KvAttnArgs& a, int dim, int dt, bool int4, hipStream_t s);
 hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int waves, hipStream_t s);
 int kv_step_unit(int dim, bool int4, bool whole);
+int64_t qk_norm_split(QkArgs& a, int dim, int cus);
+hipError_t launch_qk_norm(QkArgs a, int dim, int dt, hipStream_t s);
+hipError_t launch_qk_norm_back(const QkArgs& a, int dim, int dt, hipStream_t s);
+hipError_t launch_lp(const LpArgs& a, int dt, hipStream_t s);
+hipError_t launch_lp_grad(const LpGradArgs& a, int dt, hipStream_t s);
 
 static thread_local int g_last_hip = 0;
 
@@ -779,6 +785,37 @@ whtq_status kv_check(const whtq_kv_cache* c, KvCache* out) {
 bool kv_rows_valid(const int64_t* st) { return st && st[0] >= 0 && st[1] >= 0; }
 bool kv_rows_aligned(const void* p, const int64_t* st) { return aligned16(p) && !((st[0] * 2) & 15) && !((st[1] * 2) & 15); }
 
+// the rules of rotary positions for rows of dim values, but for alignment
+whtq_status kv_rope_check(const whtq_rope* r, int64_t dim, int64_t tokens) {
+  if (!r) return WHTQ_OK;
+  if (r->rot_dim < 16 || r->rot_dim > dim || r->rot_dim % 16) return WHTQ_EINVAL;
+  if (r->interleaved != 0 && r->interleaved != 1) return WHTQ_EINVAL;
+  if (r->max_position < 1 || r->ld < r->rot_dim / 2) return WHTQ_EINVAL;
+  if (tokens > 0 && (!r->cos || !r->sin || !r->positions)) return WHTQ_EINVAL;
+  return WHTQ_OK;
+}
+bool kv_rope_aligned(const whtq_rope* r) {
+  return !r || (aligned16(r->cos) && aligned16(r->sin) && !(r->ld & 3) && aligned4(r->positions));
+}
+KvTurn kv_turn_of(const whtq_rope* r) {
+  if (!r) return KvTurn{};
+  return KvTurn{r->cos, r->sin, r->positions, r->ld, r->max_position, r->rot_dim, r->interleaved};
+}
+// the rules of norm weights, but for alignment
+whtq_status kv_norm_check(const whtq_qk_norm* n) {
+  if (!dt_valid(n->dtype) || !std::isfinite(n->eps) || n->eps < 0.f) return WHTQ_EINVAL;
+  if (n->q_head < 0 || n->k_head < 0) return WHTQ_EINVAL;
+  return WHTQ_OK;
+}
+bool kv_norm_aligned(const whtq_qk_norm* n) {
+  const int64_t esz = dt_bytes(n->dtype);
+  return aligned16(n->q) && aligned16(n->k) && !(n->q_head * esz & 15) && !(n->k_head * esz & 15);
+}
+KvNorm kv_norm_of(const whtq_qk_norm* n) {
+  const int64_t esz = dt_bytes(n->dtype);
+  return KvNorm{{(const uint8_t*)n->q, n->q_head * esz}, {(const uint8_t*)n->k, n->k_head * esz}, n->dtype, n->eps};
+}
+
 // how an attention call runs: which kernel, and over how many blocks the keys of a row are split
 struct KvPlan {
   bool step;
@@ -882,6 +919,14 @@ whtq_status kv_append(const whtq_kv_cache* cache, const void* k, const int64_t* 
                       const int64_t* v_stride, whtq_dtype dtype, int64_t tokens, const int64_t* slots,
                       const whtq_rope* rope, const void* q, const int64_t* q_stride, int64_t heads, void* q_out,
                       const int64_t* q_out_stride, void* stream) {
+  return kv_append_norm(cache, k, k_stride, v, v_stride, dtype, tokens, slots, nullptr, rope, q, q_stride, heads, q_out,
+                        q_out_stride, stream);
+}
+
+whtq_status kv_append_norm(const whtq_kv_cache* cache, const void* k, const int64_t* k_stride, const void* v,
+                           const int64_t* v_stride, whtq_dtype dtype, int64_t tokens, const int64_t* slots,
+                           const whtq_qk_norm* norm, const whtq_rope* rope, const void* q, const int64_t* q_stride,
+                           int64_t heads, void* q_out, const int64_t* q_out_stride, void* stream) {
   KvCache c;
   whtq_status st = kv_check(cache, &c);
   if (st != WHTQ_OK) return st;
@@ -891,26 +936,21 @@ whtq_status kv_append(const whtq_kv_cache* cache, const void* k, const int64_t* 
   if (tokens > 0 && (!k || !v || !slots)) return WHTQ_EINVAL;
   if (q && (heads < 1 || !q_out || !kv_rows_valid(q_stride) || !kv_rows_valid(q_out_stride))) return WHTQ_EINVAL;
   if (q && q == q_out && (q_stride[0] != q_out_stride[0] || q_stride[1] != q_out_stride[1])) return WHTQ_EINVAL;
-  if (rope) {
-    if (rope->rot_dim < 16 || rope->rot_dim > cache->dim || rope->rot_dim % 16) return WHTQ_EINVAL;
-    if (rope->interleaved != 0 && rope->interleaved != 1) return WHTQ_EINVAL;
-    if (rope->max_position < 1 || rope->ld < rope->rot_dim / 2) return WHTQ_EINVAL;
-    if (tokens > 0 && (!rope->cos || !rope->sin || !rope->positions)) return WHTQ_EINVAL;
-  }
+  st = kv_rope_check(rope, cache->dim, tokens);
+  if (st == WHTQ_OK && norm) st = kv_norm_check(norm);
+  if (st != WHTQ_OK) return st;
+  if (norm && norm->q && !q) return WHTQ_EINVAL;
   if (tokens > kMost || (q && heads > 65535)) return WHTQ_EUNSUPPORTED;
   if (!kv_rows_aligned(k, k_stride) || !kv_rows_aligned(v, v_stride)) return WHTQ_EALIGN;
   if (q && (!kv_rows_aligned(q, q_stride) || !kv_rows_aligned(q_out, q_out_stride))) return WHTQ_EALIGN;
   if (reinterpret_cast<uintptr_t>(slots) & 7u) return WHTQ_EALIGN;
-  if (rope && (!aligned16(rope->cos) || !aligned16(rope->sin) || (rope->ld & 3) || !aligned4(rope->positions)))
-    return WHTQ_EALIGN;
+  if (!kv_rope_aligned(rope) || (norm && !kv_norm_aligned(norm))) return WHTQ_EALIGN;
   if (tokens == 0) return WHTQ_OK;
   st = need_device();
   if (st != WHTQ_OK) return st;
   return hip_status(launch_kv_append(c, (int)cache->dim, dtype, cache->format == WHTQ_KV_INT4, tokens, k, k_stride, v,
-                                     v_stride, slots, cache->num_pages * cache->page_size, rope ? rope->cos : nullptr,
-                                     rope ? rope->sin : nullptr, rope ? rope->positions : nullptr,
-                                     rope ? rope->ld : 0, rope ? rope->max_position : 0, rope ? rope->rot_dim : 0,
-                                     rope ? rope->interleaved : 0, q, q_stride, q ? (int)heads : 0, q_out,
+                                     v_stride, slots, cache->num_pages * cache->page_size, kv_turn_of(rope),
+                                     norm ? kv_norm_of(norm) : KvNorm{}, q, q_stride, q ? (int)heads : 0, q_out,
                                      q_out_stride, (hipStream_t)stream));
 }
 
@@ -1004,6 +1044,231 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   hipError_t e = p.step ? launch_kv_step(a, dim, dtype, int4, p.nq, s) : launch_kv_chunk(a, dim, dtype, int4, p.waves, s);
   if (e == hipSuccess && !p.step && p.splits > 1) e = launch_kv_join(a, dim, dtype, int4, s);
   return hip_status(e);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- norms and positions of dense rows
+
+namespace {
+
+// one side of a call; rows: in and out (x, y) or, backward, x, dy and dx
+whtq_status qk_side(const void* x, const int64_t* xs, const void* a, const int64_t* as, const void* b, const int64_t* bs,
+                    bool back, int64_t heads, int64_t tokens, const void* w) {
+  if (heads == 0) return x || a || b || w ? WHTQ_EINVAL : WHTQ_OK;
+  if (!w || !kv_rows_valid(xs) || !kv_rows_valid(as) || (back && !kv_rows_valid(bs))) return WHTQ_EINVAL;
+  if (tokens > 0 && (!x || !a || (back && !b))) return WHTQ_EINVAL;
+  auto alias = [](const void* p, const int64_t* ps, const void* r, const int64_t* rs) {
+    return p && p == r && (ps[0] != rs[0] || ps[1] != rs[1]);
+  };
+  if (back ? alias(x, xs, b, bs) || alias(a, as, b, bs) : alias(x, xs, a, as)) return WHTQ_EINVAL;
+  return WHTQ_OK;
+}
+whtq_status qk_check(int64_t heads, int64_t kv_heads, int dtype, int64_t dim, int64_t tokens, const whtq_qk_norm* norm,
+                     const whtq_rope* rope) {
+  if (heads < 0 || kv_heads < 0 || heads + kv_heads < 1 || tokens < 0 || !norm || !kv_dtype(dtype) || dim < 1) return WHTQ_EINVAL;
+  whtq_status st = kv_norm_check(norm);
+  if (st == WHTQ_OK) st = kv_rope_check(rope, dim, tokens);
+  if (st != WHTQ_OK) return st;
+  if ((dim != 64 && dim != 128) || tokens > kMost || heads > 65535 || kv_heads > 65535) return WHTQ_EUNSUPPORTED;
+  return WHTQ_OK;
+}
+KvRows qk_rows(const void* p, const int64_t* st) { return p ? KvRows{(const uint8_t*)p, st[0] * 2, st[1] * 2} : KvRows{}; }
+int qk_classes(int64_t heads, int64_t stride) { return heads == 0 ? 0 : stride ? (int)heads : 1; }
+bool qk_aligned(const void* p, const int64_t* st) { return !p || kv_rows_aligned(p, st); }
+
+}  // namespace
+
+extern "C" {
+
+whtq_status qk_norm_rope(const void* q, const int64_t* q_stride, int64_t heads, const void* k, const int64_t* k_stride,
+                         int64_t kv_heads, whtq_dtype dtype, int64_t dim, int64_t tokens, const whtq_qk_norm* norm,
+                         const whtq_rope* rope, void* q_out, const int64_t* q_out_stride, void* k_out,
+                         const int64_t* k_out_stride, void* stream) {
+  whtq_status st = qk_check(heads, kv_heads, dtype, dim, tokens, norm, rope);
+  if (st == WHTQ_OK) st = qk_side(q, q_stride, q_out, q_out_stride, nullptr, nullptr, false, heads, tokens, norm->q);
+  if (st == WHTQ_OK) st = qk_side(k, k_stride, k_out, k_out_stride, nullptr, nullptr, false, kv_heads, tokens, norm->k);
+  if (st != WHTQ_OK) return st;
+  if (!qk_aligned(q, q_stride) || !qk_aligned(q_out, q_out_stride) || !qk_aligned(k, k_stride) ||
+      !qk_aligned(k_out, k_out_stride) || !kv_norm_aligned(norm) || !kv_rope_aligned(rope))
+    return WHTQ_EALIGN;
+  if (tokens == 0) return WHTQ_OK;
+  st = need_device();
+  if (st != WHTQ_OK) return st;
+  const KvNorm n = kv_norm_of(norm);
+  QkArgs a{};
+  a.q = {qk_rows(q, q_stride), qk_rows(q_out, q_out_stride), {}, {}, n.q, nullptr, (int)heads, 0, 0};
+  a.k = {qk_rows(k, k_stride), qk_rows(k_out, k_out_stride), {}, {}, n.k, nullptr, (int)kv_heads, 0, 0};
+  a.turn = kv_turn_of(rope);
+  a.tokens = tokens;
+  a.dt = n.dt;
+  a.eps = n.eps;
+  return hip_status(launch_qk_norm(a, (int)dim, dtype, (hipStream_t)stream));
+}
+
+int64_t qk_norm_rope_backward_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t tokens,
+                                              const whtq_qk_norm* norm) {
+  if (qk_check(heads, kv_heads, WHTQ_BF16, dim, tokens, norm, nullptr) != WHTQ_OK || need_device() != WHTQ_OK) return -1;
+  QkArgs a{};
+  a.tokens = tokens;
+  a.q.heads = (int)heads;
+  a.k.heads = (int)kv_heads;
+  a.q.classes = qk_classes(heads, norm->q_head);
+  a.k.classes = qk_classes(kv_heads, norm->k_head);
+  return qk_norm_split(a, (int)dim, kv_cus()) * dim * 4;
+}
+
+whtq_status qk_norm_rope_backward(const void* dq_out, const int64_t* dq_out_stride, const void* q,
+                                  const int64_t* q_stride, int64_t heads, const void* dk_out,
+                                  const int64_t* dk_out_stride, const void* k, const int64_t* k_stride, int64_t kv_heads,
+                                  whtq_dtype dtype, int64_t dim, int64_t tokens, const whtq_qk_norm* norm,
+                                  const whtq_rope* rope, void* dq, const int64_t* dq_stride, void* dk,
+                                  const int64_t* dk_stride, float* dq_norm, float* dk_norm, void* workspace,
+                                  int64_t workspace_bytes, void* stream) {
+  whtq_status st = qk_check(heads, kv_heads, dtype, dim, tokens, norm, rope);
+  if (st == WHTQ_OK) st = qk_side(q, q_stride, dq_out, dq_out_stride, dq, dq_stride, true, heads, tokens, norm->q);
+  if (st == WHTQ_OK) st = qk_side(k, k_stride, dk_out, dk_out_stride, dk, dk_stride, true, kv_heads, tokens, norm->k);
+  if (st != WHTQ_OK) return st;
+  if ((heads > 0) != (dq_norm != nullptr) || (kv_heads > 0) != (dk_norm != nullptr) || workspace_bytes < 0) return WHTQ_EINVAL;
+  if (!qk_aligned(q, q_stride) || !qk_aligned(dq_out, dq_out_stride) || !qk_aligned(dq, dq_stride) ||
+      !qk_aligned(k, k_stride) || !qk_aligned(dk_out, dk_out_stride) || !qk_aligned(dk, dk_stride) ||
+      !kv_norm_aligned(norm) || !kv_rope_aligned(rope) || !aligned4(dq_norm) || !aligned4(dk_norm) || !aligned16(workspace))
+    return WHTQ_EALIGN;
+  st = need_device();
+  if (st != WHTQ_OK) return st;
+  const KvNorm n = kv_norm_of(norm);
+  QkArgs a{};
+  a.q = {qk_rows(q, q_stride), {}, qk_rows(dq_out, dq_out_stride), qk_rows(dq, dq_stride), n.q, dq_norm, (int)heads,
+         qk_classes(heads, norm->q_head), 0};
+  a.k = {qk_rows(k, k_stride), {}, qk_rows(dk_out, dk_out_stride), qk_rows(dk, dk_stride), n.k, dk_norm, (int)kv_heads,
+         qk_classes(kv_heads, norm->k_head), 0};
+  a.turn = kv_turn_of(rope);
+  a.tokens = tokens;
+  a.dt = n.dt;
+  a.eps = n.eps;
+  const int64_t bytes = qk_norm_split(a, (int)dim, kv_cus()) * dim * 4;
+  if (bytes > 0 && (!workspace || workspace_bytes < bytes)) return WHTQ_EINVAL;
+  a.part = bytes > 0 ? (float*)workspace : nullptr;
+  return hip_status(launch_qk_norm_back(a, (int)dim, dtype, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- log probabilities
+
+namespace {
+
+static_assert(LP_MOST_TOP == WHTQ_TOP_MOST, "room for the likeliest tokens of a row");
+
+whtq_status lp_check(int dtype, int64_t rows, int64_t vocab, int64_t ld, float scale) {
+  if (!dt_valid(dtype) || rows < 0 || vocab < 1 || ld < vocab) return WHTQ_EINVAL;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return WHTQ_EINVAL;
+  if (rows > kMost || vocab > LP_MOST_VOCAB) return WHTQ_EUNSUPPORTED;
+  return WHTQ_OK;
+}
+bool lp_aligned(const void* p, int dtype) { return !(reinterpret_cast<uintptr_t>(p) & (dt_bytes(dtype) - 1)); }
+bool aligned8(const void* p) { return !(reinterpret_cast<uintptr_t>(p) & 7u); }
+
+// How a call runs: blocks of a row, groups whose maxima are kept, and the bytes of both.
+struct LpPlan {
+  int splits, width, groups;
+  int64_t parts, bytes;
+};
+LpPlan lp_plan(int64_t rows, int64_t vocab, int64_t top, int cus) {
+  LpPlan p{};
+  const int64_t chunks = (vocab + LP_CHUNK - 1) / LP_CHUNK;
+  // as many blocks as the machine holds, at least one chunk a wave
+  p.splits = (int)std::max<int64_t>(1, std::min(8 * (int64_t)cus / std::max<int64_t>(rows, 1), chunks / 4));
+  if (top) {
+    // groups enough that the last one's maximum leaves few candidates (64 and more of them, 512 at most but for
+    // vocabularies above 262144), large enough that their maxima are few bytes
+    p.width = vocab <= 4096 ? 8 : vocab <= 32768 ? 64 : LP_CHUNK;
+    p.groups = (int)((vocab + p.width - 1) / p.width);
+  }
+  if (p.splits > 1 || top) p.parts = rows * p.splits * 3;
+  p.bytes = (p.parts + rows * p.groups) * 4;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top) {
+  if (lp_check(WHTQ_F32, rows, vocab, vocab, 1.f) != WHTQ_OK || top < 0 || top > std::min<int64_t>(vocab, LP_MOST_TOP)) return -1;
+  if (need_device() != WHTQ_OK) return -1;
+  return lp_plan(rows, vocab, top, kv_cus()).bytes;
+}
+
+whtq_status token_logprobs(const void* logits, whtq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld, float scale,
+                           const int64_t* targets, float* logprob, float* lse, float* lse_low, float* entropy,
+                           int64_t top, float* top_logprob, int64_t* top_id, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+  whtq_status st = lp_check(dtype, rows, vocab, ld, scale);
+  if (st != WHTQ_OK) return st;
+  if (top < 0 || top > vocab || workspace_bytes < 0) return WHTQ_EINVAL;
+  if (top > WHTQ_TOP_MOST) return WHTQ_EUNSUPPORTED;
+  if (rows > 0 && (!logits || (targets != nullptr) != (logprob != nullptr) || (top > 0 && (!top_logprob || !top_id)))) return WHTQ_EINVAL;
+  if (!lp_aligned(logits, dtype) || !aligned8(targets) || !aligned8(top_id) || !aligned4(logprob) || !aligned4(lse) ||
+      !aligned4(lse_low) || !aligned4(entropy) || !aligned4(top_logprob) || !aligned16(workspace))
+    return WHTQ_EALIGN;
+  if (rows == 0) return WHTQ_OK;
+  st = need_device();
+  if (st != WHTQ_OK) return st;
+  const LpPlan p = lp_plan(rows, vocab, top, kv_cus());
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return WHTQ_EINVAL;
+  LpArgs a{};
+  a.x = (const uint8_t*)logits;
+  a.ld = ld * dt_bytes(dtype);
+  a.rows = rows;
+  a.vocab = (int)vocab;
+  a.scale = scale;
+  a.targets = targets;
+  a.logprob = logprob;
+  a.lse = lse;
+  a.lse_low = lse_low;
+  a.entropy = entropy;
+  a.top = (int)top;
+  a.top_logprob = top_logprob;
+  a.top_id = top_id;
+  a.splits = p.splits;
+  a.width = p.width;
+  a.groups = p.groups;
+  a.part = (float*)workspace;
+  a.best = (uint32_t*)(a.part + p.parts);
+  return hip_status(launch_lp(a, dtype, (hipStream_t)stream));
+}
+
+whtq_status token_logprobs_backward(const void* logits, whtq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                    float scale, const int64_t* targets, const float* lse, const float* lse_low,
+                                    const float* entropy, const float* dlogprob, const float* dentropy, void* dlogits,
+                                    int64_t ldd, void* stream) {
+  whtq_status st = lp_check(dtype, rows, vocab, ld, scale);
+  if (st != WHTQ_OK) return st;
+  if (ldd < vocab || (logits && logits == dlogits && ld != ldd)) return WHTQ_EINVAL;
+  if (rows > 0 && (!logits || !dlogits || !lse || (!dlogprob && !dentropy) || (dlogprob && !targets) || (dentropy && !entropy)))
+    return WHTQ_EINVAL;
+  if (!lp_aligned(logits, dtype) || !lp_aligned(dlogits, dtype) || !aligned8(targets) || !aligned4(lse) ||
+      !aligned4(lse_low) || !aligned4(entropy) || !aligned4(dlogprob) || !aligned4(dentropy))
+    return WHTQ_EALIGN;
+  if (rows == 0) return WHTQ_OK;
+  st = need_device();
+  if (st != WHTQ_OK) return st;
+  LpGradArgs a{};
+  a.x = (const uint8_t*)logits;
+  a.dx = (uint8_t*)dlogits;
+  a.ld = ld * dt_bytes(dtype);
+  a.ldd = ldd * dt_bytes(dtype);
+  a.rows = rows;
+  a.vocab = (int)vocab;
+  a.scale = scale;
+  a.targets = targets;
+  a.lse = lse;
+  a.lse_low = lse_low;
+  a.entropy = entropy;
+  a.dlogprob = dlogprob;
+  a.dentropy = dentropy;
+  return hip_status(launch_lp_grad(a, dtype, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -125,4 +125,11 @@ __device__ __forceinline__ f16x2_t kv_scale2(uint32_t w) {
   return __builtin_elementwise_fma(h, z, h);
 }
 
+// F<dim, type, INT4>(...)
+#define KV_PICK(F, DIM, T, INT4, ...)                                                            \
+  ((DIM) == 128 ? ((T) == KV_BF16 ? ((INT4) ? F<128, KV_BF16, true>(__VA_ARGS__) : F<128, KV_BF16, false>(__VA_ARGS__)) \
+                                  : ((INT4) ? F<128, KV_F16, true>(__VA_ARGS__) : F<128, KV_F16, false>(__VA_ARGS__)))  \
+                : ((T) == KV_BF16 ? ((INT4) ? F<64, KV_BF16, true>(__VA_ARGS__) : F<64, KV_BF16, false>(__VA_ARGS__))   \
+                                  : ((INT4) ? F<64, KV_F16, true>(__VA_ARGS__) : F<64, KV_F16, false>(__VA_ARGS__))))
+
 }  // namespace whtq

@@ -22,91 +22,24 @@
 
 #include <type_traits>
 
-#include "kv.hpp"
+#include "kv_rows.hpp"
 #include "launch.hpp"
 
 namespace whtq {
 
-struct KvRows {
-  const uint8_t* p;
-  int64_t tok, head;  // bytes
-};
 struct KvAppendArgs {
   KvCache c;
   KvRows k, v, q, qo;
   const int64_t* slots;
-  const float *cos, *sin;
-  const int32_t* pos;
-  int64_t ld_cs, max_pos, capacity;
+  KvTurn turn;
+  KvNorm norm;
+  int64_t capacity;
   uint32_t rows;  // tokens * (heads + 2 kv_heads)
-  int heads, rot, interleaved;
+  int heads;
 };
 
-// The two chunks of a lane rotated in place.  Each product and each sum is
-// rounded by itself (no contraction), so the result is the same wherever it
-// is computed.
-template <int D, int T>
-__device__ __forceinline__ void kv_rotate(float (&x)[16], const KvAppendArgs& a, int64_t pos, int i, const uint8_t* row) {
-#pragma clang fp contract(off)
-  constexpr int L = D / 16;
-  const float* cs = a.cos + pos * a.ld_cs;
-  const float* sn = a.sin + pos * a.ld_cs;
-  if (!a.interleaved && a.rot == D) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4 c = ldg<f32x4>(cs + 8 * i + 4 * h), s = ldg<f32x4>(sn + 8 * i + 4 * h);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float u = x[4 * h + e], w = x[8 + 4 * h + e];
-        x[4 * h + e] = u * c[e] - w * s[e];
-        x[8 + 4 * h + e] = w * c[e] + u * s[e];
-      }
-    }
-    return;
-  }
-  const int pair = a.rot / 16;  // chunks in a half
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const int ch = i + b * L;
-    if (ch * 8 >= a.rot) continue;
-    if (a.interleaved) {
-      const f32x4 c = ldg<f32x4>(cs + 4 * ch), s = ldg<f32x4>(sn + 4 * ch);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float u = x[8 * b + 2 * e], w = x[8 * b + 2 * e + 1];
-        x[8 * b + 2 * e] = u * c[e] - w * s[e];
-        x[8 * b + 2 * e + 1] = w * c[e] + u * s[e];
-      }
-    } else {
-      const bool low = ch < pair;
-      const int at = low ? ch : ch - pair;
-      float o[8];
-      kv_widen8<T>(ldg<u32x4>(row + 16 * (low ? ch + pair : ch - pair)), o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float c = cs[8 * at + e], s = sn[8 * at + e], u = x[8 * b + e];
-        const float os = o[e] * s;
-        x[8 * b + e] = low ? u * c - os : u * c + os;
-      }
-    }
-  }
-}
-
-template <int M>  // the value of the lane that differs in lane bit M = 1, 2, 4
-__device__ __forceinline__ uint32_t kv_lane_xor(uint32_t x) {
-  constexpr int QUAD = M == 1 ? 0xb1 : M == 2 ? 0x4e : 0x1b;  // quad_perm: lane ^ 1, ^ 2, ^ 3
-  if constexpr (M == 4) x = __builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true);  // row_half_mirror: lane ^ 7
-  return __builtin_amdgcn_mov_dpp(x, QUAD, 0xf, 0xf, true);
-}
-// Butterflies between lanes whose values differ in lane bit M.
-template <int M>
-__device__ __forceinline__ void kv_near_bfly(float (&x)[16], int i) {
-  const float sg = i & M ? -1.f : 1.f;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = __builtin_fmaf(x[e], sg, as_f(kv_lane_xor<M>(as_u(x[e]))));
-}
-
-template <int D, int T, bool INT4>
+// NORM: keys and queries whose weights are given are normed before they are rotated.
+template <int D, int T, bool INT4, bool NORM>
 __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
   constexpr int L = D / 16, RB = 256 / L;
   const uint32_t r = blockIdx.x * RB + threadIdx.x / L;
@@ -114,7 +47,7 @@ __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
   const uint32_t per = a.heads + 2 * a.c.kv_heads;
   const bool live = r < a.rows;
   const uint32_t t = live ? r / per : 0, hs = live ? r % per : 0;
-  const int64_t pos = a.pos ? (int64_t)a.pos[t] : 0;
+  const int64_t pos = a.turn.pos ? (int64_t)a.turn.pos[t] : 0;
   // head slots of a token: its keys, its values, its queries
   const bool is_k = hs < (uint32_t)a.c.kv_heads, is_q = hs >= 2u * a.c.kv_heads;
   const int h = is_k ? hs : is_q ? hs - 2 * a.c.kv_heads : hs - a.c.kv_heads;
@@ -124,8 +57,22 @@ __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
   kv_widen8<T>(ldg<u32x4>(row + 16 * i), x);
   kv_widen8<T>(ldg<u32x4>(row + 16 * (i + L)), x + 8);
   bool ok = live;
-  if (a.pos) ok = ok && pos >= 0 && pos < a.max_pos;
-  if (a.pos && ok && (is_k || is_q)) kv_rotate<D, T>(x, a, pos, i, row);
+  if (a.turn.pos) ok = ok && pos >= 0 && pos < a.turn.max_pos;
+  if constexpr (NORM) {
+    const KvWeight& w = is_q ? a.norm.q : a.norm.k;
+    if (is_k || is_q) {
+      const uint8_t* wp = w.p ? w.p + h * w.head : nullptr;
+      const float r = kv_norm<D>(x, wp, a.norm.dt, a.norm.eps, i);
+      if (a.turn.pos && ok)
+        kv_rotate<D>(x, a.turn, pos, i, [&](int ch, float* o) {
+          kv_widen8<T>(ldg<u32x4>(row + 16 * ch), o);
+          if (wp) kv_weigh8(o, wp, a.norm.dt, ch, r);
+        });
+    }
+  } else {
+    if (a.turn.pos && ok && (is_k || is_q))
+      kv_rotate<D>(x, a.turn, pos, i, [&](int ch, float* o) { kv_widen8<T>(ldg<u32x4>(row + 16 * ch), o); });
+  }
   if (is_q) {
     if (ok) {
       uint8_t* o = const_cast<uint8_t*>(a.qo.p) + t * a.qo.tok + h * a.qo.head;
@@ -322,11 +269,16 @@ static hipError_t by_tokens(int64_t tokens, int64_t per, int lanes, F launch) {
     else hipLaunchKernelGGL((KERNEL<64, KV_F16, false>), GRID, dim3(256), 0, S, ARGS);                                         \
   } while (0)
 
+template <int D, int T, bool INT4>
+static void append_launch(const KvAppendArgs& a, dim3 grid, hipStream_t s) {
+  if (a.norm.q.p || a.norm.k.p) hipLaunchKernelGGL((k_kv_append<D, T, INT4, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_kv_append<D, T, INT4, false>), grid, dim3(256), 0, s, a);
+}
+
 hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const void* k,
                             const int64_t* ks, const void* v, const int64_t* vs, const int64_t* slots,
-                            int64_t capacity, const float* cos, const float* sin, const int32_t* pos, int64_t ld_cs,
-                            int64_t max_pos, int rot, int interleaved, const void* q, const int64_t* qs, int heads,
-                            void* qo, const int64_t* qos, hipStream_t s) {
+                            int64_t capacity, const KvTurn& turn, const KvNorm& norm, const void* q,
+                            const int64_t* qs, int heads, void* qo, const int64_t* qos, hipStream_t s) {
   const int rb = 256 / (dim / 16);
   const int64_t per = (q ? heads : 0) + 2 * (int64_t)c.kv_heads;
   return by_tokens(tokens, per, dim / 16, [&](int64_t t0, int64_t n) {
@@ -341,16 +293,12 @@ hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_
     }
     a.slots = slots + t0;
     a.capacity = capacity;
-    a.cos = cos;
-    a.sin = sin;
-    a.pos = pos ? pos + t0 : nullptr;
-    a.ld_cs = ld_cs;
-    a.max_pos = max_pos;
-    a.rot = rot;
-    a.interleaved = interleaved;
+    a.turn = turn;
+    if (turn.pos) a.turn.pos += t0;
+    a.norm = norm;
     a.rows = (uint32_t)(n * per);
     const dim3 grid((unsigned)((n * per + rb - 1) / rb));
-    KV_DISPATCH(k_kv_append, dim, dt, int4, grid, s, a);
+    KV_PICK(append_launch, dim, dt, int4, a, grid, s);
   });
 }
 

@@ -736,12 +736,6 @@ static hipError_t join_launch(const KvAttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-#define KV_PICK(F, DIM, T, INT4, ...)                                                            \
-  ((DIM) == 128 ? ((T) == KV_BF16 ? ((INT4) ? F<128, KV_BF16, true>(__VA_ARGS__) : F<128, KV_BF16, false>(__VA_ARGS__)) \
-                                  : ((INT4) ? F<128, KV_F16, true>(__VA_ARGS__) : F<128, KV_F16, false>(__VA_ARGS__)))  \
-                : ((T) == KV_BF16 ? ((INT4) ? F<64, KV_BF16, true>(__VA_ARGS__) : F<64, KV_BF16, false>(__VA_ARGS__))   \
-                                  : ((INT4) ? F<64, KV_F16, true>(__VA_ARGS__) : F<64, KV_F16, false>(__VA_ARGS__))))
-
 // Keys of a unit of the step kernel (one tile for each wave of a block).
 int kv_step_unit(int dim, bool int4, bool whole) { return (dim == 128 && !int4 ? 32 : 64) * (whole ? 8 : 4); }
 

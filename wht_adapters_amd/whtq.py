@@ -9,7 +9,7 @@ import ctypes
 import dataclasses
 import functools
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -36,7 +36,12 @@ class _Rope(ctypes.Structure):  # whtq_rope
                 ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
+class _Norm(ctypes.Structure):  # whtq_qk_norm
+    _fields_ = [("q", _vp), ("k", _vp), ("q_head", _i64), ("k_head", _i64), ("dtype", ctypes.c_int32), ("eps", _f32)]
+
+
 _cache_p, _rope_p, _i64_p = ctypes.POINTER(_Cache), ctypes.POINTER(_Rope), ctypes.POINTER(_i64)
+_norm_p = ctypes.POINTER(_Norm)
 
 _SIG = {
     "wht_batched": [_vp, _int, _vp, _int, _i64, _i64, _i64, _i64, _vp, _int, _int, _vp],
@@ -66,6 +71,14 @@ _SIG = {
     "qwha_adapter_forward_planned": [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _int, _i64, _i64, _vp, _i64,
                                      _vp, _int, _i64, _vp],
     "kv_append": [_cache_p, _vp, _i64_p, _vp, _i64_p, _int, _i64, _vp, _rope_p, _vp, _i64_p, _i64, _vp, _i64_p, _vp],
+    "kv_append_norm": [_cache_p, _vp, _i64_p, _vp, _i64_p, _int, _i64, _vp, _norm_p, _rope_p, _vp, _i64_p, _i64, _vp,
+                       _i64_p, _vp],
+    "qk_norm_rope": [_vp, _i64_p, _i64, _vp, _i64_p, _i64, _int, _i64, _i64, _norm_p, _rope_p, _vp, _i64_p, _vp, _i64_p,
+                     _vp],
+    "qk_norm_rope_backward": [_vp, _i64_p, _vp, _i64_p, _i64, _vp, _i64_p, _vp, _i64_p, _i64, _int, _i64, _i64, _norm_p,
+                              _rope_p, _vp, _i64_p, _vp, _i64_p, _vp, _vp, _vp, _i64, _vp],
+    "token_logprobs": [_vp, _int, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp],
+    "token_logprobs_backward": [_vp, _int, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
     "kv_gather": [_cache_p, _i64, _vp, _vp, _i64_p, _vp, _i64_p, _int, _vp],
     "kv_attention": [_cache_p, _vp, _i64_p, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32,
                      _int, _i64, _vp, _i64_p, _vp, _vp, _i64, _vp],
@@ -80,6 +93,10 @@ _lib.qwha_forward_plan_bytes.argtypes = [_i64, _i64, _i64, _i64]
 _lib.qwha_forward_plan_bytes.restype = _i64
 _lib.kv_attention_workspace_bytes.argtypes = [_cache_p, _i64, _i64, _i64, _i64, _i64, _i64]
 _lib.kv_attention_workspace_bytes.restype = _i64
+_lib.qk_norm_rope_backward_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _norm_p]
+_lib.qk_norm_rope_backward_workspace_bytes.restype = _i64
+_lib.token_logprobs_workspace_bytes.argtypes = [_i64, _i64, _i64]
+_lib.token_logprobs_workspace_bytes.restype = _i64
 _lib.whtq_status_string.argtypes = [_int]
 _lib.whtq_status_string.restype = ctypes.c_char_p
 _lib.whtq_last_hip_error.restype = _int
@@ -693,12 +710,16 @@ def _on_device(dev, f, *args):
 
 
 def _head_rows(name, t, cache, tokens, heads, dtype):
+    return _dense_rows(name, t, cache._dev, "the cache's", cache.dim, tokens, heads, dtype)
+
+
+def _dense_rows(name, t, dev, whose, dim, tokens, heads, dtype):
     """Strides of a [tokens, heads, dim] tensor with contiguous head vectors."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != cache._dev:
-        raise ValueError(f"{name} must be a tensor on the cache's device")
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on {whose} device")
     shape, st = t.shape, t.stride()
-    if len(shape) != 3 or shape[2] != cache.dim or st[2] != 1:
-        raise ValueError(f"{name} must be [tokens, heads, {cache.dim}] with a contiguous last dimension")
+    if len(shape) != 3 or shape[2] != dim or st[2] != 1:
+        raise ValueError(f"{name} must be [tokens, heads, {dim}] with a contiguous last dimension")
     if shape[0] != tokens or shape[1] != heads:
         raise ValueError(f"{name} must have {tokens} tokens and {heads} heads")
     if t.dtype is not dtype:
@@ -717,41 +738,71 @@ def _rows_dtype(name, t, cache):
     return dtype
 
 
-def _ints(name, t, dtype, dev, n):
+def _ints(name, t, dtype, dev, n, whose="the cache's"):
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.shape != (n,) or \
             not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on the cache's device")
+        raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on {whose} device")
     return t.data_ptr()
 
 
+def _rope_arg(cos, sin, positions, rot_dim, interleaved, tokens, dev, whose):
+    """The rotation of a call, or None without tables and positions."""
+    if cos is None and sin is None and positions is None:
+        return None
+    for nm, t in (("cos", cos), ("sin", sin)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.dim() != 2 or \
+                t.stride(1) != 1 or t.get_device() != dev:
+            raise ValueError(f"{nm} must be a float32 [positions, rot_dim / 2] tensor with a contiguous last "
+                             f"dimension on {whose} device")
+    rows, half = cos.shape
+    ld = cos.stride(0)
+    if sin.shape != cos.shape or sin.stride(0) != ld:
+        raise ValueError("cos and sin must have one shape and layout")
+    rot = 2 * half if rot_dim is None else int(rot_dim)
+    if rot > 2 * half:
+        raise ValueError("cos and sin must hold rot_dim / 2 entries a row")
+    return _Rope(cos.data_ptr(), sin.data_ptr(), _ints("positions", positions, torch.int32, dev, tokens, whose),
+                 ld if rows > 1 else -(-half // 4) * 4, rows, rot, 1 if interleaved else 0)
+
+
+def _norm_arg(q_norm, k_norm, eps, heads, kv_heads, dim, dev, whose):
+    """The norms of a call: weights [dim], or [heads, dim] for one a head."""
+    n = _Norm(eps=eps)
+    for nm, t, h in (("q_norm", q_norm, heads), ("k_norm", k_norm, kv_heads)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+            raise ValueError(f"{nm} must be a float32, bfloat16 or float16 tensor on {whose} device")
+        shape, st = t.shape, t.stride()
+        if (shape != (dim,) and shape != (h, dim)) or st[-1] != 1:
+            raise ValueError(f"{nm} must be [{dim}] or [{h}, {dim}] with a contiguous last dimension")
+        if q_norm is not None and k_norm is not None and q_norm.dtype is not k_norm.dtype:
+            raise ValueError("q_norm and k_norm must have one dtype")
+        n.dtype = _DT[t.dtype]
+        # (a stride of 0 would say that all heads share one vector)
+        head = 0 if len(shape) == 1 else st[0] if h > 1 else dim
+        if nm == "q_norm":
+            n.q, n.q_head = t.data_ptr(), head
+        else:
+            n.k, n.k_head = t.data_ptr(), head
+    return n
+
+
 def kv_append(cache, k, v, slots, *, q=None, cos=None, sin=None, positions=None, rot_dim=None, interleaved=False,
-              q_out=None):
+              q_out=None, q_norm=None, k_norm=None, norm_eps=1e-6):
     """Rotates new keys (and queries) by their positions and writes keys and
     values [tokens, kv_heads, dim] into the cache's slots (int64 [tokens];
     outside the cache: not written).  cos, sin: float32 [positions, rot_dim /
-    2] tables, or None for no rotation; positions: int32 [tokens].  Returns
-    the rotated queries (q_out, q's shape; q_out=q rotates in place)."""
+    2] tables, or None for no rotation; positions: int32 [tokens].  q_norm,
+    k_norm: weights of norms of each head vector before the rotation, [dim] or
+    [heads, dim] (x / sqrt(mean x^2 + norm_eps) * weight; None: no norm).
+    Returns the rotated queries (q_out, q's shape; q_out=q rotates in place)."""
     dtype = _rows_dtype("k", k, cache)
     tokens, dev = k.shape[0], cache._dev
     ks = _head_rows("k", k, cache, tokens, cache.kv_heads, dtype)
     vs = _head_rows("v", v, cache, tokens, cache.kv_heads, dtype)
     slots_p = _ints("slots", slots, torch.int64, dev, tokens)
-    rope = None
-    if cos is not None or sin is not None or positions is not None:
-        for nm, t in (("cos", cos), ("sin", sin)):
-            if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.dim() != 2 or \
-                    t.stride(1) != 1 or t.get_device() != dev:
-                raise ValueError(f"{nm} must be a float32 [positions, rot_dim / 2] tensor with a contiguous last "
-                                 "dimension on the cache's device")
-        rows, half = cos.shape
-        ld = cos.stride(0)
-        if sin.shape != cos.shape or sin.stride(0) != ld:
-            raise ValueError("cos and sin must have one shape and layout")
-        rot = 2 * half if rot_dim is None else int(rot_dim)
-        if rot > 2 * half:
-            raise ValueError("cos and sin must hold rot_dim / 2 entries a row")
-        rope = _Rope(cos.data_ptr(), sin.data_ptr(), _ints("positions", positions, torch.int32, dev, tokens),
-                     ld if rows > 1 else -(-half // 4) * 4, rows, rot, 1 if interleaved else 0)
+    rope = _rope_arg(cos, sin, positions, rot_dim, interleaved, tokens, dev, "the cache's")
     qs = qos = q_p = qo_p = None
     heads = 0
     if q is not None:
@@ -763,9 +814,96 @@ def kv_append(cache, k, v, slots, *, q=None, cos=None, sin=None, positions=None,
         q_p, qo_p = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _check("kv_append", _on_device(dev, _lib.kv_append, cache._c, k.data_ptr(), ks, v.data_ptr(), vs, _DT[dtype], tokens,
-                                   slots_p, rope, q_p, qs, heads, qo_p, qos))
+    if q_norm is None and k_norm is None:
+        _check("kv_append", _on_device(dev, _lib.kv_append, cache._c, k.data_ptr(), ks, v.data_ptr(), vs, _DT[dtype],
+                                       tokens, slots_p, rope, q_p, qs, heads, qo_p, qos))
+        return q_out
+    if q is None and q_norm is not None:
+        raise ValueError("q_norm needs q")
+    norm = _norm_arg(q_norm, k_norm, norm_eps, heads, cache.kv_heads, cache.dim, dev, "the cache's")
+    _check("kv_append_norm", _on_device(dev, _lib.kv_append_norm, cache._c, k.data_ptr(), ks, v.data_ptr(), vs, _DT[dtype],
+                                        tokens, slots_p, norm, rope, q_p, qs, heads, qo_p, qos))
     return q_out
+
+
+def _qk_call(q, k, q_norm, k_norm, norm_eps, cos, sin, positions, rot_dim, interleaved):
+    """What qk_norm_rope and its backward pass have in common: sizes, strides, norms and rotation."""
+    for nm, t in (("q", q), ("k", k)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.get_device() < 0:
+            raise ValueError(f"{nm} must be a [tokens, heads, dim] device tensor")
+    dtype, dev = q.dtype, q.get_device()
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be bfloat16 or float16")
+    tokens, heads, dim = q.shape
+    kv_heads = k.shape[1]
+    if q_norm is None or k_norm is None:
+        raise ValueError("q_norm and k_norm must be given")
+    rows = lambda name, t, h: _dense_rows(name, t, dev, "q's", dim, tokens, h, dtype)
+    norm = _norm_arg(q_norm, k_norm, norm_eps, heads, kv_heads, dim, dev, "q's")
+    rope = _rope_arg(cos, sin, positions, rot_dim, interleaved, tokens, dev, "q's")
+    return dtype, dev, tokens, heads, kv_heads, dim, rows, rows("q", q, heads), rows("k", k, kv_heads), norm, rope
+
+
+def qk_norm_rope(q, k, *, q_norm, k_norm, norm_eps=1e-6, cos=None, sin=None, positions=None, rot_dim=None,
+                 interleaved=False, q_out=None, k_out=None):
+    """Norms of each head vector of q [tokens, heads, dim] and k [tokens,
+    kv_heads, dim] with weights [dim] or [heads, dim], then their rotation, as
+    in kv_append, into dense rows.  Returns (q_out, k_out); q_out=q and k_out=k
+    work in place."""
+    dtype, dev, tokens, heads, kv_heads, dim, rows, qs, ks, norm, rope = _qk_call(
+        q, k, q_norm, k_norm, norm_eps, cos, sin, positions, rot_dim, interleaved)
+    q_out = torch.empty(q.shape, dtype=dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=dtype, device=q.device) if k_out is None else k_out
+    qos, kos = rows("q_out", q_out, heads), rows("k_out", k_out, kv_heads)
+    _check("qk_norm_rope", _on_device(dev, _lib.qk_norm_rope, q.data_ptr(), qs, heads, k.data_ptr(), ks, kv_heads,
+                                      _DT[dtype], dim, tokens, norm, rope, q_out.data_ptr(), qos, k_out.data_ptr(), kos))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, *, q_norm, k_norm, norm_eps=1e-6, cos=None, sin=None, positions=None,
+                          rot_dim=None, interleaved=False, dq=None, dk=None, workspace=None):
+    """The gradients of qk_norm_rope's inputs from those of its outputs and the
+    same inputs: (dq, dk, dq_norm, dk_norm), the weights' in float32 and their
+    shape.  dq and dk may be any rows of q's and k's shapes, dq_out and dk_out
+    among them.  workspace: a tensor of qk_norm_rope_backward_workspace_bytes,
+    allocated here if not given."""
+    dtype, dev, tokens, heads, kv_heads, dim, rows, qs, ks, norm, rope = _qk_call(
+        q, k, q_norm, k_norm, norm_eps, cos, sin, positions, rot_dim, interleaved)
+    for nm, t in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) == 0:
+            raise ValueError(f"{nm} is one vector expanded over the heads: pass it as [dim], its gradient is one vector too")
+    dqos, dkos = rows("dq_out", dq_out, heads), rows("dk_out", dk_out, kv_heads)
+    dq = torch.empty(q.shape, dtype=dtype, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=dtype, device=q.device) if dk is None else dk
+    dqs, dks = rows("dq", dq, heads), rows("dk", dk, kv_heads)
+    dwq = torch.empty(q_norm.shape, dtype=torch.float32, device=q.device)
+    dwk = torch.empty(k_norm.shape, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        need = _on_device(dev, lambda *a: _lib.qk_norm_rope_backward_workspace_bytes(*a[:-1]), heads, kv_heads, dim, tokens,
+                          norm)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_p, wbytes = _workspace(workspace, dev, "q's")
+    _check("qk_norm_rope_backward", _on_device(
+        dev, _lib.qk_norm_rope_backward, dq_out.data_ptr(), dqos, q.data_ptr(), qs, heads, dk_out.data_ptr(), dkos,
+        k.data_ptr(), ks, kv_heads, _DT[dtype], dim, tokens, norm, rope, dq.data_ptr(), dqs, dk.data_ptr(), dks,
+        dwq.data_ptr(), dwk.data_ptr(), ws_p, wbytes))
+    return dq, dk, dwq, dwk
+
+
+def qk_norm_rope_backward_workspace_bytes(q, k, *, q_norm, k_norm):
+    norm = _norm_arg(q_norm, k_norm, 0.0, q.shape[1], k.shape[1], q.shape[2], q.get_device(), "q's")
+    with torch.cuda.device(q.device):
+        return int(_lib.qk_norm_rope_backward_workspace_bytes(q.shape[1], k.shape[1], q.shape[2], q.shape[0], norm))
+
+
+def _workspace(t, dev, whose):
+    """(address, bytes) of a workspace tensor or None."""
+    if t is None:
+        return 0, 0
+    if not isinstance(t, torch.Tensor) or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"workspace must be a contiguous tensor on {whose} device")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def kv_gather(cache, slots, *, dtype=None, k_out=None, v_out=None):
@@ -836,15 +974,98 @@ def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_le
                           max_q_len, max_kv_len, window)
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.get_device() != dev:
-        raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    ws_p = wbytes = 0
-    if workspace is not None:
-        ws_p, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    ws_p, wbytes = _workspace(workspace, dev, "the cache's")
     _check("kv_attention", _on_device(
         dev, _lib.kv_attention, cache._c, q.data_ptr(), qs, _DT[dtype], tokens, heads, seqs, start_p, kv_p,
         block_table.data_ptr(), ts if seqs > 1 else width, width, max_q_len, max_kv_len,
         cache._scale if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), outs, lse_p, ws_p, wbytes))
+    return out
+
+
+class TokenLogprobs(NamedTuple):
+    """Of rows of logits: float32 [rows] logprob (None without targets), lse
+    and entropy; top_logprob float32 and top_id int64 [rows, top] (None for top
+    = 0).  lse_low is what rounding lse to float32 dropped, for the gradient."""
+    logprob: Optional[torch.Tensor]
+    lse: torch.Tensor
+    entropy: torch.Tensor
+    top_logprob: Optional[torch.Tensor]
+    top_id: Optional[torch.Tensor]
+    lse_low: torch.Tensor
+
+
+def _logits(name, t, dev=None, shape=None):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.get_device() < 0 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a [rows, vocab] device tensor with a contiguous last dimension")
+    if t.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    if dev is not None and (t.get_device() != dev or t.shape != shape):
+        raise ValueError(f"{name} must have the logits' shape and device")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _row_floats(name, t, rows, dev):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != (rows,) or not t.is_contiguous() or \
+            t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous float32 [{rows}] tensor on the logits' device")
+    return t.data_ptr()
+
+
+def token_logprobs_workspace_bytes(rows, vocab, top=0, device="cuda"):
+    with torch.cuda.device(device):
+        return int(_lib.token_logprobs_workspace_bytes(rows, vocab, top))
+
+
+def token_logprobs(logits, targets=None, *, top=0, scale=1.0, workspace=None):
+    """Log probabilities under softmax(scale * logits) of logits [rows, vocab]:
+    of targets (int64 [rows]; one outside the vocabulary gives 0), the `top`
+    likeliest tokens of each row (equal logits: the lower index first) and the
+    entropy, in one pass.  workspace: a tensor of
+    token_logprobs_workspace_bytes, allocated here if not given.  Returns
+    TokenLogprobs."""
+    ld = _logits("logits", logits)
+    (rows, vocab), dev = logits.shape, logits.get_device()
+    t_p = lp_p = None
+    out = torch.empty((4, rows), dtype=torch.float32, device=logits.device)
+    lse, low, entropy, logprob = out.unbind(0)
+    if targets is not None:
+        t_p, lp_p = _ints("targets", targets, torch.int64, dev, rows, "the logits'"), logprob.data_ptr()
+    else:
+        logprob = None
+    top_logprob = top_id = None
+    if top > 0:
+        top_logprob = torch.empty((rows, top), dtype=torch.float32, device=logits.device)
+        top_id = torch.empty((rows, top), dtype=torch.int64, device=logits.device)
+    if workspace is None:
+        need = _on_device(dev, lambda *a: _lib.token_logprobs_workspace_bytes(*a[:-1]), rows, vocab, top)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+    ws_p, wbytes = _workspace(workspace, dev, "the logits'")
+    _check("token_logprobs", _on_device(
+        dev, _lib.token_logprobs, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p, lp_p, lse.data_ptr(),
+        low.data_ptr(), entropy.data_ptr(), top, top_logprob.data_ptr() if top > 0 else None,
+        top_id.data_ptr() if top > 0 else None, ws_p, wbytes))
+    return TokenLogprobs(logprob, lse, entropy, top_logprob, top_id, low)
+
+
+def token_logprobs_backward(logits, targets, result, dlogprob=None, dentropy=None, *, scale=1.0, out=None):
+    """The gradient of the logits for float32 [rows] gradients of `result`'s
+    logprob and entropy (either may be None), `result` being token_logprobs's of
+    the same logits, targets and scale.  out: a tensor of the logits' shape and
+    type (out=logits works in place)."""
+    ld = _logits("logits", logits)
+    (rows, vocab), dev = logits.shape, logits.get_device()
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    ldd = _logits("out", out, dev, logits.shape)
+    if out.dtype is not logits.dtype:
+        raise ValueError("out must have the logits' dtype")
+    t_p = _ints("targets", targets, torch.int64, dev, rows, "the logits'") if targets is not None else None
+    of = lambda name, t: _row_floats(name, t, rows, dev) if t is not None else None
+    _check("token_logprobs_backward", _on_device(
+        dev, _lib.token_logprobs_backward, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p,
+        of("result.lse", result.lse), of("result.lse_low", result.lse_low), of("result.entropy", result.entropy),
+        of("dlogprob", dlogprob), of("dentropy", dentropy), out.data_ptr(), ldd))
     return out
 
 
