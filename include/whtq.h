@@ -681,6 +681,27 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
                          int64_t workspace_bytes, void* stream);
 
 /*
+ * kv_attention_sinks -- kv_attention under a window, with the first `sinks`
+ *   keys of each sequence visible as well: query i sees key j < kv_len with
+ *   j <= p (causal) and (j > p - window or j < sinks).  window 0 (all keys) or
+ *   sinks 0 is kv_attention.  Keys that no query of a sequence sees are not
+ *   part of the result whatever they hold, and pages between the sinks and the
+ *   windows may have gone to others: of their table entries and their pages
+ *   only whole tiles of keys at either end of the gap are read, and an entry
+ *   outside the cache reads page 0 as ever.  workspace: of
+ *   kv_attention_sinks_workspace_bytes(...).
+ */
+int64_t kv_attention_sinks_workspace_bytes(const whtq_kv_cache* cache, int64_t q_tokens, int64_t heads, int64_t seqs,
+                                           int64_t max_q_len, int64_t max_kv_len, int64_t window,
+                                           int64_t sinks); /* -1: invalid sizes or no device */
+whtq_status kv_attention_sinks(const whtq_kv_cache* cache, const void* q, const int64_t* q_stride, whtq_dtype dtype,
+                               int64_t q_tokens, int64_t heads, int64_t seqs, const int32_t* q_start,
+                               const int32_t* kv_len, const int32_t* block_table, int64_t table_stride,
+                               int64_t table_width, int64_t max_q_len, int64_t max_kv_len, float scale, int causal,
+                               int64_t window, int64_t sinks, void* out, const int64_t* out_stride, float* lse,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * ---- Log probabilities.  How far a quantised model or an adapter is from
  * the original is judged by the log probabilities that it gives to a text,
  * and an adapter trains on them.

@@ -5,7 +5,8 @@ Rotary positions: a pair (a, b) of a head vector at position p becomes
 or, interleaved, (2i, 2i + 1) of the first r coordinates.
 
 Attention: query i of a chunk of n over kv keys sits at p = kv - n + i and sees
-key j < kv when (not causal or j <= p) and (window == 0 or j > p - window);
+key j < kv when (not causal or j <= p) and (window == 0 or j > p - window or
+j < sinks);
 out = sum_j softmax_j(scale q.k_j) v_j over the keys it sees, 0 if none, and
 lse = log sum_j exp(scale q.k_j), -inf if none.  A key that is not seen takes
 no part at all, whatever it holds.
@@ -25,18 +26,18 @@ def rotate(x, cos, sin, interleaved=False):
     return y
 
 
-def sees(kv, n, i, j, causal, window):
+def sees(kv, n, i, j, causal, window, sinks=0):
     p = kv - n + i
-    return j < kv and (not causal or j <= p) and (window == 0 or j > p - window)
+    return j < kv and (not causal or j <= p) and (window == 0 or j > p - window or j < sinks)
 
 
-def attention(q, k, v, scale, causal=True, window=0):
+def attention(q, k, v, scale, causal=True, window=0, sinks=0):
     """q [n, H, D], k and v [kv, G, D]; returns out [n, H, D], lse [n, H]."""
     n, heads, d = q.shape
     kv, kvh = k.shape[:2]
     out, lse = np.zeros((n, heads, d)), np.full((n, heads), -np.inf)
     for i in range(n):
-        js = [j for j in range(kv) if sees(kv, n, i, j, causal, window)]
+        js = [j for j in range(kv) if sees(kv, n, i, j, causal, window, sinks)]
         if not js:
             continue
         for h in range(heads):

@@ -146,3 +146,15 @@ def test_logprob_gradient_rules():
     assert grad(dx=P + 1) == EALIGN
     assert grad(g=P + 2) == EALIGN
     assert grad(t=None, g=None, rows=0) == OK
+
+
+def test_sinks_rules():
+    def attend(sinks, window=4, ws=None, wb=0, out=2 * P, n=3):
+        return L.kv_attention_sinks(cache(), P, st(256, 64), W.BF16, n, 4, 1, P, P, P, 8, 8, 3, 100, 0.1, 1, window, sinks, out,
+                                    st(256, 64), None, ws, wb, None)
+    assert attend(-1) == EINVAL
+    assert attend(4, window=-1) == EINVAL
+    assert attend(4, out=P) == EINVAL
+    assert attend(4, ws=P + 8) == EALIGN
+    assert attend(4, n=0) == OK
+    assert L.kv_attention_sinks_workspace_bytes(cache(), 3, 4, 1, 3, 100, 4, -1) == -1

@@ -68,3 +68,13 @@ def test_logprobs_gradient(scale):
     x[:, 5] = -np.inf
     d = lm.logprobs_backward(x, t, g, h, scale)
     assert np.isfinite(d).all() and (d[:, 5] == 0).all()
+
+
+def test_sinks_by_hand():
+    """Position 5 under a window of 2 with 3 sinks sees 0, 1, 2, 4 and 5; equal scores: the mean of their values."""
+    from oracle import kv as K
+    v = np.arange(6.0)[:, None, None] ** 2
+    out, lse = K.attention(np.zeros((1, 1, 1)), np.ones((6, 1, 1)), v, 1.0, True, 2, 3)
+    assert np.isclose(out[0, 0, 0], (0 + 1 + 4 + 16 + 25) / 5) and np.isclose(lse[0, 0], np.log(5))
+    assert [j for j in range(6) if K.sees(6, 4, 0, j, True, 1, 2)] == [0, 1, 2]
+    assert [j for j in range(6) if K.sees(6, 4, 0, j, False, 1, 1)] == [0, 2, 3, 4, 5]

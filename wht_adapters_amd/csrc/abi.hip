@@ -824,8 +824,11 @@ struct KvPlan {
 };
 
 KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t seqs, int64_t max_q, int64_t max_kv,
-               int64_t window, int cus) {
+               int64_t window, int64_t sinks, int cus) {
   KvPlan p{};
+  // sinks and window, and a tile's rounding of each: the keys of a step, whatever the length (without sinks the
+  // step's blocks are planned for max_kv, as they were)
+  if (sinks > 0) max_kv = std::min(max_kv, std::min(window, kMost) + std::min(sinks, kMost) + max_q + 128);
   const int64_t group = heads / c->kv_heads, kvh = c->kv_heads;
   const bool int4 = c->format == WHTQ_KV_INT4;
   p.splits = 1;
@@ -876,7 +879,7 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
     // tokens each, 121 us against 180 counting a tile for each; 128 of 1000 to
     // 1500: 152 and 127)
     const int64_t blocks = (q_tokens * group + rows - 1) / rows * kvh;
-    const int64_t keys = window > 0 ? std::min(max_kv, std::min(window, kMost) + rows / group + 64) : max_kv;
+    const int64_t keys = window > 0 ? std::min(max_kv, std::min(window, kMost) + std::min(sinks, kMost) + rows / group + 64) : max_kv;
     // split the keys of a block's rows where that shortens the longest chain
     // of tiles a slot works off; the joining kernel costs about 8 tiles' time
     // (16-bit pages, 512 tokens over 33000 keys: 328 us against 626 unsplit and
@@ -977,12 +980,17 @@ whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t*
 
 int64_t kv_attention_workspace_bytes(const whtq_kv_cache* cache, int64_t q_tokens, int64_t heads, int64_t seqs,
                                      int64_t max_q_len, int64_t max_kv_len, int64_t window) {
+  return kv_attention_sinks_workspace_bytes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window, 0);
+}
+
+int64_t kv_attention_sinks_workspace_bytes(const whtq_kv_cache* cache, int64_t q_tokens, int64_t heads, int64_t seqs,
+                                           int64_t max_q_len, int64_t max_kv_len, int64_t window, int64_t sinks) {
   KvCache c;
   if (kv_check(cache, &c) != WHTQ_OK) return -1;
   if (kv_attn_sizes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len) != WHTQ_OK) return -1;
-  if (window < 0 || need_device() != WHTQ_OK) return -1;
+  if (window < 0 || sinks < 0 || need_device() != WHTQ_OK) return -1;
   if (q_tokens == 0 || seqs == 0) return 0;
-  return kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window, kv_cus()).bytes;
+  return kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window, window > 0 ? sinks : 0, kv_cus()).bytes;
 }
 
 whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_t* q_stride, whtq_dtype dtype,
@@ -991,13 +999,24 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
                          int64_t table_width, int64_t max_q_len, int64_t max_kv_len, float scale, int causal,
                          int64_t window, void* out, const int64_t* out_stride, float* lse, void* workspace,
                          int64_t workspace_bytes, void* stream) {
+  return kv_attention_sinks(cache, q, q_stride, dtype, q_tokens, heads, seqs, q_start, kv_len, block_table, table_stride,
+                            table_width, max_q_len, max_kv_len, scale, causal, window, 0, out, out_stride, lse, workspace,
+                            workspace_bytes, stream);
+}
+
+whtq_status kv_attention_sinks(const whtq_kv_cache* cache, const void* q, const int64_t* q_stride, whtq_dtype dtype,
+                               int64_t q_tokens, int64_t heads, int64_t seqs, const int32_t* q_start,
+                               const int32_t* kv_len, const int32_t* block_table, int64_t table_stride,
+                               int64_t table_width, int64_t max_q_len, int64_t max_kv_len, float scale, int causal,
+                               int64_t window, int64_t sinks, void* out, const int64_t* out_stride, float* lse,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
   KvAttnArgs a{};
   whtq_status st = kv_check(cache, &a.c);
   if (st != WHTQ_OK) return st;
   st = kv_attn_sizes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len);
   if (st != WHTQ_OK) return st;
   if (!kv_dtype(dtype) || (cache->format == WHTQ_KV_DENSE && dtype != cache->dtype)) return WHTQ_EINVAL;
-  if ((causal != 0 && causal != 1) || window < 0 || !std::isfinite(scale) || workspace_bytes < 0) return WHTQ_EINVAL;
+  if ((causal != 0 && causal != 1) || window < 0 || sinks < 0 || !std::isfinite(scale) || workspace_bytes < 0) return WHTQ_EINVAL;
   if (table_width < 0 || table_stride < table_width) return WHTQ_EINVAL;
   if (!kv_rows_valid(q_stride) || !kv_rows_valid(out_stride)) return WHTQ_EINVAL;
   const bool any = q_tokens > 0 && seqs > 0;
@@ -1009,7 +1028,8 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   if (!any) return WHTQ_OK;
   st = need_device();
   if (st != WHTQ_OK) return st;
-  const KvPlan p = kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window, kv_cus());
+  if (window == 0) sinks = 0;  // every key is seen
+  const KvPlan p = kv_plan(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window, sinks, kv_cus());
   if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return WHTQ_EINVAL;
   if (p.grid > INT32_MAX) return WHTQ_EUNSUPPORTED;
   a.q = (const uint8_t*)q;
@@ -1030,6 +1050,7 @@ whtq_status kv_attention(const whtq_kv_cache* cache, const void* q, const int64_
   a.seqs = (int)seqs;
   a.causal = causal;
   a.window = (int)std::min(window, kMost);
+  a.sinks = (int)std::min(sinks, kMost);
   a.splits = p.splits;
   a.grid = (int)p.grid;
   a.scale = scale * 1.4426950408889634f;

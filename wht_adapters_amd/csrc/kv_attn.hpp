@@ -31,6 +31,7 @@ struct KvAttnArgs {
   int blocks, rows;        // step kernel: runs a head (0: a block per sequence), rows of a sequence and head (max_q_len * group)
   int launched;            // blocks (chunk kernel) or sequences (joining of steps) in the launches before this one
   float scale;  // times log2(e)
+  int sinks;    // > 0 only with a window
 };
 
 constexpr float KV_NEG_INF = -__builtin_huge_valf();
@@ -63,6 +64,19 @@ __device__ __forceinline__ int kv_page(const KvAttnArgs& a, int entry) {
 // 2^30 keys: sums of a position, a window and a tile stay inside 32 bits.
 __device__ __forceinline__ int kv_held(const KvAttnArgs& a, int len) {
   return max(0, min(len, (int)min<int64_t>((int64_t)a.table_width << a.c.page_shift, 1 << 30)));
+}
+
+// The walk over tiles of TK keys of queries that see the first `sinks` keys
+// beside those from `first` on: `tiles` tiles hold the sinks, and the tile of
+// `first` is `gap` further than the one behind them.  Sinks that reach that
+// tile leave no gap.
+struct KvNear {
+  int tiles, gap;
+};
+template <int TK>
+__device__ __forceinline__ KvNear kv_near(int sinks, int first) {
+  const int far = first / TK, near = min((min(sinks, first) + TK - 1) / TK, far);
+  return {near, far - near};
 }
 
 template <int T>

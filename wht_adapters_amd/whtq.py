@@ -71,6 +71,8 @@ _SIG = {
     "qwha_adapter_forward_planned": [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _int, _i64, _i64, _vp, _i64,
                                      _vp, _int, _i64, _vp],
     "kv_append": [_cache_p, _vp, _i64_p, _vp, _i64_p, _int, _i64, _vp, _rope_p, _vp, _i64_p, _i64, _vp, _i64_p, _vp],
+    "kv_attention_sinks": [_cache_p, _vp, _i64_p, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32,
+                           _int, _i64, _i64, _vp, _i64_p, _vp, _vp, _i64, _vp],
     "kv_append_norm": [_cache_p, _vp, _i64_p, _vp, _i64_p, _int, _i64, _vp, _norm_p, _rope_p, _vp, _i64_p, _i64, _vp,
                        _i64_p, _vp],
     "qk_norm_rope": [_vp, _i64_p, _i64, _vp, _i64_p, _i64, _int, _i64, _i64, _norm_p, _rope_p, _vp, _i64_p, _vp, _i64_p,
@@ -93,6 +95,8 @@ _lib.qwha_forward_plan_bytes.argtypes = [_i64, _i64, _i64, _i64]
 _lib.qwha_forward_plan_bytes.restype = _i64
 _lib.kv_attention_workspace_bytes.argtypes = [_cache_p, _i64, _i64, _i64, _i64, _i64, _i64]
 _lib.kv_attention_workspace_bytes.restype = _i64
+_lib.kv_attention_sinks_workspace_bytes.argtypes = [_cache_p, _i64, _i64, _i64, _i64, _i64, _i64, _i64]
+_lib.kv_attention_sinks_workspace_bytes.restype = _i64
 _lib.qk_norm_rope_backward_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _norm_p]
 _lib.qk_norm_rope_backward_workspace_bytes.restype = _i64
 _lib.token_logprobs_workspace_bytes.argtypes = [_i64, _i64, _i64]
@@ -929,19 +933,20 @@ def kv_gather(cache, slots, *, dtype=None, k_out=None, v_out=None):
     return k_out, v_out
 
 
-def kv_attention_workspace_bytes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window=0):
+def kv_attention_workspace_bytes(cache, q_tokens, heads, seqs, max_q_len, max_kv_len, window=0, sinks=0):
     with torch.cuda.device(cache._dev):
-        return int(_lib.kv_attention_workspace_bytes(cache._c, q_tokens, heads, seqs, max_q_len, max_kv_len, window))
+        return int(_lib.kv_attention_sinks_workspace_bytes(cache._c, q_tokens, heads, seqs, max_q_len, max_kv_len, window,
+                                                           sinks))
 
 
-def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_len, scale=None, causal=True, window=0,
+def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_len, scale=None, causal=True, window=0, sinks=0,
                  out=None, lse=None, workspace=None):
     """Attention of new tokens q [tokens, heads, dim] over their sequences'
     pages.  q_start: int32 [seqs + 1]; kv_len: int32 [seqs] (keys, the new
     tokens' included); block_table: int32 [seqs, width].  max_q_len and
     max_kv_len bound the lengths (host numbers).  scale: 1 / sqrt(dim) by
-    default; window: 0, or how many of the latest keys a query sees.  lse: a
-    float32 [tokens, heads] tensor to fill.  workspace: a uint8 tensor of
+    default; window: 0, or how many of the latest keys a query sees; sinks: how
+    many of a sequence's first keys it sees as well.  lse: a float32 [tokens, heads] tensor to fill.  workspace: a uint8 tensor of
     kv_attention_workspace_bytes, allocated here if not given."""
     dtype = _rows_dtype("q", q, cache)
     dev = cache._dev
@@ -970,15 +975,15 @@ def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_le
             raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor on the cache's device")
         lse_p = lse.data_ptr()
     if workspace is None:
-        need = _on_device(dev, lambda *a: _lib.kv_attention_workspace_bytes(*a[:-1]), cache._c, tokens, heads, seqs,
-                          max_q_len, max_kv_len, window)
+        need = _on_device(dev, lambda *a: _lib.kv_attention_sinks_workspace_bytes(*a[:-1]), cache._c, tokens, heads, seqs,
+                          max_q_len, max_kv_len, window, sinks)
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_p, wbytes = _workspace(workspace, dev, "the cache's")
     _check("kv_attention", _on_device(
-        dev, _lib.kv_attention, cache._c, q.data_ptr(), qs, _DT[dtype], tokens, heads, seqs, start_p, kv_p,
+        dev, _lib.kv_attention_sinks, cache._c, q.data_ptr(), qs, _DT[dtype], tokens, heads, seqs, start_p, kv_p,
         block_table.data_ptr(), ts if seqs > 1 else width, width, max_q_len, max_kv_len,
-        cache._scale if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), outs, lse_p, ws_p, wbytes))
+        cache._scale if scale is None else scale, 1 if causal else 0, window, sinks, out.data_ptr(), outs, lse_p, ws_p, wbytes))
     return out
 
 
