@@ -709,15 +709,17 @@ whtq_status kv_attention_sinks(const whtq_kv_cache* cache, const void* q, const 
  * token_logprobs -- for rows of `vocab` logits x (fp32, bf16 or fp16, row
  *   stride ld in elements, no alignment beyond an element's), z = scale x
  *   (scale > 0: 1 / temperature) and p = softmax(z):
- *     lse = log sum e^z             (lse_low: what rounding it to fp32 dropped)
+ *     lse = log sum e^z
  *     logprob = z[targets[row]] - lse   (a target outside [0, vocab): 0)
  *     entropy = -sum p log p
  *     top_id, top_logprob [rows][top]: the `top` largest logits, largest first,
  *       equal ones by index (the order is that of x), and their z - lse.
- *   Any of lse, lse_low, entropy may be NULL; targets and logprob both or
- *   neither.  top: 0 to WHTQ_TOP_MOST and at most vocab.  vocab: up to 2^20.
- *   Logits of -inf have probability 0 and take part in nothing else; a row of
- *   only those has lse = logprob = top_logprob = -inf and entropy 0.  A row
+ *     row_ref, row_sum: for the gradient, a logit m near the row's largest
+ *       and sum e^(scale (x - m)).
+ *   Any of lse, entropy may be NULL; targets and logprob both or neither, row_ref
+ *   and row_sum too.  top: 0 to WHTQ_TOP_MOST and at most vocab.  vocab: up to 2^20.
+ *   Logits of -inf have probability 0 and take part in nothing else (the
+ *   type's lowest value is a logit like any other); a row of only those has lse = logprob = top_logprob = -inf and entropy 0.  A row
  *   with a NaN or +inf gives NaN for lse, logprob, entropy and top_logprob (a
  *   NaN counts as -inf in the order of top_id).
  *   workspace: device memory of token_logprobs_workspace_bytes(...), 16-byte
@@ -726,7 +728,7 @@ whtq_status kv_attention_sinks(const whtq_kv_cache* cache, const void* q, const 
  * token_logprobs_backward -- the gradient of the logits for gradients
  *   dlogprob and dentropy (fp32 [rows]; either may be NULL, not both),
  *     dlogits = scale (dlogprob (onehot - p) - dentropy p (log p + entropy)),
- *   rounded once to the logits' type.  lse, lse_low (NULL: 0) and entropy (for
+ *   rounded once to the logits' type.  row_ref, row_sum and entropy (for
  *   dentropy) are token_logprobs's of the same logits and scale.  A target
  *   outside [0, vocab) makes its row's dlogprob count as 0, whatever it holds.
  *   A row of only -inf gets zeros.  dlogits == logits (equal strides) is
@@ -736,11 +738,11 @@ whtq_status kv_attention_sinks(const whtq_kv_cache* cache, const void* q, const 
 
 int64_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top); /* -1: invalid sizes or no device */
 whtq_status token_logprobs(const void* logits, whtq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld, float scale,
-                           const int64_t* targets, float* logprob, float* lse, float* lse_low, float* entropy,
-                           int64_t top, float* top_logprob, int64_t* top_id, void* workspace, int64_t workspace_bytes,
+                           const int64_t* targets, float* logprob, float* lse, float* row_ref, float* row_sum,
+                           float* entropy, int64_t top, float* top_logprob, int64_t* top_id, void* workspace, int64_t workspace_bytes,
                            void* stream);
 whtq_status token_logprobs_backward(const void* logits, whtq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
-                                    float scale, const int64_t* targets, const float* lse, const float* lse_low,
+                                    float scale, const int64_t* targets, const float* row_ref, const float* row_sum,
                                     const float* entropy, const float* dlogprob, const float* dentropy, void* dlogits,
                                     int64_t ldd, void* stream);
 

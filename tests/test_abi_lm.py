@@ -93,12 +93,12 @@ def test_backward_workspace_refuses():
     assert bytes_(4, 2, 64, 3, None) == -1
 
 
-def logp(x=P, dt=W.BF16, rows=2, vocab=100, ld=100, scale=1.0, t=P, lp=P, top=0, tl=None, ti=None, ws=None, wb=0, ent=P):
-    return L.token_logprobs(x, dt, rows, vocab, ld, scale, t, lp, P, P, ent, top, tl, ti, ws, wb, None)
+def logp(x=P, dt=W.BF16, rows=2, vocab=100, ld=100, scale=1.0, t=P, lp=P, top=0, tl=None, ti=None, ws=None, wb=0, ent=P, ref=P):
+    return L.token_logprobs(x, dt, rows, vocab, ld, scale, t, lp, P, ref, P, ent, top, tl, ti, ws, wb, None)
 
 
-def grad(x=P, dt=W.BF16, rows=2, vocab=100, ld=100, scale=1.0, t=P, lse=P, ent=P, g=P, h=P, dx=2 * P, ldd=100):
-    return L.token_logprobs_backward(x, dt, rows, vocab, ld, scale, t, lse, P, ent, g, h, dx, ldd, None)
+def grad(x=P, dt=W.BF16, rows=2, vocab=100, ld=100, scale=1.0, t=P, ref=P, ent=P, g=P, h=P, dx=2 * P, ldd=100):
+    return L.token_logprobs_backward(x, dt, rows, vocab, ld, scale, t, ref, P, ent, g, h, dx, ldd, None)
 
 
 @pytest.mark.parametrize("call", [logp, grad])
@@ -123,6 +123,7 @@ def test_logits_rules(call):
 def test_logprob_rules():
     assert logp(t=None) == EINVAL               # a place for it, and no targets
     assert logp(lp=None) == EINVAL
+    assert logp(ref=None) == EINVAL             # one of the gradient's two without the other
     assert logp(top=-1) == EINVAL
     assert logp(top=101, tl=P, ti=P) == EINVAL
     assert logp(top=33, tl=P, ti=P) == EUNSUP
@@ -139,7 +140,8 @@ def test_logprob_gradient_rules():
     assert grad(g=None, h=None) == EINVAL
     assert grad(t=None) == EINVAL
     assert grad(ent=None) == EINVAL
-    assert grad(lse=None) == EINVAL
+    assert grad(ref=None) == EINVAL
+    assert grad(ref=P + 2) == EALIGN
     assert grad(dx=None) == EINVAL
     assert grad(ldd=99) == EINVAL
     assert grad(dx=P, ldd=101) == EINVAL        # in place with another stride

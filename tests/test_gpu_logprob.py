@@ -61,9 +61,10 @@ def check(r, x, t, scale, top):
         ok = np.isfinite(ref)
         bound = rel + 4 * E32 * (np.abs(m) + size + np.abs(want["lse"]) + 20)
         assert np.all(np.abs(got - ref)[ok] <= bound[ok])
-    # lse and its low part together: only log S is rounded (and m scale, exactly, in fp64)
-    both = lse + host64(r.lse_low)
-    assert np.all(np.abs(both - want["lse"])[fine] <= (rel + 2 * E32 * (np.abs(want["lse"] - m) + 10))[fine])
+    # what the gradient takes: a logit near the largest, and the sum relative to it
+    ref, total = host64(r.row_ref), host64(r.row_sum)
+    assert np.all(np.abs(ref * scale - m)[fine] <= 6 * np.log(2) + 1e-6)
+    assert np.all(np.abs(ref * scale + np.log(np.where(fine, total, 1)) - want["lse"])[fine] <= (rel + 2 * E32)[fine])
     # log S - T / S, T relative like S with one rounding more a term
     assert np.all(np.abs(ent - want["entropy"])[fine] <= ((2 * rel + 8 * E32) * (1 + bar + 5 + np.abs(want["lse"] - m)))[fine])
     if top:
@@ -166,7 +167,7 @@ def test_gradient(W, dtype, rows, vocab, offset):
 
 
 def test_gradient_of_large_logits(W):
-    """Logits around 3000: lse alone is good to 2^-13 there, its low part carries the rest."""
+    """Logits around 3000: lse is good to 2^-13 there, the gradient does not go by it."""
     rng = np.random.default_rng(5)
     x = torch.from_numpy((rng.standard_normal((3, 2000)) * 2 + 3000).astype(np.float32))
     t = np.array([4, 5, 1999])
@@ -206,6 +207,42 @@ def test_rows_do_not_depend_on_the_call(W):
     assert torch.equal(one.top_id[0], a.top_id[77])
     rel, _ = slack(host64(x)[77:78], 1.0)
     assert abs(float(one.logprob[0]) - float(a.logprob[77])) <= 2 * rel[0] + 64 * E32
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("scale", [1.0, 0.5, 2.0])
+def test_masks_of_the_lowest_value(W, dtype, scale):
+    """Rows masked with the type's lowest value, in part, but for one token, and whole (uniform, like any row of equals)."""
+    rng = np.random.default_rng(11)
+    low = torch.finfo(dtype).min
+    x = torch.from_numpy(rng.standard_normal((4, 1500)).astype(np.float32)).to(dtype)
+    x[0, ::2] = low
+    x[1] = low
+    x[1, 77] = 1.0
+    x[2] = low
+    x[3, :-1] = -float("inf")
+    x[3, -1] = low
+    t = np.array([1, 77, 5, 1499])
+    td, ones = torch.from_numpy(t).to(DEV), torch.ones(4, device=DEV)
+    r = W.token_logprobs(x.to(DEV), td, top=3, scale=scale)
+    with np.errstate(over="ignore"):
+        # (in fp64 the lowest value is as good as -inf next to others, and a row of it alone as good as a row of 0)
+        y = host64(x)
+    y = np.where(y <= float(low), -np.inf, y)
+    y[2], y[3, -1] = 0.0, 0.0
+    want = lm.logprobs(y, t, scale, 3)
+    rel, _ = slack(y, scale)
+    # (twice the lowest bf16 or fp32 value is beyond fp32, which lse is given in: -inf there)
+    with np.errstate(over="ignore"):
+        assert float(r.lse[2]) == pytest.approx(float(np.float32(float(low) * scale + np.log(1500))), rel=2 * E32)
+    assert np.all(np.abs(host64(r.logprob) - want["logprob"]) <= rel + 64 * E32)
+    assert np.all(np.abs(host64(r.entropy) - want["entropy"]) <= (2 * rel + 8 * E32) * 24)
+    ids = r.top_id.cpu().numpy()
+    assert ids[0].tolist() == want["top_id"][0].tolist() and ids[1].tolist() == [77, 0, 1] and ids[2].tolist() == [0, 1, 2]
+    assert ids[3].tolist() == [1499, 0, 1]
+    got = host64(W.token_logprobs_backward(x.to(DEV), td, r, ones, ones, scale=scale))
+    wg = lm.logprobs_backward(y, t, np.ones(4), np.ones(4), scale)
+    assert np.all(np.abs(got - wg) <= U[dtype] * np.abs(wg) + TINY[dtype] + scale * (4 * rel[:, None] + 400 * E32) * (np.exp(np.maximum(y * scale - want["lse"][:, None], -700)) * 12 + E32))
 
 
 def test_nothing_to_do(W):

@@ -68,8 +68,8 @@ hipError_t launch_qi_refine(const float* g, int64_t n, const float* p, int64_t r
 
 hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const void* k,
                             const int64_t* ks, const void* v, const int64_t* vs, const int64_t* slots,
-                            int64_t capacity, const KvTurn& turn, const KvNorm& norm, const void* q,
-                            const int64_t* qs, int heads, void* qo, const int64_t* qos, hipStream_t s);
+                            int64_t capacity, const KvTurn& turn, const void* q, const int64_t* qs, int heads,
+                            void* qo, const int64_t* qos, hipStream_t s);
 hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const int64_t* slots,
                             int64_t capacity, void* ko, const int64_t* ks, void* vo, const int64_t* vs,
                             hipStream_t s);
@@ -78,7 +78,8 @@ hipError_t launch_kv_join(const KvAttnArgs& a, int dim, int dt, bool int4, hipSt
 hipError_t launch_kv_chunk(const KvAttnArgs& a, int dim, int dt, bool int4, int waves, hipStream_t s);
 int kv_step_unit(int dim, bool int4, bool whole);
 int64_t qk_norm_split(QkArgs& a, int dim, int cus);
-hipError_t launch_qk_norm(QkArgs a, int dim, int dt, hipStream_t s);
+hipError_t launch_qk_norm(const QkForwardArgs& a, const int (&heads)[3], int64_t tokens, int dim, int dt, bool int4,
+                          hipStream_t s);
 hipError_t launch_qk_norm_back(const QkArgs& a, int dim, int dt, hipStream_t s);
 hipError_t launch_lp(const LpArgs& a, int dt, hipStream_t s);
 hipError_t launch_lp_grad(const LpGradArgs& a, int dt, hipStream_t s);
@@ -785,6 +786,10 @@ whtq_status kv_check(const whtq_kv_cache* c, KvCache* out) {
 bool kv_rows_valid(const int64_t* st) { return st && st[0] >= 0 && st[1] >= 0; }
 bool kv_rows_aligned(const void* p, const int64_t* st) { return aligned16(p) && !((st[0] * 2) & 15) && !((st[1] * 2) & 15); }
 
+KvRows kv_rows_of(const void* p, const int64_t* st) {
+  return p ? KvRows{(const uint8_t*)p, st[0] * 2, st[1] * 2} : KvRows{};
+}
+
 // the rules of rotary positions for rows of dim values, but for alignment
 whtq_status kv_rope_check(const whtq_rope* r, int64_t dim, int64_t tokens) {
   if (!r) return WHTQ_OK;
@@ -951,10 +956,25 @@ whtq_status kv_append_norm(const whtq_kv_cache* cache, const void* k, const int6
   if (tokens == 0) return WHTQ_OK;
   st = need_device();
   if (st != WHTQ_OK) return st;
-  return hip_status(launch_kv_append(c, (int)cache->dim, dtype, cache->format == WHTQ_KV_INT4, tokens, k, k_stride, v,
-                                     v_stride, slots, cache->num_pages * cache->page_size, kv_turn_of(rope),
-                                     norm ? kv_norm_of(norm) : KvNorm{}, q, q_stride, q ? (int)heads : 0, q_out,
-                                     q_out_stride, (hipStream_t)stream));
+  const bool int4 = cache->format == WHTQ_KV_INT4;
+  const int64_t capacity = cache->num_pages * cache->page_size;
+  if (!norm || (!norm->q && !norm->k))
+    return hip_status(launch_kv_append(c, (int)cache->dim, dtype, int4, tokens, k, k_stride, v, v_stride, slots, capacity,
+                                       kv_turn_of(rope), q, q_stride, q ? (int)heads : 0, q_out, q_out_stride,
+                                       (hipStream_t)stream));
+  const KvNorm n = kv_norm_of(norm);
+  QkForwardArgs a{};
+  a.f[0] = {kv_rows_of(k, k_stride), {}, c.k, n.k, rope != nullptr, {}, 0, 0};
+  a.f[1] = {kv_rows_of(v, v_stride), {}, c.v, {}, false, {}, 0, 0};
+  if (q) a.f[2] = {kv_rows_of(q, q_stride), kv_rows_of(q_out, q_out_stride), {}, n.q, rope != nullptr, {}, 0, 0};
+  a.c = c;
+  a.slots = slots;
+  a.capacity = capacity;
+  a.turn = kv_turn_of(rope);
+  a.dt = n.dt;
+  a.eps = n.eps;
+  return hip_status(launch_qk_norm(a, {c.kv_heads, c.kv_heads, q ? (int)heads : 0}, tokens, (int)cache->dim, dtype, int4,
+                                   (hipStream_t)stream));
 }
 
 whtq_status kv_gather(const whtq_kv_cache* cache, int64_t tokens, const int64_t* slots, void* k_out,
@@ -1094,7 +1114,6 @@ whtq_status qk_check(int64_t heads, int64_t kv_heads, int dtype, int64_t dim, in
   if ((dim != 64 && dim != 128) || tokens > kMost || heads > 65535 || kv_heads > 65535) return WHTQ_EUNSUPPORTED;
   return WHTQ_OK;
 }
-KvRows qk_rows(const void* p, const int64_t* st) { return p ? KvRows{(const uint8_t*)p, st[0] * 2, st[1] * 2} : KvRows{}; }
 int qk_classes(int64_t heads, int64_t stride) { return heads == 0 ? 0 : stride ? (int)heads : 1; }
 bool qk_aligned(const void* p, const int64_t* st) { return !p || kv_rows_aligned(p, st); }
 
@@ -1117,14 +1136,13 @@ whtq_status qk_norm_rope(const void* q, const int64_t* q_stride, int64_t heads, 
   st = need_device();
   if (st != WHTQ_OK) return st;
   const KvNorm n = kv_norm_of(norm);
-  QkArgs a{};
-  a.q = {qk_rows(q, q_stride), qk_rows(q_out, q_out_stride), {}, {}, n.q, nullptr, (int)heads, 0, 0};
-  a.k = {qk_rows(k, k_stride), qk_rows(k_out, k_out_stride), {}, {}, n.k, nullptr, (int)kv_heads, 0, 0};
+  QkForwardArgs a{};
+  if (heads) a.f[0] = {kv_rows_of(q, q_stride), kv_rows_of(q_out, q_out_stride), {}, n.q, rope != nullptr, {}, 0, 0};
+  if (kv_heads) a.f[1] = {kv_rows_of(k, k_stride), kv_rows_of(k_out, k_out_stride), {}, n.k, rope != nullptr, {}, 0, 0};
   a.turn = kv_turn_of(rope);
-  a.tokens = tokens;
   a.dt = n.dt;
   a.eps = n.eps;
-  return hip_status(launch_qk_norm(a, (int)dim, dtype, (hipStream_t)stream));
+  return hip_status(launch_qk_norm(a, {(int)heads, (int)kv_heads, 0}, tokens, (int)dim, dtype, false, (hipStream_t)stream));
 }
 
 int64_t qk_norm_rope_backward_workspace_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t tokens,
@@ -1159,9 +1177,9 @@ whtq_status qk_norm_rope_backward(const void* dq_out, const int64_t* dq_out_stri
   if (st != WHTQ_OK) return st;
   const KvNorm n = kv_norm_of(norm);
   QkArgs a{};
-  a.q = {qk_rows(q, q_stride), {}, qk_rows(dq_out, dq_out_stride), qk_rows(dq, dq_stride), n.q, dq_norm, (int)heads,
+  a.q = {kv_rows_of(q, q_stride), kv_rows_of(dq_out, dq_out_stride), kv_rows_of(dq, dq_stride), n.q, dq_norm, (int)heads,
          qk_classes(heads, norm->q_head), 0};
-  a.k = {qk_rows(k, k_stride), {}, qk_rows(dk_out, dk_out_stride), qk_rows(dk, dk_stride), n.k, dk_norm, (int)kv_heads,
+  a.k = {kv_rows_of(k, k_stride), kv_rows_of(dk_out, dk_out_stride), kv_rows_of(dk, dk_stride), n.k, dk_norm, (int)kv_heads,
          qk_classes(kv_heads, norm->k_head), 0};
   a.turn = kv_turn_of(rope);
   a.tokens = tokens;
@@ -1197,14 +1215,14 @@ struct LpPlan {
 };
 LpPlan lp_plan(int64_t rows, int64_t vocab, int64_t top, int cus) {
   LpPlan p{};
-  const int64_t chunks = (vocab + LP_CHUNK - 1) / LP_CHUNK;
+  const int64_t chunks = (vocab + 7 + LP_CHUNK - 1) / LP_CHUNK;
   // as many blocks as the machine holds, at least one chunk a wave
   p.splits = (int)std::max<int64_t>(1, std::min(8 * (int64_t)cus / std::max<int64_t>(rows, 1), chunks / 4));
   if (top) {
     // groups enough that the last one's maximum leaves few candidates (64 and more of them, 512 at most but for
     // vocabularies above 262144), large enough that their maxima are few bytes
     p.width = vocab <= 4096 ? 8 : vocab <= 32768 ? 64 : LP_CHUNK;
-    p.groups = (int)((vocab + p.width - 1) / p.width);
+    p.groups = (int)((vocab + 7 + p.width - 1) / p.width);  // (7: a row may begin inside 16 bytes)
   }
   if (p.splits > 1 || top) p.parts = rows * p.splits * 3;
   p.bytes = (p.parts + rows * p.groups) * 4;
@@ -1222,16 +1240,16 @@ int64_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top)
 }
 
 whtq_status token_logprobs(const void* logits, whtq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld, float scale,
-                           const int64_t* targets, float* logprob, float* lse, float* lse_low, float* entropy,
-                           int64_t top, float* top_logprob, int64_t* top_id, void* workspace, int64_t workspace_bytes,
+                           const int64_t* targets, float* logprob, float* lse, float* row_ref, float* row_sum,
+                           float* entropy, int64_t top, float* top_logprob, int64_t* top_id, void* workspace, int64_t workspace_bytes,
                            void* stream) {
   whtq_status st = lp_check(dtype, rows, vocab, ld, scale);
   if (st != WHTQ_OK) return st;
   if (top < 0 || top > vocab || workspace_bytes < 0) return WHTQ_EINVAL;
   if (top > WHTQ_TOP_MOST) return WHTQ_EUNSUPPORTED;
-  if (rows > 0 && (!logits || (targets != nullptr) != (logprob != nullptr) || (top > 0 && (!top_logprob || !top_id)))) return WHTQ_EINVAL;
+  if (rows > 0 && (!logits || (targets != nullptr) != (logprob != nullptr) || (row_ref != nullptr) != (row_sum != nullptr) || (top > 0 && (!top_logprob || !top_id)))) return WHTQ_EINVAL;
   if (!lp_aligned(logits, dtype) || !aligned8(targets) || !aligned8(top_id) || !aligned4(logprob) || !aligned4(lse) ||
-      !aligned4(lse_low) || !aligned4(entropy) || !aligned4(top_logprob) || !aligned16(workspace))
+      !aligned4(row_ref) || !aligned4(row_sum) || !aligned4(entropy) || !aligned4(top_logprob) || !aligned16(workspace))
     return WHTQ_EALIGN;
   if (rows == 0) return WHTQ_OK;
   st = need_device();
@@ -1247,7 +1265,8 @@ whtq_status token_logprobs(const void* logits, whtq_dtype dtype, int64_t rows, i
   a.targets = targets;
   a.logprob = logprob;
   a.lse = lse;
-  a.lse_low = lse_low;
+  a.ref = row_ref;
+  a.sum = row_sum;
   a.entropy = entropy;
   a.top = (int)top;
   a.top_logprob = top_logprob;
@@ -1261,16 +1280,16 @@ whtq_status token_logprobs(const void* logits, whtq_dtype dtype, int64_t rows, i
 }
 
 whtq_status token_logprobs_backward(const void* logits, whtq_dtype dtype, int64_t rows, int64_t vocab, int64_t ld,
-                                    float scale, const int64_t* targets, const float* lse, const float* lse_low,
+                                    float scale, const int64_t* targets, const float* row_ref, const float* row_sum,
                                     const float* entropy, const float* dlogprob, const float* dentropy, void* dlogits,
                                     int64_t ldd, void* stream) {
   whtq_status st = lp_check(dtype, rows, vocab, ld, scale);
   if (st != WHTQ_OK) return st;
   if (ldd < vocab || (logits && logits == dlogits && ld != ldd)) return WHTQ_EINVAL;
-  if (rows > 0 && (!logits || !dlogits || !lse || (!dlogprob && !dentropy) || (dlogprob && !targets) || (dentropy && !entropy)))
+  if (rows > 0 && (!logits || !dlogits || !row_ref || !row_sum || (!dlogprob && !dentropy) || (dlogprob && !targets) || (dentropy && !entropy)))
     return WHTQ_EINVAL;
-  if (!lp_aligned(logits, dtype) || !lp_aligned(dlogits, dtype) || !aligned8(targets) || !aligned4(lse) ||
-      !aligned4(lse_low) || !aligned4(entropy) || !aligned4(dlogprob) || !aligned4(dentropy))
+  if (!lp_aligned(logits, dtype) || !lp_aligned(dlogits, dtype) || !aligned8(targets) || !aligned4(row_ref) ||
+      !aligned4(row_sum) || !aligned4(entropy) || !aligned4(dlogprob) || !aligned4(dentropy))
     return WHTQ_EALIGN;
   if (rows == 0) return WHTQ_OK;
   st = need_device();
@@ -1284,8 +1303,8 @@ whtq_status token_logprobs_backward(const void* logits, whtq_dtype dtype, int64_
   a.vocab = (int)vocab;
   a.scale = scale;
   a.targets = targets;
-  a.lse = lse;
-  a.lse_low = lse_low;
+  a.ref = row_ref;
+  a.sum = row_sum;
   a.entropy = entropy;
   a.dlogprob = dlogprob;
   a.dentropy = dentropy;

@@ -32,14 +32,12 @@ struct KvAppendArgs {
   KvRows k, v, q, qo;
   const int64_t* slots;
   KvTurn turn;
-  KvNorm norm;
   int64_t capacity;
   uint32_t rows;  // tokens * (heads + 2 kv_heads)
   int heads;
 };
 
-// NORM: keys and queries whose weights are given are normed before they are rotated.
-template <int D, int T, bool INT4, bool NORM>
+template <int D, int T, bool INT4>
 __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
   constexpr int L = D / 16, RB = 256 / L;
   const uint32_t r = blockIdx.x * RB + threadIdx.x / L;
@@ -58,21 +56,8 @@ __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
   kv_widen8<T>(ldg<u32x4>(row + 16 * (i + L)), x + 8);
   bool ok = live;
   if (a.turn.pos) ok = ok && pos >= 0 && pos < a.turn.max_pos;
-  if constexpr (NORM) {
-    const KvWeight& w = is_q ? a.norm.q : a.norm.k;
-    if (is_k || is_q) {
-      const uint8_t* wp = w.p ? w.p + h * w.head : nullptr;
-      const float r = kv_norm<D>(x, wp, a.norm.dt, a.norm.eps, i);
-      if (a.turn.pos && ok)
-        kv_rotate<D>(x, a.turn, pos, i, [&](int ch, float* o) {
-          kv_widen8<T>(ldg<u32x4>(row + 16 * ch), o);
-          if (wp) kv_weigh8(o, wp, a.norm.dt, ch, r);
-        });
-    }
-  } else {
-    if (a.turn.pos && ok && (is_k || is_q))
-      kv_rotate<D>(x, a.turn, pos, i, [&](int ch, float* o) { kv_widen8<T>(ldg<u32x4>(row + 16 * ch), o); });
-  }
+  if (a.turn.pos && ok && (is_k || is_q))
+    kv_rotate<D>(x, a.turn, pos, i, [&](int ch, float* o) { kv_widen8<T>(ldg<u32x4>(row + 16 * ch), o); });
   if (is_q) {
     if (ok) {
       uint8_t* o = const_cast<uint8_t*>(a.qo.p) + t * a.qo.tok + h * a.qo.head;
@@ -82,49 +67,7 @@ __global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
     return;
   }
   const int64_t slot = a.slots[t];
-  ok = ok && slot >= 0 && slot < a.capacity;
-  const KvSide& c = is_k ? a.c.k : a.c.v;
-  const int64_t page = slot >> a.c.page_shift, off = slot & ((1 << a.c.page_shift) - 1);
-  if constexpr (!INT4) {
-    if (!ok) return;
-    uint8_t* o = c.p + page * c.page + h * c.head + off * c.tok;
-    stg<u32x4>(o + 16 * i, kv_round8<T>(x));
-    stg<u32x4>(o + 16 * (i + L), kv_round8<T>(x + 8));
-  } else {
-    if (a.c.signs) {
-      kv_sign8(x, (a.c.signs[i >> 2] >> (8 * (i & 3))) & 255u);
-      kv_sign8(x + 8, (a.c.signs[(i + L) >> 2] >> (8 * ((i + L) & 3))) & 255u);
-    }
-    kv_bfly<8>(x);
-    kv_bfly<8>(x + 8);
-    kv_near_bfly<1>(x, i);
-    kv_near_bfly<2>(x, i);
-    if constexpr (D == 128) kv_near_bfly<4>(x, i);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) bfly(x[e], x[8 + e]);
-    // NaN stays the maximum: the row's scale is then NaN, and so is what it stands for
-    float top = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      x[e] *= D == 64 ? 0.125f : 0.08838834764831845f;  // 1 / sqrt(D)
-      top = __builtin_elementwise_maximum(top, fabsf(x[e]));
-    }
-#pragma unroll
-    for (int m = 1; m < L; m *= 2) top = __builtin_elementwise_maximum(top, as_f(m == 1 ? kv_lane_xor<1>(as_u(top)) : m == 2 ? kv_lane_xor<2>(as_u(top)) : kv_lane_xor<4>(as_u(top))));
-    const _Float16 s16 = (_Float16)(top / 7.0f);
-    const float s = (float)s16, inv = s > 0.f ? 1.0f / s : 0.f;
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int q = (int)__builtin_rintf(fminf(fmaxf(x[e] * inv, -7.f), 7.f));
-      w[e >> 3] |= (uint32_t)(q & 15) << (4 * (e & 7));
-    }
-    if (!ok) return;
-    uint8_t* o = c.p + page * c.page + h * c.head + off * c.tok;
-    stg<uint32_t>(o + 4 * i, w[0]);
-    stg<uint32_t>(o + 4 * (i + L), w[1]);
-    if (i == 0) c.scale[page * c.s_page + h * c.s_head + off] = __builtin_bit_cast(uint16_t, s16);
-  }
+  kv_keep<D, T, INT4>(x, a.c, is_k ? a.c.k : a.c.v, h, slot, ok && slot >= 0 && slot < a.capacity, i);
 }
 
 // The unscaled transform of a row's codes, as whole numbers: at most 8 D = 1024
@@ -271,16 +214,15 @@ static hipError_t by_tokens(int64_t tokens, int64_t per, int lanes, F launch) {
 
 template <int D, int T, bool INT4>
 static void append_launch(const KvAppendArgs& a, dim3 grid, hipStream_t s) {
-  if (a.norm.q.p || a.norm.k.p) hipLaunchKernelGGL((k_kv_append<D, T, INT4, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_kv_append<D, T, INT4, false>), grid, dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_kv_append<D, T, INT4>), grid, dim3(256), 0, s, a);
 }
 
 hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const void* k,
                             const int64_t* ks, const void* v, const int64_t* vs, const int64_t* slots,
-                            int64_t capacity, const KvTurn& turn, const KvNorm& norm, const void* q,
-                            const int64_t* qs, int heads, void* qo, const int64_t* qos, hipStream_t s) {
-  const int rb = 256 / (dim / 16);
+                            int64_t capacity, const KvTurn& turn, const void* q, const int64_t* qs, int heads,
+                            void* qo, const int64_t* qos, hipStream_t s) {
   const int64_t per = (q ? heads : 0) + 2 * (int64_t)c.kv_heads;
+  const int rb = 256 / (dim / 16);
   return by_tokens(tokens, per, dim / 16, [&](int64_t t0, int64_t n) {
     KvAppendArgs a{};
     a.c = c;
@@ -295,7 +237,6 @@ hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_
     a.capacity = capacity;
     a.turn = turn;
     if (turn.pos) a.turn.pos += t0;
-    a.norm = norm;
     a.rows = (uint32_t)(n * per);
     const dim3 grid((unsigned)((n * per + rb - 1) / rb));
     KV_PICK(append_launch, dim, dt, int4, a, grid, s);

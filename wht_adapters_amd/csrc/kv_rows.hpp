@@ -86,6 +86,52 @@ __device__ __forceinline__ void kv_rotate(float (&x)[16], const KvTurn& a, int64
   }
 }
 
+// The ways of a rotation, each a kernel of its own where registers count: a
+// whole row in halves, interleaved pairs, or halves of a part of the row.
+enum KvWay : int { KV_STILL = 0, KV_HALVES = 1, KV_PAIRS = 2, KV_PART = 3 };
+inline int kv_way(const KvTurn& a, int dim) {
+  return !a.pos ? KV_STILL : a.interleaved ? KV_PAIRS : a.rot == dim ? KV_HALVES : KV_PART;
+}
+// kv_rotate with the table's entries taken beforehand (but for KV_PART, whose
+// pairs lie in other lanes).
+struct KvCs {
+  f32x4 c[2], s[2];
+};
+template <int D, int WAY>
+__device__ __forceinline__ void kv_load_cs(KvCs& t, const KvTurn& a, int64_t pos, int i) {
+  if constexpr (WAY == KV_HALVES || WAY == KV_PAIRS) {
+    const float* cs = a.cos + pos * a.ld;
+    const float* sn = a.sin + pos * a.ld;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // (an interleaved chunk that is not rotated has no entry: the first one is not used)
+      const int at = WAY == KV_HALVES ? 8 * i + 4 * h : 8 * (i + h * (D / 16)) < a.rot ? 4 * (i + h * (D / 16)) : 0;
+      t.c[h] = ldg<f32x4>(cs + at);
+      t.s[h] = ldg<f32x4>(sn + at);
+    }
+  }
+}
+template <int D, int WAY, bool BACK, typename Load>
+__device__ __forceinline__ void kv_turn(float (&x)[16], const KvTurn& a, const KvCs& t, int64_t pos, int i, Load load) {
+#pragma clang fp contract(off)
+  if constexpr (WAY == KV_PART) kv_rotate<D, BACK>(x, a, pos, i, load);
+  if constexpr (WAY == KV_HALVES || WAY == KV_PAIRS) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (WAY == KV_PAIRS && 8 * (i + h * (D / 16)) >= a.rot) continue;
+      const f32x4 c = t.c[h], s = BACK ? -t.s[h] : t.s[h];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float& p = x[WAY == KV_HALVES ? 4 * h + e : 8 * h + 2 * e];
+        float& q = x[WAY == KV_HALVES ? 8 + 4 * h + e : 8 * h + 2 * e + 1];
+        const float u = p, w = q;
+        p = u * c[e] - w * s[e];
+        q = w * c[e] + u * s[e];
+      }
+    }
+  }
+}
+
 template <int M>  // the value of the lane that differs in lane bit M = 1, 2, 4
 __device__ __forceinline__ uint32_t kv_lane_xor(uint32_t x) {
   constexpr int QUAD = M == 1 ? 0xb1 : M == 2 ? 0x4e : 0x1b;  // quad_perm: lane ^ 1, ^ 2, ^ 3
@@ -98,6 +144,53 @@ __device__ __forceinline__ void kv_near_bfly(float (&x)[16], int i) {
   const float sg = i & M ? -1.f : 1.f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) x[e] = __builtin_fmaf(x[e], sg, as_f(kv_lane_xor<M>(as_u(x[e]))));
+}
+
+// The row x of head h, spread over the lanes, into its slot of the cache's keys or values.
+template <int D, int T, bool INT4>
+__device__ __forceinline__ void kv_keep(float (&x)[16], const KvCache& kv, const KvSide& c, int h, int64_t slot, bool ok, int i) {
+  constexpr int L = D / 16;
+  const int64_t page = slot >> kv.page_shift, off = slot & ((1 << kv.page_shift) - 1);
+  if constexpr (!INT4) {
+    if (!ok) return;
+    uint8_t* o = c.p + page * c.page + h * c.head + off * c.tok;
+    stg<u32x4>(o + 16 * i, kv_round8<T>(x));
+    stg<u32x4>(o + 16 * (i + L), kv_round8<T>(x + 8));
+  } else {
+    if (kv.signs) {
+      kv_sign8(x, (kv.signs[i >> 2] >> (8 * (i & 3))) & 255u);
+      kv_sign8(x + 8, (kv.signs[(i + L) >> 2] >> (8 * ((i + L) & 3))) & 255u);
+    }
+    kv_bfly<8>(x);
+    kv_bfly<8>(x + 8);
+    kv_near_bfly<1>(x, i);
+    kv_near_bfly<2>(x, i);
+    if constexpr (D == 128) kv_near_bfly<4>(x, i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bfly(x[e], x[8 + e]);
+    // NaN stays the maximum: the row's scale is then NaN, and so is what it stands for
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      x[e] *= D == 64 ? 0.125f : 0.08838834764831845f;  // 1 / sqrt(D)
+      top = __builtin_elementwise_maximum(top, fabsf(x[e]));
+    }
+#pragma unroll
+    for (int m = 1; m < L; m *= 2) top = __builtin_elementwise_maximum(top, as_f(m == 1 ? kv_lane_xor<1>(as_u(top)) : m == 2 ? kv_lane_xor<2>(as_u(top)) : kv_lane_xor<4>(as_u(top))));
+    const _Float16 s16 = (_Float16)(top / 7.0f);
+    const float s = (float)s16, inv = s > 0.f ? 1.0f / s : 0.f;
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int q = (int)__builtin_rintf(fminf(fmaxf(x[e] * inv, -7.f), 7.f));
+      w[e >> 3] |= (uint32_t)(q & 15) << (4 * (e & 7));
+    }
+    if (!ok) return;
+    uint8_t* o = c.p + page * c.page + h * c.head + off * c.tok;
+    stg<uint32_t>(o + 4 * i, w[0]);
+    stg<uint32_t>(o + 4 * (i + L), w[1]);
+    if (i == 0) c.scale[page * c.s_page + h * c.s_head + off] = __builtin_bit_cast(uint16_t, s16);
+  }
 }
 
 // Sum over the L lanes of a row, in every one of them.

@@ -218,10 +218,6 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
                       : v0 < v1 ? min(sp.last, tile_of(v1 - 1) * TK + TK - 1) : kfirst - 1;
     // whether any query sees the key
     auto counts = [&](int key) { return key >= kfirst && key <= klast && (!SINKS || key < a.sinks || key >= sp.first); };
-    auto row_sees = [&](int key, int pos) {
-      return key >= kfirst && key <= klast && (!a.causal || key <= pos) &&
-             (a.window <= 0 || key > pos - a.window || (SINKS && key < a.sinks));
-    };
     const int32_t* table = a.table + b * a.table_stride;
 
     const uint8_t* kbase = a.c.k.p + h * a.c.k.head;
@@ -391,7 +387,8 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
           const int key = key0 + 16 * kb + k;
 #pragma unroll
           for (int n = 0; n < NQ; ++n) {
-            const bool in = row_sees(key, qpos[n]);
+            const bool in = key >= kfirst && key <= klast && (!a.causal || key <= qpos[n]) &&
+                            (a.window <= 0 || key > qpos[n] - a.window || (SINKS && key < a.sinks));
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -502,7 +499,8 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
           if constexpr (INT4) sc[n][s] *= ks[s];
           if (!full) {
             const int key = key_of(s);
-            const bool in = row_sees(key, qpos[n]);
+            const bool in = key >= kfirst && key <= klast && (!a.causal || key <= qpos[n]) &&
+                            (a.window <= 0 || key > qpos[n] - a.window || (SINKS && key < a.sinks));
             sc[n][s] = in ? sc[n][s] : KV_NEG_INF;
           }
           top = fmaxf(top, sc[n][s]);

@@ -2,12 +2,16 @@
 // probabilities of given tokens, the entropy and the likeliest tokens, and
 // the gradient of the logits.
 //
-// With z = scale x, m a value near the row's largest, S = sum e^(z - m) and
-// T = sum e^(z - m) (z - m):
-//   lse = m + log S,  logprob = (z_t - m) - log S,  entropy = log S - T / S,
-// every term of the entropy of one sign.  Each lane keeps (m, S, T) of its
-// own logits over one pass; m may lag behind the largest by 2^LP_LAG, so
-// that S and T are rescaled a few times in a row and not for every vector.
+// With z = scale x, m a logit near the row's largest, S = sum e^(z - scale m)
+// and T = sum e^(z - scale m) (z - scale m):
+//   lse = scale m + log S,  logprob = scale (x_t - m) - log S,
+//   entropy = log S - T / S  (every term of one sign).
+// Each lane keeps (m, S, T) of its own logits over one pass; m may lag behind
+// the largest by LP_LAG, so that S and T are rescaled a few times in a row and
+// not for every vector.  Exponents are differences of logits times a factor
+// and never products that could overflow: rows masked with the type's lowest
+// value, even all of a row, come out right.  The gradient takes m and S again
+// rather than lse, whose rounding would be an error of every p.
 //
 // The likeliest tokens cost that pass one maximum over a group of logits
 // (kept in memory, 4 bytes for 512 logits of a long row): the k largest, ties
@@ -16,12 +20,13 @@
 // The last kernel of a row picks those groups and reads only them again.
 //
 // What bounds both directions is memory.  Rows need no alignment beyond their
-// elements': loads of 16 bytes are given their true alignment, and the last
-// few logits of a row are loaded one by one.
+// elements': a row is taken by the aligned 16 bytes it lies in, and the few
+// logits at its two ends are loaded one by one.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "io.hpp"
@@ -46,28 +51,45 @@ typedef u32x4 u32x4_by2 __attribute__((aligned(2)));
 struct Lp8 {  // eight logits as loaded
   u32x4 w[2];
 };
-// Logits i .. i + 7 of a row; what lies behind its end is -inf.
+// A row by the aligned 16 bytes that hold it: logit i stands at place i + pad,
+// places [pad, end) are the row's.
+struct LpRow {
+  const uint8_t* p;
+  int pad, end;
+};
 template <int DT>
-__device__ __forceinline__ void lp_load(const uint8_t* row, int i, int vocab, Lp8& r) {
+__device__ __forceinline__ LpRow lp_row(const uint8_t* x, int vocab) {
+  const int off = (int)(reinterpret_cast<uintptr_t>(x) & 15u);
+  return {x - off, off / LP_BYTES<DT>, vocab + off / LP_BYTES<DT>};
+}
+// Places i .. i + 7.  NT: read once, and not to be kept.
+template <int DT, bool ALIGNED, bool NT>
+__device__ __forceinline__ void lp_load8(const uint8_t* row, int i, Lp8& r) {
   const uint8_t* p = row + (int64_t)i * LP_BYTES<DT>;
-  if (i + 8 <= vocab) {
-    if constexpr (DT == DT_F32) {
-      r.w[0] = *reinterpret_cast<const u32x4_by4*>(p);
-      r.w[1] = *reinterpret_cast<const u32x4_by4*>(p + 16);
-    } else {
-      r.w[0] = *reinterpret_cast<const u32x4_by2*>(p);
-    }
-    return;
+  constexpr int N = DT == DT_F32 ? 2 : 1;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    using V = std::conditional_t<ALIGNED, u32x4, std::conditional_t<DT == DT_F32, u32x4_by4, u32x4_by2>>;
+    const V* v = reinterpret_cast<const V*>(p) + k;
+    if constexpr (NT) r.w[k] = __builtin_nontemporal_load(v);
+    else r.w[k] = *v;
   }
+}
+// The same where some places may not be the row's: those give -inf.
+template <int DT>
+__device__ __forceinline__ void lp_load_edge(const LpRow& x, int i, Lp8& r) {
+  if (i >= x.pad && i + 8 <= x.end) return lp_load8<DT, false, false>(x.p, i, r);
+  const uint8_t* p = x.p + (int64_t)i * LP_BYTES<DT>;
+  auto in = [&](int e) { return i + e >= x.pad && i + e < x.end; };
   constexpr uint32_t NONE = DT == DT_BF16 ? 0xff80u : 0xfc00u;
   if constexpr (DT == DT_F32) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r.w[e >> 2][e & 3] = i + e < vocab ? reinterpret_cast<const uint32_t*>(p)[e] : 0xff800000u;
+    for (int e = 0; e < 8; ++e) r.w[e >> 2][e & 3] = in(e) ? reinterpret_cast<const uint32_t*>(p)[e] : 0xff800000u;
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = i + 2 * e < vocab ? reinterpret_cast<const uint16_t*>(p)[2 * e] : NONE;
-      const uint32_t hi = i + 2 * e + 1 < vocab ? reinterpret_cast<const uint16_t*>(p)[2 * e + 1] : NONE;
+      const uint32_t lo = in(2 * e) ? reinterpret_cast<const uint16_t*>(p)[2 * e] : NONE;
+      const uint32_t hi = in(2 * e + 1) ? reinterpret_cast<const uint16_t*>(p)[2 * e + 1] : NONE;
       r.w[0][e] = lo | hi << 16;
     }
   }
@@ -98,7 +120,18 @@ __device__ __forceinline__ uint32_t lp_key(float x) {
 }
 __device__ __forceinline__ float lp_value(uint32_t k) { return as_f(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
-// (m, S, T) of some logits; T in units of log 2.
+// The largest of eight (fmaxf would quiet each of them first, as many
+// operations again).  A signalling NaN makes it NaN, other NaNs drop out.
+__device__ __forceinline__ float lp_max8(const float* f) {
+  float a, b;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(a) : "v"(f[0]), "v"(f[1]), "v"(f[2]));
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(b) : "v"(f[3]), "v"(f[4]), "v"(f[5]));
+  asm("v_max3_f32 %0, %0, %1, %2" : "+v"(a) : "v"(f[6]), "v"(f[7]));
+  asm("v_max_f32 %0, %0, %1" : "+v"(a) : "v"(b));
+  return a;
+}
+
+// (m, S, T) of some logits; exponents are in units of log 2.
 struct LpSum {
   float m, s, t;
 };
@@ -128,11 +161,11 @@ template <int DT>
 __device__ __forceinline__ void lp_finish(const LpArgs& a, int64_t row, const LpSum& r) {
   const bool none = r.s == 0.f;
   const float ls = logf(r.s);
-  // lse as the sum of two floats: the gradient's exponent needs more than one where logits are large
-  const double lse = none ? (double)LP_NEG_INF : (double)r.m * (double)a.scale + (double)ls;
-  const float hi = (float)lse;
-  if (a.lse) a.lse[row] = hi;
-  if (a.lse_low) a.lse_low[row] = fabsf(hi) < __builtin_huge_valf() ? (float)(lse - (double)hi) : 0.f;
+  if (a.lse) a.lse[row] = none ? LP_NEG_INF : (float)((double)r.m * (double)a.scale + (double)ls);
+  if (a.ref) {
+    a.ref[row] = none ? 0.f : r.m;
+    a.sum[row] = r.s;
+  }
   if (a.entropy) a.entropy[row] = none ? 0.f : ls - r.t / r.s * LP_LN2;
   if (a.targets && a.logprob) {
     const int64_t t = a.targets[row];
@@ -143,25 +176,31 @@ __device__ __forceinline__ void lp_finish(const LpArgs& a, int64_t row, const Lp
 }
 
 // A block's share of a row: chunks c, c + 4, .. by each of its waves.
-// TOP: the maxima of groups of LANES lanes' logits are kept.
+// LANES > 0: the maxima of groups of as many lanes' logits are kept.
 template <int DT, int LANES>
 __global__ __launch_bounds__(256) void k_lp_row(const LpArgs a) {
   constexpr int AHEAD = DT == DT_F32 ? 2 : 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x % (uint32_t)a.splits;
   const int64_t row = a.row0 + blockIdx.x / (uint32_t)a.splits;
-  const int chunks = (a.vocab + LP_CHUNK - 1) / LP_CHUNK;
+  const LpRow x = lp_row<DT>(a.x + row * a.ld, a.vocab);
+  const int chunks = (x.end + LP_CHUNK - 1) / LP_CHUNK, first = x.pad > 0, whole = x.end / LP_CHUNK;  // [first, whole) are whole
   const int c0 = (int)((int64_t)chunks * split / a.splits), c1 = (int)((int64_t)chunks * (split + 1) / a.splits);
-  const uint8_t* x = a.x + row * a.ld;
   const float c = a.scale * LP_LOG2E, lag = fminf(LP_LAG / c, 1e30f);
   LpSum r{LP_NEG_INF, 0.f, 0.f};
   Lp8 buf[AHEAD];
-  auto take = [&](const Lp8& w, int ch) {
+  auto take = [&](const Lp8& w, int ch) __attribute__((always_inline)) {
     float f[8];
     lp_widen<DT>(w, f);
-    float top = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+    const float top = lp_max8(f);
     if constexpr (LANES > 0) {
-      uint32_t k = lp_key(top == top ? top : LP_NEG_INF);  // (a NaN counts as -inf in the order)
+      float most = top;
+      if (__any(top != top)) {  // a NaN counts as -inf in the order
+        most = LP_NEG_INF;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = f[e] > most ? f[e] : most;
+      }
+      uint32_t k = lp_key(most);
       if constexpr (LANES == 64) {
         k = wave_max_u32(k);
         if (lane == 0) a.best[row * a.groups + ch] = k;
@@ -188,22 +227,39 @@ __global__ __launch_bounds__(256) void k_lp_row(const LpArgs a) {
     for (int e = 0; e < 8; ++e) {
       const float z = (f[e] - base) * c, p = __builtin_amdgcn_exp2f(z);
       r.s += p;
-      r.t += p * fmaxf(z, LP_LEAST);
+      r.t = __builtin_fmaf(p, fmaxf(z, LP_LEAST), r.t);
     }
   };
-  int ch = c0 + wave;
+  // Whole chunks, each loaded AHEAD of its use; no branch between a load and
+  // its use but at the end, so that every wait is for one load alone.
+  auto load = [&](Lp8& w, int ch) __attribute__((always_inline)) { lp_load8<DT, true, true>(x.p, ch * LP_CHUNK + 8 * lane, w); };
+  const int start = max(c0, first), end = min(c1, whole);
+  int ch = start + wave;
+  if (start < end) {
 #pragma unroll
-  for (int u = 0; u < AHEAD; ++u)
-    if (ch + 4 * u < c1) lp_load<DT>(x, (ch + 4 * u) * LP_CHUNK + 8 * lane, a.vocab, buf[u]);
-  while (ch < c1) {
+    for (int u = 0; u < AHEAD; ++u) load(buf[u], min(ch + 4 * u, end - 1));
+  }
+  for (; ch + 4 * (2 * AHEAD - 1) < end; ch += 4 * AHEAD)
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
-      if (ch + 4 * u < c1) {
-        take(buf[u], ch + 4 * u);
-        const int next = ch + 4 * (u + AHEAD);
-        if (next < c1) lp_load<DT>(x, next * LP_CHUNK + 8 * lane, a.vocab, buf[u]);
-      }
-    ch += 4 * AHEAD;
+    for (int u = 0; u < AHEAD; ++u) {
+      take(buf[u], ch + 4 * u);
+      load(buf[u], ch + 4 * (u + AHEAD));
+    }
+#pragma unroll
+  for (int v = 0; v < 2; ++v, ch += 4 * AHEAD)
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (ch + 4 * u < end) take(buf[u], ch + 4 * u);
+      if (v == 0 && ch + 4 * (u + AHEAD) < end) load(buf[u], ch + 4 * (u + AHEAD));
+    }
+  // the chunks at the row's ends (one, where it is short)
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    const int at = e ? whole : 0;
+    if (e ? whole == chunks || (first && whole == 0) : !first) continue;
+    if (at < c0 || at >= c1 || (at + e) % 4 != wave) continue;
+    lp_load_edge<DT>(x, at * LP_CHUNK + 8 * lane, buf[0]);
+    take(buf[0], at);
   }
   r = lp_lanes<64>(r, c);
   __shared__ LpSum sw[4];
@@ -211,9 +267,7 @@ __global__ __launch_bounds__(256) void k_lp_row(const LpArgs a) {
   __syncthreads();
   if (threadIdx.x == 0) {
     r = lp_add(lp_add(sw[0], sw[1], c), lp_add(sw[2], sw[3], c), c);
-    if (a.splits == 1) {
-      lp_finish<DT>(a, row, r);
-    }
+    if (a.splits == 1) lp_finish<DT>(a, row, r);
     if (a.splits > 1 || LANES > 0) {
       float* p = a.part + (row * a.splits + split) * 3;
       p[0] = r.m;
@@ -223,68 +277,110 @@ __global__ __launch_bounds__(256) void k_lp_row(const LpArgs a) {
   }
 }
 
-// Joins a row's shares, a wave a row.
-template <int DT>
-__global__ __launch_bounds__(256) void k_lp_join(const LpArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = a.row0 + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= a.rows) return;
+// A row's shares joined, by a wave.
+__device__ __forceinline__ LpSum lp_shares(const LpArgs& a, int64_t row, int lane) {
   const float c = a.scale * LP_LOG2E;
   LpSum r{LP_NEG_INF, 0.f, 0.f};
   for (int s = lane; s < a.splits; s += 64) {
     const float* p = a.part + (row * a.splits + s) * 3;
     r = lp_add(r, {p[0], p[1], p[2]}, c);
   }
-  r = lp_lanes<64>(r, c);
+  return lp_lanes<64>(r, c);
+}
+template <int DT>
+__global__ __launch_bounds__(256) void k_lp_join(const LpArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = a.row0 + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= a.rows) return;
+  const LpSum r = lp_shares(a, row, lane);
   if (lane == 0) lp_finish<DT>(a, row, r);
 }
 
-// The same for a row whose likeliest tokens are asked for, a block a row.
+// The n groups of largest maxima, ties to the lower group, by a wave; lane i
+// holds PER groups side by side.  Bit by bit the largest number that n of the
+// maxima reach: most of the time the count is n before the last bit, and the
+// groups that reach it are the ones.  Returns a number that they reach and no
+// other group exceeds.  A group may be several of those whose maxima were
+// kept (`merge`).
+template <int PER>
+__device__ __forceinline__ uint32_t lp_pick(const uint32_t* best, int kept, int merge, int groups, int n, int lane, int* pick) {
+  uint32_t key[PER];
+  if (merge == 1) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) key[j] = best[min(lane * PER + j, groups - 1)];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) key[j] = lane * PER + j < groups ? key[j] : 0u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int g = lane * PER + j;
+      key[j] = 0;
+      for (int k = g * merge; k < min((g + 1) * merge, kept); ++k) key[j] = max(key[j], best[k]);
+    }
+  }
+  uint32_t bar = 0;
+  int have = 0;
+  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+    const uint32_t to = bar | bit;
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) c += __popcll(__ballot(key[j] >= to));
+    if (c < n) continue;
+    bar = to;
+    have = c;
+    if (c == n) break;
+  }
+  // (n groups are there, and their maxima are not 0: bar > 0)
+  int spare = n, mine = 0;  // places for the last of equals; those of them before this lane's
+  const uint64_t below = (1ull << lane) - 1;
+  if (have > n) {
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      above += __popcll(__ballot(key[j] > bar));
+      mine += __popcll(__ballot(key[j] == bar) & below);
+    }
+    spare = n - above;
+  }
+  int at = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const bool in = key[j] > bar || (key[j] == bar && (have == n || mine < spare));
+    mine += key[j] == bar;
+    const uint64_t m = __ballot(in);
+    if (in) pick[at + __popcll(m & below)] = lane * PER + j;
+    at += __popcll(m);
+  }
+  return bar;
+}
+
+// A row whose likeliest tokens are asked for, a block a row.
 template <int DT>
 __global__ __launch_bounds__(256) void k_lp_top(const LpArgs a) {
-  constexpr int CAP = 256;  // candidates ranked at once
-  __shared__ uint32_t key[LP_MOST_VOCAB / LP_CHUNK];
+  constexpr int CAP = 256, VECS = 128;  // candidates ranked at once, vectors that may hold any
+  constexpr int MOST = 4;  // vectors of a thread under way (8 and fewer blocks a CU: 2047 rows 11.9 us against 9.4)
   __shared__ int pick[LP_MOST_TOP];
   __shared__ uint64_t cand[CAP], sbest[4];
+  __shared__ __attribute__((aligned(16))) float vec[VECS][8];
+  __shared__ int first[VECS], base[VECS];
   __shared__ uint32_t bar;
-  __shared__ int count;
+  __shared__ int vectors, count;
   __shared__ float sm, sls;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row = a.row0 + blockIdx.x;
-  const uint8_t* x = a.x + row * a.ld;
-  const int n = min(a.top, a.groups);
-  for (int i = threadIdx.x; i < a.groups; i += 256) key[i] = a.best[row * a.groups + i];
-  if (threadIdx.x == 0) count = 0;
-  __syncthreads();
+  const LpRow x = lp_row<DT>(a.x + row * a.ld, a.vocab);
+  const int kept = (x.end + a.width - 1) / a.width;  // at most a.groups
+  const int merge = kept <= 512 ? 1 : (kept + 511) / 512, groups = merge == 1 ? kept : (kept + merge - 1) / merge;
+  const int n = min(a.top, groups);
+  if (threadIdx.x == 0) vectors = count = 0;
   if (wave == 0) {
-    // the n groups of largest maxima, one after another: lane i watches over its own run of groups
-    const int per = (a.groups + 63) / 64, g0 = min(lane * per, a.groups), g1 = min(g0 + per, a.groups);
-    uint32_t k = 0;
-    int at = g0;
-    auto look = [&] {
-      k = 0;
-      for (int g = g0; g < g1; ++g)
-        if (key[g] > k) k = key[g], at = g;
-    };
-    look();
-    for (int i = 0; i < n; ++i) {
-      const uint32_t top = wave_max_u32(k);
-      const int l = __builtin_ctzll(__ballot(k == top));
-      if (lane == l) {
-        pick[i] = at;
-        key[at] = 0;
-        look();
-        if (i == n - 1) bar = n == a.top ? top : 0u;
-      }
-    }
+    const uint32_t* best = a.best + row * a.groups;
+    const uint32_t reach = groups <= 64 ? lp_pick<1>(best, kept, merge, groups, n, lane, pick)
+                          : groups <= 256 ? lp_pick<4>(best, kept, merge, groups, n, lane, pick)
+                                          : lp_pick<8>(best, kept, merge, groups, n, lane, pick);
+    if (lane == 0) bar = n == a.top ? reach : 0u;
   } else if (wave == 1) {
-    const float c = a.scale * LP_LOG2E;
-    LpSum r{LP_NEG_INF, 0.f, 0.f};
-    for (int s = lane; s < a.splits; s += 64) {
-      const float* p = a.part + (row * a.splits + s) * 3;
-      r = lp_add(r, {p[0], p[1], p[2]}, c);
-    }
-    r = lp_lanes<64>(r, c);
+    const LpSum r = lp_shares(a, row, lane);
     if (lane == 0) {
       if (a.splits > 1) lp_finish<DT>(a, row, r);
       sm = r.s == 0.f ? 0.f : r.m;
@@ -292,43 +388,79 @@ __global__ __launch_bounds__(256) void k_lp_top(const LpArgs a) {
     }
   }
   __syncthreads();
-  // candidates: logits of those groups that reach the last one's maximum.
-  // (value, index) as one number, larger first and the lower index first
-  const int vecs = a.width / 8;
-  auto each = [&](auto f) {
-    for (int v = threadIdx.x; v < n * vecs; v += 256) {
-      const int i = pick[v / vecs] * a.width + v % vecs * 8;
-      if (i >= a.vocab) continue;
-      Lp8 w;
-      float y[8];
-      lp_load<DT>(x, i, a.vocab, w);
-      lp_widen<DT>(w, y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (i + e < a.vocab) {
-          const float z = y[e] == y[e] ? y[e] : LP_NEG_INF;
-          f((uint64_t)lp_key(z) << 32 | ~(uint32_t)(i + e));
-        }
-    }
+  // candidates: logits of those groups that reach `bar`; (value, index) as one
+  // number, larger first and the lower index first
+  const int shift = a.width == 8 ? 0 : a.width == 64 ? 3 : 6, all = n * merge << shift;
+  auto at = [&](int v) {  // the first place of vector v
+    const int u = v >> shift, in = v & ((1 << shift) - 1);
+    return ((merge == 1 ? pick[u] : pick[u / merge] * merge + u % merge) << (shift + 3)) + 8 * in;
   };
-  const uint64_t least = (uint64_t)bar << 32;
-  each([&](uint64_t q) {
-    if (q >= least) {
-      const int at = atomicAdd(&count, 1);
-      if (at < CAP) cand[at] = q;
+  // vector v: its first place i, and the place from which 8 are loaded for it,
+  // inside the row
+  auto place = [&](int v, int& i, int& from) {
+    i = v < all ? at(v) : x.end;
+    from = max(min(i, x.end - 8), x.pad);
+  };
+  auto fetch = [&](Lp8& w, int from) __attribute__((always_inline)) {
+    if (a.vocab < 8) lp_load_edge<DT>(x, from, w);
+    else lp_load8<DT, false, false>(x.p, from, w);
+  };
+  const uint32_t least = bar;
+  // 8 logits y from `from` on: f of the key and the token of those from i on
+  auto one = [&](float y, int e, int i, int from, auto f) __attribute__((always_inline)) {
+    const int id = from + e;
+    if (id >= i && id < i + 8 && id < x.end) f(lp_key(y == y ? y : LP_NEG_INF), ~(uint32_t)(id - x.pad));
+  };
+  // vectors that may hold candidates first, then their logits side by side
+  for (int v0 = 0; v0 < all; v0 += 256 * MOST) {
+    Lp8 w[MOST];
+    int i[MOST], from[MOST];
+#pragma unroll
+    for (int u = 0; u < MOST; ++u)  // all of them under way together
+      if (v0 + 256 * u < all) {
+        place(v0 + 256 * u + threadIdx.x, i[u], from[u]);
+        fetch(w[u], from[u]);
+      }
+#pragma unroll
+    for (int u = 0; u < MOST; ++u) {
+      if (v0 + 256 * u >= all) break;
+      float y[8];
+      lp_widen<DT>(w[u], y);
+      const float top = lp_max8(y);
+      if (i[u] < x.end && (top != top || lp_key(top) >= least)) {  // (a NaN hides what is beside it)
+        const int to = atomicAdd(&vectors, 1);
+        if (to < VECS) {
+          *reinterpret_cast<f32x4*>(&vec[to][0]) = f32x4{y[0], y[1], y[2], y[3]};
+          *reinterpret_cast<f32x4*>(&vec[to][4]) = f32x4{y[4], y[5], y[6], y[7]};
+          first[to] = i[u];
+          base[to] = from[u];
+        }
+      }
     }
-  });
+  }
+  __syncthreads();
+  if (vectors <= VECS) {
+    for (int t = threadIdx.x; t < 8 * vectors; t += 256) {
+      const int v = t >> 3;
+      one(vec[v][t & 7], t & 7, first[v], base[v], [&](uint32_t k, uint32_t id) {
+        if (k >= least) {
+          const int to = atomicAdd(&count, 1);
+          if (to < CAP) cand[to] = (uint64_t)k << 32 | id;
+        }
+      });
+    }
+  }
   __syncthreads();
   auto put = [&](int i, uint64_t q) {
-    const uint32_t id = ~(uint32_t)q;
-    a.top_id[row * a.top + i] = id;
-    a.top_logprob[row * a.top + i] = (lp_one<DT>(x, id) - sm) * a.scale - sls;
+    a.top_id[row * a.top + i] = ~(uint32_t)q;
+    a.top_logprob[row * a.top + i] = (lp_value((uint32_t)(q >> 32)) - sm) * a.scale - sls;
   };
-  const int have = count;
+  const int have = vectors <= VECS ? count : CAP + 1;
   if (have <= CAP) {
     if ((int)threadIdx.x < have) {
       const uint64_t q = cand[threadIdx.x];
       int rank = 0;
+#pragma unroll 4
       for (int i = 0; i < have; ++i) rank += cand[i] > q;
       if (rank < a.top) put(rank, q);
     }
@@ -338,7 +470,20 @@ __global__ __launch_bounds__(256) void k_lp_top(const LpArgs a) {
   uint64_t last = ~0ull;
   for (int i = 0; i < a.top; ++i) {
     uint64_t q = 0;
-    each([&](uint64_t p) { q = p < last && p > q ? p : q; });
+    for (int v = threadIdx.x; v < all; v += 256) {
+      Lp8 w;
+      int k, from;
+      place(v, k, from);
+      fetch(w, from);
+      float y[8];
+      lp_widen<DT>(w, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        one(y[e], e, k, from, [&](uint32_t z, uint32_t id) {
+          const uint64_t p = (uint64_t)z << 32 | id;
+          q = p < last && p > q ? p : q;
+        });
+    }
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) q = max(q, (uint64_t)__shfl_xor((unsigned long long)q, m, 64));
     if (lane == 0) sbest[wave] = q;
@@ -349,62 +494,66 @@ __global__ __launch_bounds__(256) void k_lp_top(const LpArgs a) {
   }
 }
 
-// d logits = scale (g (onehot - p) - h p (log p + H)).
+// d logits = scale (g (onehot - p) - h p (log p + H)), with p = e / S and
+// log p = z - log S: e times a line in z, whose two numbers a row has.
 template <int DT>
 __global__ __launch_bounds__(256) void k_lp_grad(const LpGradArgs a) {
   constexpr int U = 4;
   const int64_t row = a.row0 + blockIdx.x / (uint32_t)a.pieces;
   const int piece = blockIdx.x % (uint32_t)a.pieces;
-  const uint8_t* x = a.x + row * a.ld;
-  uint8_t* dx = a.dx + row * a.ldd;
+  // by the aligned 16 bytes of the gradient's row; the logits lie alike, or are loaded unaligned
+  const LpRow o = lp_row<DT>(a.dx + row * a.ldd, a.vocab);
+  const uint8_t* x = a.x + row * a.ld - o.pad * LP_BYTES<DT>;
   const int64_t t = a.targets ? a.targets[row] : -1;
   const bool given = t >= 0 && t < a.vocab;
-  const float lse = a.lse[row], low = a.lse_low ? a.lse_low[row] : 0.f;
-  const float g = given && a.dlogprob ? a.dlogprob[row] * a.scale : 0.f;
+  const float m = a.ref[row], sum = a.sum[row], c = a.scale * LP_LOG2E;
+  const bool none = sum == 0.f;
+  const float g = given && a.dlogprob && !none ? a.dlogprob[row] * a.scale : 0.f;
   const float h = a.dentropy ? a.dentropy[row] * a.scale : 0.f, ent = a.dentropy ? a.entropy[row] : 0.f;
-  const bool none = lse == LP_NEG_INF;
+  const float inv = none ? 0.f : -1.f / sum, ls = none ? 0.f : logf(sum);
+  const float slope = h * LP_LN2 * inv, at0 = (g + h * (ent - ls)) * inv;
+  const int64_t tp = given ? t + o.pad : -1;
   const int i0 = (piece * U * 256 + (int)threadIdx.x) * 8;
+  auto inner = [&](int i) { return i >= o.pad && i + 8 <= o.end; };
+  auto grad = [&](const Lp8& w, int i, float* f) __attribute__((always_inline)) {
+    lp_widen<DT>(w, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float z = (f[e] - m) * c;
+      const float d = __builtin_amdgcn_exp2f(z) * __builtin_fmaf(fmaxf(z, LP_LEAST), slope, at0);
+      f[e] = i + e == tp ? d + g : d;
+    }
+  };
   Lp8 w[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (i0 + 2048 * u < a.vocab) lp_load<DT>(x, i0 + 2048 * u, a.vocab, w[u]);
+    if (inner(i0 + 2048 * u)) lp_load8<DT, false, true>(x, i0 + 2048 * u, w[u]);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int i = i0 + 2048 * u;
-    if (i >= a.vocab) break;
     float f[8];
-    lp_widen<DT>(w[u], f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float lp = __builtin_fmaf(f[e], a.scale, -lse) - low;
-      const float p = __builtin_amdgcn_exp2f(lp * LP_LOG2E);
-      float d = -p * (g + h * (fmaxf(lp, LP_LEAST) + ent));
-      if (i + e == t) d += g;
-      f[e] = none ? 0.f : d;
-    }
-    uint8_t* o = dx + (int64_t)i * LP_BYTES<DT>;
-    if constexpr (DT == DT_F32) {
-      if (i + 8 <= a.vocab) {
-        *reinterpret_cast<u32x4_by4*>(o) = u32x4{as_u(f[0]), as_u(f[1]), as_u(f[2]), as_u(f[3])};
-        *reinterpret_cast<u32x4_by4*>(o + 16) = u32x4{as_u(f[4]), as_u(f[5]), as_u(f[6]), as_u(f[7])};
+    uint8_t* to = const_cast<uint8_t*>(o.p) + (int64_t)i * LP_BYTES<DT>;
+    if (inner(i)) {
+      grad(w[u], i, f);
+      if constexpr (DT == DT_F32) {
+        __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4*>(to));
+        __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, reinterpret_cast<f32x4*>(to) + 1);
       } else {
+        u32x4 v;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (i + e < a.vocab) reinterpret_cast<float*>(o)[e] = f[e];
+        for (int q = 0; q < 4; ++q) v[q] = DT == DT_BF16 ? pack_bf16(f[2 * q], f[2 * q + 1]) : pack_f16(f[2 * q], f[2 * q + 1]);
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(to));
       }
-    } else {
-      u32x4 v;
+    } else if (i < o.end) {  // the row's ends
+      Lp8 y;
+      lp_load_edge<DT>(LpRow{x, o.pad, o.end}, i, y);
+      grad(y, i, f);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = DT == DT_BF16 ? pack_bf16(f[2 * q], f[2 * q + 1]) : pack_f16(f[2 * q], f[2 * q + 1]);
-      if (i + 8 <= a.vocab) {
-        *reinterpret_cast<u32x4_by2*>(o) = v;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t y = v[e >> 1];
-          if (i + e < a.vocab) reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(e & 1 ? y >> 16 : y & 0xffffu);
+      for (int e = 0; e < 8; ++e)
+        if (i + e >= o.pad && i + e < o.end) {
+          if constexpr (DT == DT_F32) reinterpret_cast<float*>(to)[e] = f[e];
+          else reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)((DT == DT_BF16 ? pack_bf16(f[e], 0.f) : pack_f16(f[e], 0.f)) & 0xffffu);
         }
-      }
     }
   }
 }
@@ -435,7 +584,7 @@ hipError_t rows_launch(LpArgs a, hipStream_t s) {
 }
 template <int DT>
 hipError_t grad_launch(LpGradArgs a, hipStream_t s) {
-  a.pieces = (a.vocab + 8191) / 8192;
+  a.pieces = (a.vocab + 7 + 8191) / 8192;  // (with a row's padding)
   const int64_t most = kLaunchThreads / 256 / a.pieces;
   for (a.row0 = 0; a.row0 < a.rows; a.row0 += most) {
     hipLaunchKernelGGL((k_lp_grad<DT>), dim3((unsigned)(std::min(a.rows - a.row0, most) * a.pieces)), dim3(256), 0, s, a);

@@ -15,7 +15,7 @@ struct LpArgs {
   int vocab;
   float scale;
   const int64_t* targets;
-  float *logprob, *lse, *lse_low, *entropy;
+  float *logprob, *lse, *ref, *sum, *entropy;
   int top;
   float* top_logprob;
   int64_t* top_id;
@@ -31,7 +31,7 @@ struct LpGradArgs {
   int vocab, pieces;      // blocks of a row
   float scale;
   const int64_t* targets;
-  const float *lse, *lse_low, *entropy, *dlogprob, *dentropy;
+  const float *ref, *sum, *entropy, *dlogprob, *dentropy;
   int64_t row0;
 };
 

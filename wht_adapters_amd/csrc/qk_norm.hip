@@ -1,5 +1,6 @@
-// qk_norm_rope and its backward pass: norms of each head's queries and keys
-// and their rotary positions on dense rows.
+// kv_append with norms, qk_norm_rope and its backward pass: norms of each
+// head's queries and keys and their rotary positions, into a cache's slots
+// and dense rows.
 //
 //   r = (mean x^2 + eps)^-1/2,  y = R (w o x r)
 // and with g = R^T dy (the opposite rotation), u = w o g:
@@ -9,9 +10,11 @@
 // less to keep, and x has to be read anyway.
 //
 // Both directions move bytes.  A row belongs to D / 16 lanes as in kv_append.
-// Backward, a block walks rows of one weight vector, so that a lane's part of
-// dw stays in registers; blocks leave one partial sum each, which a second
-// kernel adds in a fixed order (no atomics: the same result every time).
+// Forward, the blocks of keys, values and queries are apart, so that a row's
+// kind, its bases and strides are scalars.  Backward, a block walks rows of
+// one weight vector, so that a lane's part of dw stays in registers; blocks
+// leave one partial sum each, which a second kernel adds in a fixed order (no
+// atomics: the same result every time).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,38 +25,48 @@ namespace whtq {
 
 namespace {
 
-template <int D, int T>
-__global__ __launch_bounds__(256) void k_qk_norm(const QkArgs a, uint32_t rows) {
+__device__ __forceinline__ uint32_t kv_div(uint32_t n, const KvDiv& d) { return d.m ? __umulhi(n, d.m) >> d.s : n; }
+
+template <int D, int T, bool INT4, int WAY>
+__global__ __launch_bounds__(256) void k_qk_norm(const QkForwardArgs a) {
   constexpr int L = D / 16, RB = 256 / L;
-  const uint32_t n = blockIdx.x * RB + threadIdx.x / L;
+  uint32_t b = blockIdx.x;
+  const int kind = b < a.f[0].blocks ? 0 : b < a.f[0].blocks + a.f[1].blocks ? 1 : 2;
+  if (kind > 0) b -= a.f[0].blocks;
+  if (kind > 1) b -= a.f[1].blocks;
+  const QkForward& f = a.f[kind];
+  const uint32_t n = b * RB + threadIdx.x / L;
   const int i = threadIdx.x % L;
-  const uint32_t per = a.q.heads + a.k.heads;
-  const bool live = n < rows;
-  const uint32_t t = live ? n / per : 0, hs = live ? n % per : 0;
-  const bool is_q = hs < (uint32_t)a.q.heads;
-  const QkSide& s = is_q ? a.q : a.k;
-  const int h = is_q ? hs : hs - a.q.heads;
-  const uint8_t* row = s.x.p + t * s.x.tok + h * s.x.head;
-  const uint8_t* w = s.w.p + h * s.w.head;
-  const int64_t pos = a.turn.pos ? (int64_t)a.turn.pos[t] : 0;
+  const bool live = n < f.rows;
+  const uint32_t t = live ? kv_div(n, f.heads) : 0, h = live ? n - t * f.heads.d : 0;
+  const uint8_t* row = f.in.p + t * f.in.tok + h * f.in.head;
+  const u32x4 raw0 = ldg<u32x4>(row + 16 * i), raw1 = ldg<u32x4>(row + 16 * (i + L));
+  const int64_t pos = WAY ? (int64_t)a.turn.pos[t] : 0, slot = f.out.p ? 0 : a.slots[t];
+  const bool ok = live && (!WAY || (pos >= 0 && pos < a.turn.max_pos));
+  KvCs cs;
+  if (f.turned) kv_load_cs<D, WAY>(cs, a.turn, ok ? pos : 0, i);
   float x[16];
-  kv_widen8<T>(ldg<u32x4>(row + 16 * i), x);
-  kv_widen8<T>(ldg<u32x4>(row + 16 * (i + L)), x + 8);
-  const float r = kv_norm<D>(x, w, a.dt, a.eps, i);
-  if (!live) return;
-  if (a.turn.pos) {
-    if (pos < 0 || pos >= a.turn.max_pos) return;
-    kv_rotate<D>(x, a.turn, pos, i, [&](int ch, float* o) {
+  kv_widen8<T>(raw0, x);
+  kv_widen8<T>(raw1, x + 8);
+  const uint8_t* w = f.w.p ? f.w.p + h * f.w.head : nullptr;
+  float r = 1.f;
+  if (f.w.p) r = kv_norm<D>(x, w, a.dt, a.eps, i);
+  if (f.turned && (WAY != KV_PART || ok))
+    kv_turn<D, WAY, false>(x, a.turn, cs, pos, i, [&](int ch, float* o) {
       kv_widen8<T>(ldg<u32x4>(row + 16 * ch), o);
-      kv_weigh8(o, w, a.dt, ch, r);
+      if (w) kv_weigh8(o, w, a.dt, ch, r);
     });
+  if (f.out.p) {
+    if (!ok) return;
+    uint8_t* o = const_cast<uint8_t*>(f.out.p) + t * f.out.tok + h * f.out.head;
+    stg<u32x4>(o + 16 * i, kv_round8<T>(x));
+    stg<u32x4>(o + 16 * (i + L), kv_round8<T>(x + 8));
+  } else {
+    kv_keep<D, T, INT4>(x, a.c, f.side, h, slot, ok && slot >= 0 && slot < a.capacity, i);
   }
-  uint8_t* o = const_cast<uint8_t*>(s.y.p) + t * s.y.tok + h * s.y.head;
-  stg<u32x4>(o + 16 * i, kv_round8<T>(x));
-  stg<u32x4>(o + 16 * (i + L), kv_round8<T>(x + 8));
 }
 
-template <int D, int T>
+template <int D, int T, int WAY>
 __global__ __launch_bounds__(256) void k_qk_norm_back(const QkArgs a) {
   constexpr int L = D / 16, RB = 256 / L;
   const int i = threadIdx.x % L, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -61,7 +74,7 @@ __global__ __launch_bounds__(256) void k_qk_norm_back(const QkArgs a) {
   const bool is_q = (int)blockIdx.x < qb;
   const QkSide& s = is_q ? a.q : a.k;
   const int b = is_q ? blockIdx.x : blockIdx.x - qb, cls = b / s.blocks, slot = b % s.blocks;
-  const uint32_t per = s.classes == 1 ? s.heads : 1;  // heads of a token in this class
+  const uint32_t per = s.classes == 1 ? s.heads : 1;  // rows of a token in this class
   const int64_t rows = a.tokens * per;
   float w[16], dw[16];
   const uint8_t* wp = s.w.p + cls * s.w.head;
@@ -70,20 +83,23 @@ __global__ __launch_bounds__(256) void k_qk_norm_back(const QkArgs a) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) dw[e] = 0.f;
   for (int64_t n = (int64_t)slot * RB + threadIdx.x / L; n < rows; n += (int64_t)s.blocks * RB) {
-    const int64_t t = n >> 31 ? n / per : (uint32_t)n / per;
+    const int64_t t = n >> 31 ? n / per : (int64_t)((uint32_t)n / per);
     const int h = per == 1 ? cls : (int)(n - t * per);
-    const int64_t pos = a.turn.pos ? (int64_t)a.turn.pos[t] : 0;
-    if (a.turn.pos && (pos < 0 || pos >= a.turn.max_pos)) continue;
+    const int64_t pos = WAY ? (int64_t)a.turn.pos[t] : 0;
     const uint8_t* xp = s.x.p + t * s.x.tok + h * s.x.head;
     const uint8_t* dp = s.dy.p + t * s.dy.tok + h * s.dy.head;
+    const u32x4 x0 = ldg<u32x4>(xp + 16 * i), x1 = ldg<u32x4>(xp + 16 * (i + L));
+    const u32x4 g0 = ldg<u32x4>(dp + 16 * i), g1 = ldg<u32x4>(dp + 16 * (i + L));
+    if (WAY && (pos < 0 || pos >= a.turn.max_pos)) continue;
+    KvCs cs;
+    kv_load_cs<D, WAY>(cs, a.turn, pos, i);
     float x[16], g[16];
-    kv_widen8<T>(ldg<u32x4>(xp + 16 * i), x);
-    kv_widen8<T>(ldg<u32x4>(xp + 16 * (i + L)), x + 8);
-    kv_widen8<T>(ldg<u32x4>(dp + 16 * i), g);
-    kv_widen8<T>(ldg<u32x4>(dp + 16 * (i + L)), g + 8);
+    kv_widen8<T>(x0, x);
+    kv_widen8<T>(x1, x + 8);
+    kv_widen8<T>(g0, g);
+    kv_widen8<T>(g1, g + 8);
     const float r = kv_rms<D>(x, a.eps);
-    if (a.turn.pos)
-      kv_rotate<D, true>(g, a.turn, pos, i, [&](int ch, float* o) { kv_widen8<T>(ldg<u32x4>(dp + 16 * ch), o); });
+    kv_turn<D, WAY, true>(g, a.turn, cs, pos, i, [&](int ch, float* o) { kv_widen8<T>(ldg<u32x4>(dp + 16 * ch), o); });
     float dot = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -127,7 +143,13 @@ __global__ __launch_bounds__(1024) void k_qk_norm_join(const QkArgs a, int dim) 
   const int c = is_q ? cls : cls - a.q.classes;
   const float* p = a.part + ((int64_t)(is_q ? 0 : a.q.classes * a.q.blocks) + (int64_t)c * s.blocks) * dim + col;
   float v = 0.f;
-  for (int b = r; b < s.blocks; b += 64) v += p[(int64_t)b * dim];
+  for (int b0 = r; b0 < s.blocks; b0 += 64 * 8) {
+    float part[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[k] = p[(int64_t)min(b0 + 64 * k, s.blocks - 1) * dim];  // under way together
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v += b0 + 64 * k < s.blocks ? part[k] : 0.f;
+  }
   sw[r][threadIdx.x & 15] = v;
   __syncthreads();
   for (int m = 32; m; m >>= 1) {
@@ -148,6 +170,12 @@ int64_t qk_norm_split(QkArgs& a, int dim, int cus) {
       return;
     }
     const int64_t rows = a.tokens * s.heads, need = (rows / s.classes + rb - 1) / rb;
+    // a few turns of one block cost less than the joining kernel's launch (333 tokens, 2 x 24 heads of 64 with a weight
+    // each: 6 turns 9.7 us, against 6.2 and 3.0)
+    if (need <= 6) {
+      s.blocks = 1;
+      return;
+    }
     const int64_t share = (4 * (int64_t)cus * rows / all + s.classes - 1) / s.classes;
     s.blocks = (int)std::max<int64_t>(1, std::min(need, share));
   };
@@ -157,35 +185,66 @@ int64_t qk_norm_split(QkArgs& a, int dim, int cus) {
   return (int64_t)a.q.classes * a.q.blocks + (int64_t)a.k.classes * a.k.blocks;
 }
 
-hipError_t launch_qk_norm(QkArgs a, int dim, int dt, hipStream_t s) {
-  const int lanes = dim / 16, rb = 256 / lanes;
-  const int64_t per = a.q.heads + a.k.heads, most = kLaunchThreads / (per * lanes), tokens = a.tokens;
+static KvDiv kv_div_by(uint32_t d) {
+  int l = 0;
+  while ((1ull << l) < d) ++l;
+  if (l == 0) return {0, 1, 0};
+  // 2^(31 + l) / d rounded up is off by at most d 2^-(31 + l) of a quotient, less than 1 / d for n < 2^31
+  return {(uint32_t)((1ull << (31 + l)) / d + 1), d, l - 1};
+}
+
+template <int D, int T, bool INT4>
+static void forward_launch(const QkForwardArgs& a, dim3 grid, hipStream_t s) {
+  switch (kv_way(a.turn, D)) {
+    case KV_STILL: hipLaunchKernelGGL((k_qk_norm<D, T, INT4, KV_STILL>), grid, dim3(256), 0, s, a); break;
+    case KV_HALVES: hipLaunchKernelGGL((k_qk_norm<D, T, INT4, KV_HALVES>), grid, dim3(256), 0, s, a); break;
+    case KV_PAIRS: hipLaunchKernelGGL((k_qk_norm<D, T, INT4, KV_PAIRS>), grid, dim3(256), 0, s, a); break;
+    default: hipLaunchKernelGGL((k_qk_norm<D, T, INT4, KV_PART>), grid, dim3(256), 0, s, a);
+  }
+}
+
+// a: rows, divisions and blocks are set here
+hipError_t launch_qk_norm(const QkForwardArgs& args, const int (&heads)[3], int64_t tokens, int dim, int dt, bool int4,
+                          hipStream_t s) {
+  const int64_t rb = 256 / (dim / 16), per = (int64_t)heads[0] + heads[1] + heads[2];
+  const int64_t most = ((int64_t(1) << 31) - 1) / (per * (dim / 16));  // rows stay below 2^31, and so do threads
   for (int64_t t = 0; t < tokens; t += most) {
     const int64_t n = std::min(most, tokens - t);
-    const dim3 grid((unsigned)((n * per + rb - 1) / rb));
-    QkArgs b = a;
-    for (QkSide* x : {&b.q, &b.k}) {
-      x->x.p += t * x->x.tok;
-      x->y.p += t * x->y.tok;
+    QkForwardArgs a = args;
+    int64_t blocks = 0;
+    for (int k = 0; k < 3; ++k) {
+      QkForward& f = a.f[k];
+      f.rows = (uint32_t)(n * heads[k]);
+      f.blocks = (uint32_t)((n * heads[k] + rb - 1) / rb);
+      f.heads = kv_div_by(std::max(heads[k], 1));
+      f.in.p += t * f.in.tok;
+      if (f.out.p) f.out.p += t * f.out.tok;
+      blocks += f.blocks;
     }
-    if (b.turn.pos) b.turn.pos += t;
-    const uint32_t rows = (uint32_t)(n * per);
-    if (dim == 128 && dt == KV_BF16) hipLaunchKernelGGL((k_qk_norm<128, KV_BF16>), grid, dim3(256), 0, s, b, rows);
-    else if (dim == 128) hipLaunchKernelGGL((k_qk_norm<128, KV_F16>), grid, dim3(256), 0, s, b, rows);
-    else if (dt == KV_BF16) hipLaunchKernelGGL((k_qk_norm<64, KV_BF16>), grid, dim3(256), 0, s, b, rows);
-    else hipLaunchKernelGGL((k_qk_norm<64, KV_F16>), grid, dim3(256), 0, s, b, rows);
+    if (a.turn.pos) a.turn.pos += t;
+    if (a.slots) a.slots += t;
+    const dim3 grid((unsigned)blocks);
+    KV_PICK(forward_launch, dim, dt, int4, a, grid, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
+template <int D, int T>
+static void back_launch(const QkArgs& a, dim3 grid, hipStream_t s) {
+  switch (kv_way(a.turn, D)) {
+    case KV_STILL: hipLaunchKernelGGL((k_qk_norm_back<D, T, KV_STILL>), grid, dim3(256), 0, s, a); break;
+    case KV_HALVES: hipLaunchKernelGGL((k_qk_norm_back<D, T, KV_HALVES>), grid, dim3(256), 0, s, a); break;
+    case KV_PAIRS: hipLaunchKernelGGL((k_qk_norm_back<D, T, KV_PAIRS>), grid, dim3(256), 0, s, a); break;
+    default: hipLaunchKernelGGL((k_qk_norm_back<D, T, KV_PART>), grid, dim3(256), 0, s, a);
+  }
+}
+
 hipError_t launch_qk_norm_back(const QkArgs& a, int dim, int dt, hipStream_t s) {
   const dim3 grid((unsigned)(a.q.classes * a.q.blocks + a.k.classes * a.k.blocks));
-  if (dim == 128 && dt == KV_BF16) hipLaunchKernelGGL((k_qk_norm_back<128, KV_BF16>), grid, dim3(256), 0, s, a);
-  else if (dim == 128) hipLaunchKernelGGL((k_qk_norm_back<128, KV_F16>), grid, dim3(256), 0, s, a);
-  else if (dt == KV_BF16) hipLaunchKernelGGL((k_qk_norm_back<64, KV_BF16>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_qk_norm_back<64, KV_F16>), grid, dim3(256), 0, s, a);
+  if (dim == 128) dt == KV_BF16 ? back_launch<128, KV_BF16>(a, grid, s) : back_launch<128, KV_F16>(a, grid, s);
+  else dt == KV_BF16 ? back_launch<64, KV_BF16>(a, grid, s) : back_launch<64, KV_F16>(a, grid, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
   hipLaunchKernelGGL(k_qk_norm_join, dim3((unsigned)((a.q.classes + a.k.classes) * (dim / 16))), dim3(1024), 0, s, a, dim);

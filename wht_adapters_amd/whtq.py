@@ -79,7 +79,7 @@ _SIG = {
                      _vp],
     "qk_norm_rope_backward": [_vp, _i64_p, _vp, _i64_p, _i64, _vp, _i64_p, _vp, _i64_p, _i64, _int, _i64, _i64, _norm_p,
                               _rope_p, _vp, _i64_p, _vp, _i64_p, _vp, _vp, _vp, _i64, _vp],
-    "token_logprobs": [_vp, _int, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp],
+    "token_logprobs": [_vp, _int, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp],
     "token_logprobs_backward": [_vp, _int, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
     "kv_gather": [_cache_p, _i64, _vp, _vp, _i64_p, _vp, _i64_p, _int, _vp],
     "kv_attention": [_cache_p, _vp, _i64_p, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _f32,
@@ -990,13 +990,15 @@ def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_le
 class TokenLogprobs(NamedTuple):
     """Of rows of logits: float32 [rows] logprob (None without targets), lse
     and entropy; top_logprob float32 and top_id int64 [rows, top] (None for top
-    = 0).  lse_low is what rounding lse to float32 dropped, for the gradient."""
+    = 0).  row_ref (a logit near the row's largest) and row_sum (of the
+    exponentials relative to it) are for the gradient."""
     logprob: Optional[torch.Tensor]
     lse: torch.Tensor
     entropy: torch.Tensor
     top_logprob: Optional[torch.Tensor]
     top_id: Optional[torch.Tensor]
-    lse_low: torch.Tensor
+    row_ref: torch.Tensor
+    row_sum: torch.Tensor
 
 
 def _logits(name, t, dev=None, shape=None):
@@ -1031,8 +1033,8 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, workspace=None):
     ld = _logits("logits", logits)
     (rows, vocab), dev = logits.shape, logits.get_device()
     t_p = lp_p = None
-    out = torch.empty((4, rows), dtype=torch.float32, device=logits.device)
-    lse, low, entropy, logprob = out.unbind(0)
+    out = torch.empty((5, rows), dtype=torch.float32, device=logits.device)
+    lse, ref, total, entropy, logprob = out.unbind(0)
     if targets is not None:
         t_p, lp_p = _ints("targets", targets, torch.int64, dev, rows, "the logits'"), logprob.data_ptr()
     else:
@@ -1048,9 +1050,9 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, workspace=None):
     ws_p, wbytes = _workspace(workspace, dev, "the logits'")
     _check("token_logprobs", _on_device(
         dev, _lib.token_logprobs, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p, lp_p, lse.data_ptr(),
-        low.data_ptr(), entropy.data_ptr(), top, top_logprob.data_ptr() if top > 0 else None,
+        ref.data_ptr(), total.data_ptr(), entropy.data_ptr(), top, top_logprob.data_ptr() if top > 0 else None,
         top_id.data_ptr() if top > 0 else None, ws_p, wbytes))
-    return TokenLogprobs(logprob, lse, entropy, top_logprob, top_id, low)
+    return TokenLogprobs(logprob, lse, entropy, top_logprob, top_id, ref, total)
 
 
 def token_logprobs_backward(logits, targets, result, dlogprob=None, dentropy=None, *, scale=1.0, out=None):
@@ -1069,7 +1071,7 @@ def token_logprobs_backward(logits, targets, result, dlogprob=None, dentropy=Non
     of = lambda name, t: _row_floats(name, t, rows, dev) if t is not None else None
     _check("token_logprobs_backward", _on_device(
         dev, _lib.token_logprobs_backward, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p,
-        of("result.lse", result.lse), of("result.lse_low", result.lse_low), of("result.entropy", result.entropy),
+        of("result.row_ref", result.row_ref), of("result.row_sum", result.row_sum), of("result.entropy", result.entropy),
         of("dlogprob", dlogprob), of("dentropy", dentropy), out.data_ptr(), ldd))
     return out
 
