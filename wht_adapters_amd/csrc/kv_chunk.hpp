@@ -126,7 +126,21 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   // The split's share of the block's tiles: keys [kfirst, klast].  Sinks: tile
   // t of the walk is tile tile_of(t) of the sequence (kv_near); where there is
   // no gap, or in the sinks, the first tile counts from its first key.
-  const KvNear near = SINKS ? kv_near<KV_TILE>(a.sinks, first) : KvNear{};
+  // Where the keys that the window's first tile hides leave room for the sinks,
+  // they take their places there (guest: that tile's first key, with the first
+  // `guests` rows of it from the sequence's start): no tile of their own, 4 % of
+  // a prompt under a window of 1500, a quarter under one of 128.
+  constexpr int CR = 64 / CH;  // rows of one copy instruction (4 or 8; in one page)
+  KvNear near = SINKS ? kv_near<KV_TILE>(a.sinks, first) : KvNear{};
+  int guest = -1, guests = 0;
+  if constexpr (SINKS) {
+    const int far = near.tiles + near.gap, rows = INT4 ? a.sinks : (a.sinks + CR - 1) & ~(CR - 1);
+    if (near.gap > 0 && near.tiles == 1 && rows <= first - far * KV_TILE) {
+      near = {0, far};
+      guest = far * KV_TILE;
+      guests = rows;
+    }
+  }
   auto tile_of = [&](int t) KV_INLINE { return SINKS && t >= near.tiles ? t + near.gap : t; };
   int kfirst, klast, t0, t1;
   if constexpr (SINKS) {
@@ -215,7 +229,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
 
   // --- tile loads.  Keys outside [kfirst, klast] are replaced by the nearest
   // inside, so a tile holds only keys that some row sees.
-  constexpr int CR = 64 / CH;                  // rows of one copy instruction (4 or 8; in one page)
   constexpr int COPIES = KV_TILE / (CR * NW);  // copy instructions of a wave for K, and for V
   const int lr = lane / CH, pmask = (1 << a.c.page_shift) - 1;
   // a lane's 16 bytes among the rows of a copy; the swizzle depends on the
@@ -225,6 +238,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   const uint32_t kswz = 16 * kv_k_at<D>(trl, lane % CH), vswz = 16 * kv_v_at<D>(trl, lane % CH);
   const uint32_t ktok = (uint32_t)a.c.k.tok, vtok = (uint32_t)a.c.v.tok;
   auto copy_key = [&](int n, int key0) KV_INLINE {  // first key of copy n, wave-uniform for a given n
+    if (SINKS && key0 == guest && (n * NW + wave) * CR < guests) return (n * NW + wave) * CR;
     return min(max(key0 + (n * NW + wave) * CR, kfirst & ~(CR - 1)), klast & ~(CR - 1));
   };
   const uint32_t klane = lr * ktok + kswz, vlane = lr * vtok + vswz;
@@ -254,7 +268,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
 #pragma unroll
       for (int n = 0; n < COPIES; ++n) {
         const int k0 = copy_key(n, key0);
-        const uint32_t r = min(max(lr, kfirst - k0), klast - k0);
+        const bool is_guest = SINKS && key0 == guest && (n * NW + wave) * CR < guests;
+        const uint32_t r = is_guest ? lr : min(max(lr, kfirst - k0), klast - k0);
         go(0, n, r * ktok + kswz);
         go(1, n, r * vtok + vswz);
       }
@@ -270,6 +285,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   auto unit_of_v = [&](int n) KV_INLINE { return n * NW + wave >= UNITS / 64; };  // wave-uniform
   auto has_unit = [&](int n) KV_INLINE { return n * NW + wave < UNITS / 32; };
   auto inside = [&](int key) KV_INLINE {
+    if (SINKS && guest >= 0 && key >= guest && key - guest < guests) return key - guest;
     key = min(max(key, kfirst), klast);
     // a key that no row sees, between the sinks and the window: its scale must not set the outputs' unit
     if (SINKS && key >= a.sinks && key < first) key = a.sinks - 1;
@@ -348,7 +364,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   const int high = a.causal ? min(klast, pos) : klast;
   const uint32_t span = high < low ? 0u : (uint32_t)(high - low);
   if (high < low) low = INT32_MAX;  // none
-  const int near_end = SINKS ? min(a.sinks, high + 1) : 0;  // and of the sinks, those below this
+  // and of the sinks, those below this (guests: every row's position is beyond them)
+  const int near_end = !SINKS ? 0 : guest >= 0 ? guest + a.sinks : min(a.sinks, high + 1);
   auto sees = [&](int key) KV_INLINE { return (uint32_t)(key - low) <= span || (SINKS && key < near_end); };
   // A probability of 0 does not hide a value that is not finite, so in a
   // tile that some row does not see whole such values are taken out: the
@@ -550,7 +567,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
   auto masked = [&](const Range& r, int t) KV_INLINE {
     return (t < r.f0 && !(SINKS && (t + 1) * KV_TILE <= a.sinks)) || t >= r.f1;
   };
-  auto seen = [&](const Range& r, int t) KV_INLINE { return (t >= r.n0 || (SINKS && t * KV_TILE < a.sinks)) && t <= r.n1; };
+  auto seen = [&](const Range& r, int t) KV_INLINE {
+    return (t >= r.n0 || (SINKS && (t * KV_TILE < a.sinks || t * KV_TILE == guest))) && t <= r.n1;
+  };
   constexpr std::false_type B0{};
   constexpr std::true_type B1{};
   f32x16 s[KB];

@@ -701,8 +701,14 @@ def kv_cache_alloc(num_pages, page_size, kv_heads, dim, *, int4=False, dtype=tor
     return KVCache(*codes, *scales, signs)
 
 
+_NORM_DT = frozenset((torch.float32, torch.bfloat16, torch.float16))
 _pair = functools.lru_cache(maxsize=1024)(lambda a, b: (_i64 * 2)(a, b))  # strides as the library takes them
 _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _rows_like(t):
+    """A new contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _on_device(dev, f, *args):
@@ -754,13 +760,13 @@ def _rope_arg(cos, sin, positions, rot_dim, interleaved, tokens, dev, whose):
     if cos is None and sin is None and positions is None:
         return None
     for nm, t in (("cos", cos), ("sin", sin)):
-        if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.dim() != 2 or \
-                t.stride(1) != 1 or t.get_device() != dev:
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.dim() != 2 or t.get_device() != dev:
             raise ValueError(f"{nm} must be a float32 [positions, rot_dim / 2] tensor with a contiguous last "
                              f"dimension on {whose} device")
-    rows, half = cos.shape
-    ld = cos.stride(0)
-    if sin.shape != cos.shape or sin.stride(0) != ld:
+    (rows, half), (ld, one) = cos.shape, cos.stride()
+    if one != 1:
+        raise ValueError("cos and sin must have a contiguous last dimension")
+    if sin.shape != (rows, half) or sin.stride() != (ld, 1):
         raise ValueError("cos and sin must have one shape and layout")
     rot = 2 * half if rot_dim is None else int(rot_dim)
     if rot > 2 * half:
@@ -771,25 +777,23 @@ def _rope_arg(cos, sin, positions, rot_dim, interleaved, tokens, dev, whose):
 
 def _norm_arg(q_norm, k_norm, eps, heads, kv_heads, dim, dev, whose):
     """The norms of a call: weights [dim], or [heads, dim] for one a head."""
-    n = _Norm(eps=eps)
-    for nm, t, h in (("q_norm", q_norm, heads), ("k_norm", k_norm, kv_heads)):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in (torch.float32, torch.bfloat16, torch.float16):
-            raise ValueError(f"{nm} must be a float32, bfloat16 or float16 tensor on {whose} device")
-        shape, st = t.shape, t.stride()
-        if (shape != (dim,) and shape != (h, dim)) or st[-1] != 1:
-            raise ValueError(f"{nm} must be [{dim}] or [{h}, {dim}] with a contiguous last dimension")
-        if q_norm is not None and k_norm is not None and q_norm.dtype is not k_norm.dtype:
-            raise ValueError("q_norm and k_norm must have one dtype")
-        n.dtype = _DT[t.dtype]
-        # (a stride of 0 would say that all heads share one vector)
-        head = 0 if len(shape) == 1 else st[0] if h > 1 else dim
-        if nm == "q_norm":
-            n.q, n.q_head = t.data_ptr(), head
-        else:
-            n.k, n.k_head = t.data_ptr(), head
-    return n
+    if q_norm is not None and k_norm is not None and q_norm.dtype is not k_norm.dtype:
+        raise ValueError("q_norm and k_norm must have one dtype")
+    q_p, q_head = _norm_weight("q_norm", q_norm, heads, dim, dev, whose)
+    k_p, k_head = _norm_weight("k_norm", k_norm, kv_heads, dim, dev, whose)
+    return _Norm(q_p, k_p, q_head, k_head, _DT[(k_norm if q_norm is None else q_norm).dtype], eps)
+
+
+def _norm_weight(name, t, heads, dim, dev, whose):
+    if t is None:
+        return 0, 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in _NORM_DT:
+        raise ValueError(f"{name} must be a float32, bfloat16 or float16 tensor on {whose} device")
+    shape, st = t.shape, t.stride()
+    if (shape != (dim,) and shape != (heads, dim)) or st[-1] != 1:
+        raise ValueError(f"{name} must be [{dim}] or [{heads}, {dim}] with a contiguous last dimension")
+    # (a stride of 0 says that all heads share one vector)
+    return t.data_ptr(), 0 if len(shape) == 1 else st[0] if heads > 1 else dim
 
 
 def kv_append(cache, k, v, slots, *, q=None, cos=None, sin=None, positions=None, rot_dim=None, interleaved=False,
@@ -813,7 +817,7 @@ def kv_append(cache, k, v, slots, *, q=None, cos=None, sin=None, positions=None,
         heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
         qs = _head_rows("q", q, cache, tokens, heads, dtype)
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = _rows_like(q)
         qos = _head_rows("q_out", q_out, cache, tokens, heads, dtype)
         q_p, qo_p = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
@@ -856,8 +860,8 @@ def qk_norm_rope(q, k, *, q_norm, k_norm, norm_eps=1e-6, cos=None, sin=None, pos
     work in place."""
     dtype, dev, tokens, heads, kv_heads, dim, rows, qs, ks, norm, rope = _qk_call(
         q, k, q_norm, k_norm, norm_eps, cos, sin, positions, rot_dim, interleaved)
-    q_out = torch.empty(q.shape, dtype=dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=dtype, device=q.device) if k_out is None else k_out
+    q_out = _rows_like(q) if q_out is None else q_out
+    k_out = _rows_like(k) if k_out is None else k_out
     qos, kos = rows("q_out", q_out, heads), rows("k_out", k_out, kv_heads)
     _check("qk_norm_rope", _on_device(dev, _lib.qk_norm_rope, q.data_ptr(), qs, heads, k.data_ptr(), ks, kv_heads,
                                       _DT[dtype], dim, tokens, norm, rope, q_out.data_ptr(), qos, k_out.data_ptr(), kos))
@@ -877,14 +881,12 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, *, q_norm, k_norm, norm_eps=1e-6
         if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) == 0:
             raise ValueError(f"{nm} is one vector expanded over the heads: pass it as [dim], its gradient is one vector too")
     dqos, dkos = rows("dq_out", dq_out, heads), rows("dk_out", dk_out, kv_heads)
-    dq = torch.empty(q.shape, dtype=dtype, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=dtype, device=q.device) if dk is None else dk
+    dq = _rows_like(q) if dq is None else dq
+    dk = _rows_like(k) if dk is None else dk
     dqs, dks = rows("dq", dq, heads), rows("dk", dk, kv_heads)
-    dwq = torch.empty(q_norm.shape, dtype=torch.float32, device=q.device)
-    dwk = torch.empty(k_norm.shape, dtype=torch.float32, device=q.device)
+    dwq, dwk = (torch.empty_like(t, dtype=torch.float32, memory_format=torch.contiguous_format) for t in (q_norm, k_norm))
     if workspace is None:
-        need = _on_device(dev, lambda *a: _lib.qk_norm_rope_backward_workspace_bytes(*a[:-1]), heads, kv_heads, dim, tokens,
-                          norm)
+        need = _bytes(dev, _lib.qk_norm_rope_backward_workspace_bytes, heads, kv_heads, dim, tokens, norm)
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_p, wbytes = _workspace(workspace, dev, "q's")
@@ -899,6 +901,14 @@ def qk_norm_rope_backward_workspace_bytes(q, k, *, q_norm, k_norm):
     norm = _norm_arg(q_norm, k_norm, 0.0, q.shape[1], k.shape[1], q.shape[2], q.get_device(), "q's")
     with torch.cuda.device(q.device):
         return int(_lib.qk_norm_rope_backward_workspace_bytes(q.shape[1], k.shape[1], q.shape[2], q.shape[0], norm))
+
+
+def _bytes(dev, f, *args):
+    """f(*args), a workspace's size on device `dev`."""
+    if torch.cuda.current_device() == dev:
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
 
 
 def _workspace(t, dev, whose):
@@ -966,7 +976,7 @@ def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_le
     if heads % cache.kv_heads:
         raise ValueError("q's heads must be a multiple of the cache's")
     if out is None:
-        out = q.new_empty(q.shape)
+        out = _rows_like(q)
     outs = _head_rows("out", out, cache, tokens, heads, dtype)
     lse_p = None
     if lse is not None:
@@ -975,8 +985,8 @@ def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_le
             raise ValueError("lse must be a contiguous float32 [tokens, heads] tensor on the cache's device")
         lse_p = lse.data_ptr()
     if workspace is None:
-        need = _on_device(dev, lambda *a: _lib.kv_attention_sinks_workspace_bytes(*a[:-1]), cache._c, tokens, heads, seqs,
-                          max_q_len, max_kv_len, window, sinks)
+        need = _bytes(dev, _lib.kv_attention_sinks_workspace_bytes, cache._c, tokens, heads, seqs, max_q_len, max_kv_len,
+                      window, sinks)
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_p, wbytes = _workspace(workspace, dev, "the cache's")
@@ -1044,7 +1054,7 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, workspace=None):
         top_logprob = torch.empty((rows, top), dtype=torch.float32, device=logits.device)
         top_id = torch.empty((rows, top), dtype=torch.int64, device=logits.device)
     if workspace is None:
-        need = _on_device(dev, lambda *a: _lib.token_logprobs_workspace_bytes(*a[:-1]), rows, vocab, top)
+        need = _bytes(dev, _lib.token_logprobs_workspace_bytes, rows, vocab, top)
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
     ws_p, wbytes = _workspace(workspace, dev, "the logits'")
