@@ -33,6 +33,10 @@ def make(rng, rows, vocab, dtype, offset=0, spread=3.0):
     return x, wide[:, offset:offset + vocab]
 
 
+def parts(r):
+    return r.logprob, r.lse, r.entropy, r.row_ref, r.row_sum, r.top_logprob, r.top_id
+
+
 def slack(x, scale):
     """Bounds of fp32 over a row: of the sum S (relative), and the mean of |z - max| under p."""
     z = x * scale
@@ -201,7 +205,7 @@ def test_rows_do_not_depend_on_the_call(W):
     x, xd = make(rng, 2100, 9001, torch.bfloat16)
     t = torch.from_numpy(rng.integers(0, 9001, 2100)).to(DEV)
     a, b = W.token_logprobs(xd, t, top=6), W.token_logprobs(xd, t, top=6)
-    for u, v in zip(a, b):
+    for u, v in zip(parts(a), parts(b)):
         assert torch.equal(u, v)
     one = W.token_logprobs(xd[77:78], t[77:78], top=6)
     assert torch.equal(one.top_id[0], a.top_id[77])
@@ -282,7 +286,7 @@ def test_captured_and_replayed(W):
         graph.replay()
         torch.cuda.synchronize()
         r, d = step()
-        for u, v in zip(kept, r):
+        for u, v in zip(parts(kept), parts(r)):
             assert torch.equal(u, v)
         assert torch.equal(dx, d)
 
@@ -297,10 +301,13 @@ def test_refusals(W):
         W.token_logprobs(x, t.int())
     with pytest.raises(ValueError):
         W.token_logprobs(x, t[:1])
-    for kw in (dict(top=11), dict(top=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-               dict(top=3, workspace=torch.empty(4, dtype=torch.uint8, device=DEV))):
+    for kw in (dict(top=11), dict(top=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan"))):
         with pytest.raises(W.WhtqError):
             W.token_logprobs(x, t, **kw)
+    long = torch.zeros((2, 50000), device=DEV)  # few long rows are split over blocks
+    assert W.token_logprobs_workspace_bytes(2, 50000, 3) > 16
+    with pytest.raises(W.WhtqError):
+        W.token_logprobs(long, t, top=3, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     r = W.token_logprobs(x, t)
     g = torch.zeros(2, device=DEV)
     with pytest.raises(W.WhtqError):

@@ -1224,8 +1224,11 @@ LpPlan lp_plan(int64_t rows, int64_t vocab, int64_t top, int cus) {
     p.width = vocab <= 4096 ? 8 : vocab <= 32768 ? 64 : LP_CHUNK;
     p.groups = (int)((vocab + 7 + p.width - 1) / p.width);  // (7: a row may begin inside 16 bytes)
   }
-  if (p.splits > 1 || top) p.parts = rows * p.splits * 3;
-  p.bytes = (p.parts + rows * p.groups) * 4;
+  // a block that has all of its row keeps both to itself
+  if (p.splits > 1) {
+    p.parts = rows * p.splits * 3;
+    p.bytes = (p.parts + rows * p.groups) * 4;
+  }
   return p;
 }
 

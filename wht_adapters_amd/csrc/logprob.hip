@@ -175,108 +175,6 @@ __device__ __forceinline__ void lp_finish(const LpArgs& a, int64_t row, const Lp
   }
 }
 
-// A block's share of a row: chunks c, c + 4, .. by each of its waves.
-// LANES > 0: the maxima of groups of as many lanes' logits are kept.
-template <int DT, int LANES>
-__global__ __launch_bounds__(256) void k_lp_row(const LpArgs a) {
-  constexpr int AHEAD = DT == DT_F32 ? 2 : 4;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x % (uint32_t)a.splits;
-  const int64_t row = a.row0 + blockIdx.x / (uint32_t)a.splits;
-  const LpRow x = lp_row<DT>(a.x + row * a.ld, a.vocab);
-  const int chunks = (x.end + LP_CHUNK - 1) / LP_CHUNK, first = x.pad > 0, whole = x.end / LP_CHUNK;  // [first, whole) are whole
-  const int c0 = (int)((int64_t)chunks * split / a.splits), c1 = (int)((int64_t)chunks * (split + 1) / a.splits);
-  const float c = a.scale * LP_LOG2E, lag = fminf(LP_LAG / c, 1e30f);
-  LpSum r{LP_NEG_INF, 0.f, 0.f};
-  Lp8 buf[AHEAD];
-  auto take = [&](const Lp8& w, int ch) __attribute__((always_inline)) {
-    float f[8];
-    lp_widen<DT>(w, f);
-    const float top = lp_max8(f);
-    if constexpr (LANES > 0) {
-      float most = top;
-      if (__any(top != top)) {  // a NaN counts as -inf in the order
-        most = LP_NEG_INF;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) most = f[e] > most ? f[e] : most;
-      }
-      uint32_t k = lp_key(most);
-      if constexpr (LANES == 64) {
-        k = wave_max_u32(k);
-        if (lane == 0) a.best[row * a.groups + ch] = k;
-      } else {
-#pragma unroll
-        for (int m = 1; m < LANES; m *= 2) k = max(k, (uint32_t)__shfl_xor((int)k, m, 64));
-        const int g = (ch * 64 + lane) / LANES;
-        if (lane % LANES == 0 && g < a.groups) a.best[row * a.groups + g] = k;
-      }
-    }
-    if (__any(top > r.m + lag)) {
-      const float m = fmaxf(r.m, top);
-      if (r.m == LP_NEG_INF) {
-        r.m = m;
-      } else if (m > r.m) {
-        const float d = fmaxf((r.m - m) * c, LP_LEAST), f2 = __builtin_amdgcn_exp2f(d);
-        r.t = f2 * (r.t + d * r.s);
-        r.s *= f2;
-        r.m = m;
-      }
-    }
-    const float base = r.m == LP_NEG_INF ? 0.f : r.m;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float z = (f[e] - base) * c, p = __builtin_amdgcn_exp2f(z);
-      r.s += p;
-      r.t = __builtin_fmaf(p, fmaxf(z, LP_LEAST), r.t);
-    }
-  };
-  // Whole chunks, each loaded AHEAD of its use; no branch between a load and
-  // its use but at the end, so that every wait is for one load alone.
-  auto load = [&](Lp8& w, int ch) __attribute__((always_inline)) { lp_load8<DT, true, true>(x.p, ch * LP_CHUNK + 8 * lane, w); };
-  const int start = max(c0, first), end = min(c1, whole);
-  int ch = start + wave;
-  if (start < end) {
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) load(buf[u], min(ch + 4 * u, end - 1));
-  }
-  for (; ch + 4 * (2 * AHEAD - 1) < end; ch += 4 * AHEAD)
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      take(buf[u], ch + 4 * u);
-      load(buf[u], ch + 4 * (u + AHEAD));
-    }
-#pragma unroll
-  for (int v = 0; v < 2; ++v, ch += 4 * AHEAD)
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      if (ch + 4 * u < end) take(buf[u], ch + 4 * u);
-      if (v == 0 && ch + 4 * (u + AHEAD) < end) load(buf[u], ch + 4 * (u + AHEAD));
-    }
-  // the chunks at the row's ends (one, where it is short)
-#pragma unroll 1
-  for (int e = 0; e < 2; ++e) {
-    const int at = e ? whole : 0;
-    if (e ? whole == chunks || (first && whole == 0) : !first) continue;
-    if (at < c0 || at >= c1 || (at + e) % 4 != wave) continue;
-    lp_load_edge<DT>(x, at * LP_CHUNK + 8 * lane, buf[0]);
-    take(buf[0], at);
-  }
-  r = lp_lanes<64>(r, c);
-  __shared__ LpSum sw[4];
-  if (lane == 0) sw[wave] = r;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    r = lp_add(lp_add(sw[0], sw[1], c), lp_add(sw[2], sw[3], c), c);
-    if (a.splits == 1) lp_finish<DT>(a, row, r);
-    if (a.splits > 1 || LANES > 0) {
-      float* p = a.part + (row * a.splits + split) * 3;
-      p[0] = r.m;
-      p[1] = r.s;
-      p[2] = r.t;
-    }
-  }
-}
-
 // A row's shares joined, by a wave.
 __device__ __forceinline__ LpSum lp_shares(const LpArgs& a, int64_t row, int lane) {
   const float c = a.scale * LP_LOG2E;
@@ -354,9 +252,10 @@ __device__ __forceinline__ uint32_t lp_pick(const uint32_t* best, int kept, int 
   return bar;
 }
 
-// A row whose likeliest tokens are asked for, a block a row.
-template <int DT>
-__global__ __launch_bounds__(256) void k_lp_top(const LpArgs a) {
+// A row's likeliest tokens, by a block, from the maxima `best` of its groups.
+// `sums` gives the row's sums, in one wave.
+template <int DT, typename Sums>
+__device__ __forceinline__ void lp_tops(const LpArgs& a, int64_t row, const LpRow& x, const uint32_t* best, Sums sums) {
   constexpr int CAP = 256, VECS = 128;  // candidates ranked at once, vectors that may hold any
   constexpr int MOST = 4;  // vectors of a thread under way (8 and fewer blocks a CU: 2047 rows 11.9 us against 9.4)
   __shared__ int pick[LP_MOST_TOP];
@@ -367,22 +266,19 @@ __global__ __launch_bounds__(256) void k_lp_top(const LpArgs a) {
   __shared__ int vectors, count;
   __shared__ float sm, sls;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = a.row0 + blockIdx.x;
-  const LpRow x = lp_row<DT>(a.x + row * a.ld, a.vocab);
   const int kept = (x.end + a.width - 1) / a.width;  // at most a.groups
   const int merge = kept <= 512 ? 1 : (kept + 511) / 512, groups = merge == 1 ? kept : (kept + merge - 1) / merge;
   const int n = min(a.top, groups);
   if (threadIdx.x == 0) vectors = count = 0;
   if (wave == 0) {
-    const uint32_t* best = a.best + row * a.groups;
     const uint32_t reach = groups <= 64 ? lp_pick<1>(best, kept, merge, groups, n, lane, pick)
                           : groups <= 256 ? lp_pick<4>(best, kept, merge, groups, n, lane, pick)
                                           : lp_pick<8>(best, kept, merge, groups, n, lane, pick);
     if (lane == 0) bar = n == a.top ? reach : 0u;
   } else if (wave == 1) {
-    const LpSum r = lp_shares(a, row, lane);
+    const LpSum r = sums(lane);
     if (lane == 0) {
-      if (a.splits > 1) lp_finish<DT>(a, row, r);
+      lp_finish<DT>(a, row, r);
       sm = r.s == 0.f ? 0.f : r.m;
       sls = r.s == 0.f ? 0.f : logf(r.s);
     }
@@ -494,6 +390,122 @@ __global__ __launch_bounds__(256) void k_lp_top(const LpArgs a) {
   }
 }
 
+template <int DT>
+__global__ __launch_bounds__(256) void k_lp_top(const LpArgs a) {
+  const int64_t row = a.row0 + blockIdx.x;
+  lp_tops<DT>(a, row, lp_row<DT>(a.x + row * a.ld, a.vocab), a.best + row * a.groups,
+              [&](int lane) { return lp_shares(a, row, lane); });
+}
+
+// A block's share of a row: chunks c, c + 4, .. by each of its waves.
+// LANES > 0: the maxima of groups of as many lanes' logits are kept.  WHOLE:
+// the block has all of its row and goes on to the likeliest tokens itself.
+template <int DT, int LANES, bool WHOLE>
+__global__ __launch_bounds__(256, WHOLE ? 8 : 1) void k_lp_row(const LpArgs a) {
+  constexpr int AHEAD = DT == DT_F32 ? 2 : 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.x % (uint32_t)a.splits;
+  const int64_t row = a.row0 + blockIdx.x / (uint32_t)a.splits;
+  const LpRow x = lp_row<DT>(a.x + row * a.ld, a.vocab);
+  const int chunks = (x.end + LP_CHUNK - 1) / LP_CHUNK, first = x.pad > 0, whole = x.end / LP_CHUNK;  // [first, whole) are whole
+  const int c0 = (int)((int64_t)chunks * split / a.splits), c1 = (int)((int64_t)chunks * (split + 1) / a.splits);
+  const float c = a.scale * LP_LOG2E, lag = fminf(LP_LAG / c, 1e30f);
+  __shared__ uint32_t mine[WHOLE ? LP_MOST_GROUPS : 1];
+  uint32_t* best = WHOLE ? mine : a.best + row * a.groups;
+  LpSum r{LP_NEG_INF, 0.f, 0.f};
+  Lp8 buf[AHEAD];
+  auto take = [&](const Lp8& w, int ch) __attribute__((always_inline)) {
+    float f[8];
+    lp_widen<DT>(w, f);
+    const float top = lp_max8(f);
+    if constexpr (LANES > 0) {
+      float most = top;
+      if (__any(top != top)) {  // a NaN counts as -inf in the order
+        most = LP_NEG_INF;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = f[e] > most ? f[e] : most;
+      }
+      uint32_t k = lp_key(most);
+      if constexpr (LANES == 64) {
+        k = wave_max_u32(k);
+        if (lane == 0) best[ch] = k;
+      } else {
+#pragma unroll
+        for (int m = 1; m < LANES; m *= 2) k = max(k, (uint32_t)__shfl_xor((int)k, m, 64));
+        const int g = (ch * 64 + lane) / LANES;
+        if (lane % LANES == 0 && g < a.groups) best[g] = k;
+      }
+    }
+    if (__any(top > r.m + lag)) {
+      const float m = fmaxf(r.m, top);
+      if (r.m == LP_NEG_INF) {
+        r.m = m;
+      } else if (m > r.m) {
+        const float d = fmaxf((r.m - m) * c, LP_LEAST), f2 = __builtin_amdgcn_exp2f(d);
+        r.t = f2 * (r.t + d * r.s);
+        r.s *= f2;
+        r.m = m;
+      }
+    }
+    const float base = r.m == LP_NEG_INF ? 0.f : r.m;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float z = (f[e] - base) * c, p = __builtin_amdgcn_exp2f(z);
+      r.s += p;
+      r.t = __builtin_fmaf(p, fmaxf(z, LP_LEAST), r.t);
+    }
+  };
+  // Whole chunks, each loaded AHEAD of its use; no branch between a load and
+  // its use but at the end, so that every wait is for one load alone.
+  auto load = [&](Lp8& w, int ch) __attribute__((always_inline)) { lp_load8<DT, true, true>(x.p, ch * LP_CHUNK + 8 * lane, w); };
+  const int start = max(c0, first), end = min(c1, whole);
+  int ch = start + wave;
+  if (start < end) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) load(buf[u], min(ch + 4 * u, end - 1));
+  }
+  for (; ch + 4 * (2 * AHEAD - 1) < end; ch += 4 * AHEAD)
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      take(buf[u], ch + 4 * u);
+      load(buf[u], ch + 4 * (u + AHEAD));
+    }
+#pragma unroll
+  for (int v = 0; v < 2; ++v, ch += 4 * AHEAD)
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (ch + 4 * u < end) take(buf[u], ch + 4 * u);
+      if (v == 0 && ch + 4 * (u + AHEAD) < end) load(buf[u], ch + 4 * (u + AHEAD));
+    }
+  // the chunks at the row's ends (one, where it is short)
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    const int at = e ? whole : 0;
+    if (e ? whole == chunks || (first && whole == 0) : !first) continue;
+    if (at < c0 || at >= c1 || (at + e) % 4 != wave) continue;
+    lp_load_edge<DT>(x, at * LP_CHUNK + 8 * lane, buf[0]);
+    take(buf[0], at);
+  }
+  r = lp_lanes<64>(r, c);
+  __shared__ LpSum sw[4];
+  if (lane == 0) sw[wave] = r;
+  __syncthreads();
+  auto sums = [&](int) { return lp_add(lp_add(sw[0], sw[1], c), lp_add(sw[2], sw[3], c), c); };
+  if constexpr (WHOLE) {
+    lp_tops<DT>(a, row, x, best, sums);
+  } else if (threadIdx.x == 0) {
+    r = sums(0);
+    if (a.splits == 1) {
+      lp_finish<DT>(a, row, r);
+    } else {
+      float* p = a.part + (row * a.splits + split) * 3;
+      p[0] = r.m;
+      p[1] = r.s;
+      p[2] = r.t;
+    }
+  }
+}
+
 // d logits = scale (g (onehot - p) - h p (log p + H)), with p = e / S and
 // log p = z - log S: e times a line in z, whose two numbers a row has.
 template <int DT>
@@ -564,12 +576,17 @@ hipError_t rows_launch(LpArgs a, hipStream_t s) {
   for (a.row0 = 0; a.row0 < a.rows; a.row0 += most) {
     const int64_t n = std::min(a.rows - a.row0, most);
     const dim3 grid((unsigned)(n * a.splits));
-    if (!a.top) hipLaunchKernelGGL((k_lp_row<DT, 0>), grid, dim3(256), 0, s, a);
-    else if (a.width == 8) hipLaunchKernelGGL((k_lp_row<DT, 1>), grid, dim3(256), 0, s, a);
-    else if (a.width == 64) hipLaunchKernelGGL((k_lp_row<DT, 8>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_lp_row<DT, 64>), grid, dim3(256), 0, s, a);
+    const bool whole = a.top && a.splits == 1;
+    if (!a.top) hipLaunchKernelGGL((k_lp_row<DT, 0, false>), grid, dim3(256), 0, s, a);
+    else if (whole && a.width == 8) hipLaunchKernelGGL((k_lp_row<DT, 1, true>), grid, dim3(256), 0, s, a);
+    else if (whole && a.width == 64) hipLaunchKernelGGL((k_lp_row<DT, 8, true>), grid, dim3(256), 0, s, a);
+    else if (whole) hipLaunchKernelGGL((k_lp_row<DT, 64, true>), grid, dim3(256), 0, s, a);
+    else if (a.width == 8) hipLaunchKernelGGL((k_lp_row<DT, 1, false>), grid, dim3(256), 0, s, a);
+    else if (a.width == 64) hipLaunchKernelGGL((k_lp_row<DT, 8, false>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_lp_row<DT, 64, false>), grid, dim3(256), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (whole) continue;
     if (a.top) {
       hipLaunchKernelGGL((k_lp_top<DT>), dim3((unsigned)n), dim3(256), 0, s, a);
     } else if (a.splits > 1) {

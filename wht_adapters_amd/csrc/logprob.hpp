@@ -8,6 +8,7 @@ namespace whtq {
 
 constexpr int LP_MOST_VOCAB = 1 << 20, LP_MOST_TOP = 32;  // (WHTQ_TOP_MOST)
 constexpr int LP_CHUNK = 512;  // logits a wave takes at a time, 8 a lane
+constexpr int LP_MOST_GROUPS = (LP_MOST_VOCAB + 7) / LP_CHUNK + 1;  // of a row
 
 struct LpArgs {
   const uint8_t* x;

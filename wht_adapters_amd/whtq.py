@@ -9,7 +9,7 @@ import ctypes
 import dataclasses
 import functools
 import os
-from typing import NamedTuple, Optional
+from typing import Optional
 
 import torch
 
@@ -997,18 +997,28 @@ def kv_attention(cache, q, q_start, kv_len, block_table, *, max_q_len, max_kv_le
     return out
 
 
-class TokenLogprobs(NamedTuple):
+class TokenLogprobs:
     """Of rows of logits: float32 [rows] logprob (None without targets), lse
     and entropy; top_logprob float32 and top_id int64 [rows, top] (None for top
     = 0).  row_ref (a logit near the row's largest) and row_sum (of the
     exponentials relative to it) are for the gradient."""
-    logprob: Optional[torch.Tensor]
-    lse: torch.Tensor
-    entropy: torch.Tensor
-    top_logprob: Optional[torch.Tensor]
-    top_id: Optional[torch.Tensor]
-    row_ref: torch.Tensor
-    row_sum: torch.Tensor
+    __slots__ = ("_buf", "_at", "_n", "_targets", "top_logprob", "top_id")
+
+    def __init__(self, buf, at, rows, targets, top_logprob, top_id):
+        self._buf, self._at, self._n, self._targets = buf, at, rows, targets
+        self.top_logprob, self.top_id = top_logprob, top_id
+
+    def _row(self, i):  # parts of one tensor, taken out when they are asked for
+        return self._buf[self._at + i * self._n:self._at + (i + 1) * self._n]
+
+    lse = property(lambda self: self._row(0))
+    row_ref = property(lambda self: self._row(1))
+    row_sum = property(lambda self: self._row(2))
+    entropy = property(lambda self: self._row(3))
+    logprob = property(lambda self: self._row(4) if self._targets else None)
+
+    def _ptr(self, i):
+        return self._buf.data_ptr() + 4 * (self._at + i * self._n)
 
 
 def _logits(name, t, dev=None, shape=None):
@@ -1042,27 +1052,24 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, workspace=None):
     TokenLogprobs."""
     ld = _logits("logits", logits)
     (rows, vocab), dev = logits.shape, logits.get_device()
-    t_p = lp_p = None
-    out = torch.empty((5, rows), dtype=torch.float32, device=logits.device)
-    lse, ref, total, entropy, logprob = out.unbind(0)
+    t_p = None
     if targets is not None:
-        t_p, lp_p = _ints("targets", targets, torch.int64, dev, rows, "the logits'"), logprob.data_ptr()
-    else:
-        logprob = None
-    top_logprob = top_id = None
+        t_p = _ints("targets", targets, torch.int64, dev, rows, "the logits'")
+    top_logprob = top_id = top_lp = top_ip = None
     if top > 0:
         top_logprob = torch.empty((rows, top), dtype=torch.float32, device=logits.device)
         top_id = torch.empty((rows, top), dtype=torch.int64, device=logits.device)
-    if workspace is None:
-        need = _bytes(dev, _lib.token_logprobs_workspace_bytes, rows, vocab, top)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
-    ws_p, wbytes = _workspace(workspace, dev, "the logits'")
+        top_lp, top_ip = top_logprob.data_ptr(), top_id.data_ptr()
+    need = _bytes(dev, _lib.token_logprobs_workspace_bytes, rows, vocab, top) if workspace is None else 0
+    # a workspace of few rows (a fraction of the logits) and the results in one tensor
+    at = max(need, 0) // 4
+    buf = torch.empty(at + 5 * rows, dtype=torch.float32, device=logits.device)
+    ws_p, wbytes = _workspace(workspace, dev, "the logits'") if need == 0 else (buf.data_ptr(), need)
+    r = TokenLogprobs(buf, at, rows, t_p is not None, top_logprob, top_id)
     _check("token_logprobs", _on_device(
-        dev, _lib.token_logprobs, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p, lp_p, lse.data_ptr(),
-        ref.data_ptr(), total.data_ptr(), entropy.data_ptr(), top, top_logprob.data_ptr() if top > 0 else None,
-        top_id.data_ptr() if top > 0 else None, ws_p, wbytes))
-    return TokenLogprobs(logprob, lse, entropy, top_logprob, top_id, ref, total)
+        dev, _lib.token_logprobs, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p,
+        None if t_p is None else r._ptr(4), r._ptr(0), r._ptr(1), r._ptr(2), r._ptr(3), top, top_lp, top_ip, ws_p, wbytes))
+    return r
 
 
 def token_logprobs_backward(logits, targets, result, dlogprob=None, dentropy=None, *, scale=1.0, out=None):
@@ -1079,10 +1086,11 @@ def token_logprobs_backward(logits, targets, result, dlogprob=None, dentropy=Non
         raise ValueError("out must have the logits' dtype")
     t_p = _ints("targets", targets, torch.int64, dev, rows, "the logits'") if targets is not None else None
     of = lambda name, t: _row_floats(name, t, rows, dev) if t is not None else None
+    if not isinstance(result, TokenLogprobs) or result._n != rows or result._buf.get_device() != dev:
+        raise ValueError("result must be token_logprobs's of these logits")
     _check("token_logprobs_backward", _on_device(
         dev, _lib.token_logprobs_backward, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p,
-        of("result.row_ref", result.row_ref), of("result.row_sum", result.row_sum), of("result.entropy", result.entropy),
-        of("dlogprob", dlogprob), of("dentropy", dentropy), out.data_ptr(), ldd))
+        result._ptr(1), result._ptr(2), result._ptr(3), of("dlogprob", dlogprob), of("dentropy", dentropy), out.data_ptr(), ldd))
     return out
 
 
