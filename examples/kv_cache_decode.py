@@ -55,7 +55,11 @@ class Pages:
 
 
 class Attention:
-    def __init__(self, hidden=4096, heads=32, kv_heads=8, dim=128, positions=8192, seed=0, device="cuda"):
+    """norms: head norms of queries and keys with random weights.  window, sinks:
+    how many of the latest and of the first keys a token sees (0: all)."""
+
+    def __init__(self, hidden=4096, heads=32, kv_heads=8, dim=128, positions=8192, seed=0, device="cuda", norms=False,
+                 window=0, sinks=0):
         gen = torch.Generator(device=device).manual_seed(seed)
         bits = lambda n: torch.randint(-2 ** 31, 2 ** 31 - 1, (n // 32,), dtype=torch.int32, device=device, generator=gen)
         self.heads, self.kv_heads, self.dim, self.device = heads, kv_heads, dim, torch.device(device)
@@ -68,6 +72,10 @@ class Attention:
         angle = torch.arange(positions, dtype=torch.float64)[:, None] * 10000.0 ** (
             -torch.arange(0, dim, 2, dtype=torch.float64) / dim)
         self.cos, self.sin = angle.cos().float().to(device), angle.sin().float().to(device)
+        self.window, self.sinks, self.norms = window, sinks, {}
+        if norms:
+            self.norms = {name: (1 + 0.2 * torch.randn(dim, device=device, generator=gen)).bfloat16()
+                          for name in ("q_norm", "k_norm")}
 
     def cache(self, pages, page_size, int4):
         return whtq.kv_cache_alloc(pages, page_size, self.kv_heads, self.dim, int4=int4,
@@ -85,8 +93,10 @@ class Attention:
 
         rows = lambda y, h: y.view(-1, h, self.dim)
         q, k, v = rows(self.wq(x), self.heads), rows(self.wk(x), self.kv_heads), rows(self.wv(x), self.kv_heads)
-        q = whtq.kv_append(cache, k, v, put(slots, torch.int64), q=q, q_out=q, cos=self.cos, sin=self.sin, positions=pos)
-        o = whtq.kv_attention(cache, q, start, length, table, max_q_len=max(counts), max_kv_len=max(pages.length))
+        q = whtq.kv_append(cache, k, v, put(slots, torch.int64), q=q, q_out=q, cos=self.cos, sin=self.sin, positions=pos,
+                           **self.norms)
+        o = whtq.kv_attention(cache, q, start, length, table, max_q_len=max(counts), max_kv_len=max(pages.length),
+                              window=self.window, sinks=self.sinks)
         if seen is not None:
             seen.append((q, o))
         return self.wo(o.view(-1, self.heads * self.dim))
