@@ -1216,8 +1216,14 @@ struct LpPlan {
 LpPlan lp_plan(int64_t rows, int64_t vocab, int64_t top, int cus) {
   LpPlan p{};
   const int64_t chunks = (vocab + 7 + LP_CHUNK - 1) / LP_CHUNK;
-  // as many blocks as the machine holds, at least one chunk a wave
-  p.splits = (int)std::max<int64_t>(1, std::min(8 * (int64_t)cus / std::max<int64_t>(rows, 1), chunks / 4));
+  // A block for each row saves the second kernel and its launch: where rows are short (one row of 32000, 5 tokens, a
+  // call among others: 12.8 us against 15.5 over several blocks; alone 31.8 and 29.3) and where there are enough of
+  // them (700 rows of 50257: 22.5 and 24.6, 1000 of 131072: 51.2 and 54.5; but 600 of 131072: 41.5 and 37.3, 300:
+  // 33.3 and 25.9).  Otherwise as many blocks as the machine holds, each of 4 chunks a wave or more (64 rows of
+  // 131072: 15.0 with 16 blocks a row, 15.1 with 32).
+  p.splits = chunks <= 64 || 2 * rows >= 5 * (int64_t)cus
+                 ? 1
+                 : (int)std::max<int64_t>(1, std::min(8 * (int64_t)cus / std::max<int64_t>(rows, 1), chunks / 16));
   if (top) {
     // groups enough that the last one's maximum leaves few candidates (64 and more of them, 512 at most but for
     // vocabularies above 262144), large enough that their maxima are few bytes
