@@ -575,6 +575,8 @@ whtq_status kv_append(const whtq_kv_cache* cache, const void* k, const int64_t* 
  *   side as it is, norm NULL both.  Values are never normed.  Norm, weight and
  *   rotation are fp32, rounded once to the stored type (INT4: not before the
  *   transform).  Squares of values above 2^63 overflow: such a row gives 0.
+ *   With eps 0 a row of zeros, or of values whose squares vanish, gives NaN or
+ *   infinities.
  */
 whtq_status kv_append_norm(const whtq_kv_cache* cache, const void* k, const int64_t* k_stride, const void* v,
                            const int64_t* v_stride, whtq_dtype dtype, int64_t tokens, const int64_t* slots,

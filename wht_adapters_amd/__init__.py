@@ -1,7 +1,9 @@
 """MI355X (gfx950) batched Walsh-Hadamard transforms: orthonormal FWHT,
 RHT + per-group RTN quantisation and its inverse, the QWHA adapter forward
 and a HARP-style structured rotation; a paged key/value cache in 16 bits or
-in the same rotated INT4 codes, and the attention that reads it.
+in the same rotated INT4 codes, and the attention that reads it (windows with
+sinks); norms of queries and keys with their rotation, and log probabilities of
+tokens, each with its gradient.
 
 The compute lives in the HIP shared library ``libwhtq.so`` (C ABI declared in
 ``include/whtq.h``); ``wht_adapters_amd.whtq`` is the thin ctypes binding over

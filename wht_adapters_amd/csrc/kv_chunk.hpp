@@ -24,6 +24,9 @@
 // 64 heads on 8 of 128: 549 GFLOP in 600 to 675 us and 10 us for the join.  Six
 // fp16 chunks of 5 to 1500 tokens under a window of 1000, 24 heads on 8 of
 // 64: 35 us, 1.25 us a tile of two waves a SIMD, about 10 us before and after.
+// The prompt under a window of 1500 with 4 sinks: 183 GFLOP in 245 us, 740
+// TFLOP/s; of the work done, with what the masked tiles at the window's two
+// ends cost, 950.  Without the sinks 229.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -22,6 +22,14 @@
 // What bounds both directions is memory.  Rows need no alignment beyond their
 // elements': a row is taken by the aligned 16 bytes it lies in, and the few
 // logits at its two ends are loaded one by one.
+//
+// Measured (kernel times, bf16): 2047 rows of 100003, five tokens: 410 MB in
+// 80 to 85 us, 4.8 to 5.1 TB/s (a large copy moves 4.9), with the vector pipes
+// 80 % busy (10 instructions a logit); 110 us before loads came streamed (past
+// the caches) and without a branch between them and their use.  Forward and
+// gradient of 8192 rows of 32000: 524 MB in 98 to 110 us (vector pipes 90 %)
+// and 1049 MB in 180 us, 5.8 TB/s.  One row of
+// 131072, 20 tokens: 4.8 us and 5.9 us for the likeliest, all latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

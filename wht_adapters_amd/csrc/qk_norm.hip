@@ -15,6 +15,16 @@
 // one weight vector, so that a lane's part of dw stays in registers; blocks
 // leave one partial sum each, which a second kernel adds in a fixed order (no
 // atomics: the same result every time).
+//
+// Measured (kernel times; 8192 tokens, 32 query and 8 key heads of 128, bf16):
+// into a 16-bit cache 209 MB in 40 us, 5.2 TB/s (a large copy moves 4.9);
+// dense rows 176 MB in 36 us; backward 256 MB in 46 us, 5.5 TB/s, and 4.7 us
+// for the join.  A kind's blocks together, with the rotation's kinds as
+// branches, took 50 and 59 us: the branches keep registers of every kind.
+// 2, 3 or 6 rows a group of lanes: 55 to 60 us against 45 at the time, fewer
+// waves to wait side by side.  1 token, 48 heads: 3.3 us; 61 tokens of 80 heads
+// into INT4: 4.9 us; 333 tokens, 48 heads of 64 with a weight vector each:
+// 3.9 us and 9.3 us, the latter the 11 rows in a row that a group of lanes has.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

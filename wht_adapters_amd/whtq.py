@@ -777,10 +777,10 @@ def _rope_arg(cos, sin, positions, rot_dim, interleaved, tokens, dev, whose):
 
 def _norm_arg(q_norm, k_norm, eps, heads, kv_heads, dim, dev, whose):
     """The norms of a call: weights [dim], or [heads, dim] for one a head."""
-    if q_norm is not None and k_norm is not None and q_norm.dtype is not k_norm.dtype:
-        raise ValueError("q_norm and k_norm must have one dtype")
     q_p, q_head = _norm_weight("q_norm", q_norm, heads, dim, dev, whose)
     k_p, k_head = _norm_weight("k_norm", k_norm, kv_heads, dim, dev, whose)
+    if q_norm is not None and k_norm is not None and q_norm.dtype is not k_norm.dtype:
+        raise ValueError("q_norm and k_norm must have one dtype")
     return _Norm(q_p, k_p, q_head, k_head, _DT[(k_norm if q_norm is None else q_norm).dtype], eps)
 
 
