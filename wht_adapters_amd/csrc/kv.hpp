@@ -97,19 +97,25 @@ __device__ __forceinline__ void kv_sign8(float* v, uint32_t bits8) {
 // [0, 15]; 0x6400 | u is 1024 + u and 0x6400 | (u << 4) is 1024 + 16 u.  The
 // pairs come out as codes (0,4), (1,5), (2,6), (3,7): position i of the eight
 // holds code kv_perm(i), on both operands of a product or undone at its end.
+// The offset flips a code's top bit, so that it, the mask and 0x6400 are one
+// three-way operation, (x & mask) ^ constant; of its two numbers one has to be
+// in a vector register, where the compiler does not keep it by itself.
 __device__ __forceinline__ constexpr int kv_perm(int i) { return (i >> 1) | ((i & 1) << 2); }
-__device__ __forceinline__ uint32_t kv_code_lo(uint32_t x) {  // x: u in bits 0..3 and 16..19
-  const f16x2_t h = __builtin_bit_cast(f16x2_t, (x & 0x000f000fu) | 0x64006400u);
+__device__ __forceinline__ uint32_t kv_in_vgpr(uint32_t x) {
+  asm("" : "+v"(x));
+  return x;
+}
+__device__ __forceinline__ uint32_t kv_code_lo(uint32_t x) {  // x: codes in bits 0..3 and 16..19
+  const f16x2_t h = __builtin_bit_cast(f16x2_t, (x & 0x000f000fu) ^ kv_in_vgpr(0x64086408u));
   return __builtin_bit_cast(uint32_t, h + f16x2_t{(_Float16)-1032.f, (_Float16)-1032.f});
 }
-__device__ __forceinline__ uint32_t kv_code_hi(uint32_t x) {  // x: u in bits 4..7 and 20..23
-  const f16x2_t h = __builtin_bit_cast(f16x2_t, (x & 0x00f000f0u) | 0x64006400u);
+__device__ __forceinline__ uint32_t kv_code_hi(uint32_t x) {  // x: codes in bits 4..7 and 20..23
+  const f16x2_t h = __builtin_bit_cast(f16x2_t, (x & 0x00f000f0u) ^ kv_in_vgpr(0x64806480u));
   const f16x2_t c = {(_Float16)0.0625f, (_Float16)0.0625f}, o = {(_Float16)-72.f, (_Float16)-72.f};
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(h, c, o));
 }
 __device__ __forceinline__ u32x4 kv_codes8(uint32_t w) {
-  const uint32_t a = w ^ 0x88888888u, b = a >> 8;
-  return u32x4{kv_code_lo(a), kv_code_hi(a), kv_code_lo(b), kv_code_hi(b)};
+  return u32x4{kv_code_lo(w), kv_code_hi(w), kv_code_lo(w >> 8), kv_code_hi(w >> 8)};
 }
 
 // The scale of an INT4 entry, from its bits.  An entry whose scale is not finite

@@ -22,15 +22,15 @@
 // the keys.
 //
 // Measured (kernel times): 64 sequences of 17 to 8191 keys, 32 heads on 8 of
-// 128, bf16: 363 MB in 80 us, 4.6 TB/s (a large copy moves 4.75), and 4.7 us
+// 128, bf16: 363 MB in 74 us, 4.9 TB/s (a large copy moves as much), and 4.8 us
 // for the join.  Two INT4 contexts of 100003 and 131072 keys, 64 heads on 8:
-// 244 MB in 62 us, 3.9 TB/s, the vector pipes 55 % busy unpacking codes, and
-// 7.1 us for the join.  One token over 777 keys: 8.6 + 4.1 us, all latency.
-// With 4 sinks: 64 sequences under a window of 4096, 396 MB in 85 us, 4.7 TB/s
-// (87 and without the sinks 83 in one run); 16 sequences of 64 heads on 8,
-// INT4, 37 sinks and a window of 16384, 248 MB in 75 us (71), 3.3 TB/s, the
-// vector pipes 48 % and the matrix pipes 8 % busy with two waves a SIMD.  One
-// token under a window of 1024, wherever it stands in the sequence: 10 + 4 us.
+// 244 MB in 54 us, 4.5 TB/s, and 7.1 us for the join (62 us with two more
+// operations a pair of codes and a branch a score).  One token over 777 keys:
+// 8 + 4 us, all latency.
+// With 4 sinks: 64 sequences under a window of 4096, 396 MB in 80 us, 4.9 TB/s;
+// 16 sequences of 64 heads on 8, INT4, 37 sinks and a window of 16384, 248 MB in
+// 65 us, 3.8 TB/s, the vector pipes about half busy with two waves a SIMD.  One
+// token under a window of 1024, wherever it stands in the sequence: 9 + 4 us.
 // Registers: the INT4 builds keep about 100 scalars in vector lanes, two column
 // blocks (17 to 32 rows) leave one wave a SIMD, and the 16-bit build for several
 // tokens has up to 24 vector registers in scratch (take_out, unrolled over the
@@ -227,6 +227,9 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
 
     const uint8_t* kbase = a.c.k.p + h * a.c.k.head;
     const uint8_t* vbase = a.c.v.p + h * a.c.v.head;
+    const uint8_t* kscale = INT4 ? (const uint8_t*)(a.c.k.scale + h * a.c.k.s_head) : nullptr;
+    const uint8_t* vscale = INT4 ? (const uint8_t*)(a.c.v.scale + h * a.c.v.s_head) : nullptr;
+    const int64_t kspage = 2 * a.c.k.s_page, vspage = 2 * a.c.v.s_page;
     // a lane's places in 16 keys (a page's extent is below 2^31 bytes)
     const uint32_t klane = r * (uint32_t)a.c.k.tok + g * (INT4 ? D / 8 : 16);
     const uint32_t vlane = 4 * g * (uint32_t)a.c.v.tok + r * (INT4 ? DL / 2 : 2 * DL);
@@ -245,9 +248,9 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
     auto fetch_k = [&](int key0, int pages) {
 #pragma unroll
       for (int kb = 0; kb < 2 * KP; ++kb) {
-        const int64_t page = __builtin_amdgcn_readlane(pages, kb);
-        const int off = (key0 + 16 * kb) & pmask;
-        const uint8_t* kp = kbase + (page * a.c.k.page + off * a.c.k.tok);
+        const uint64_t page = (uint32_t)__builtin_amdgcn_readlane(pages, kb);
+        const uint32_t off = (key0 + 16 * kb) & pmask;
+        const uint8_t* kp = kbase + (page * a.c.k.page + off * (uint32_t)a.c.k.tok);
         if constexpr (!INT4) {
 #pragma unroll
           for (int kk = 0; kk < KK; ++kk) kr[kb][kk] = ldg_global<u32x4>(kp + (klane + 64 * kk));
@@ -258,15 +261,15 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
           kr[kb][0] = u32x4{w.x, w.y, 0u, 0u};
         }
         if constexpr (INT4)
-          ksr[kb] = kv_load<u32x2>(a.c.k.scale + (page * a.c.k.s_page + h * a.c.k.s_head + off), 8 * g);
+          ksr[kb] = kv_load<u32x2>(kscale + (page * kspage + 2 * off), 8 * g);
       }
     };
     auto fetch_v = [&](int key0, int pages) {
 #pragma unroll
       for (int kb = 0; kb < 2 * KP; ++kb) {
-        const int64_t page = __builtin_amdgcn_readlane(pages, kb);
-        const int off = (key0 + 16 * kb) & pmask;
-        const uint8_t* vp = vbase + (page * a.c.v.page + off * a.c.v.tok);
+        const uint64_t page = (uint32_t)__builtin_amdgcn_readlane(pages, kb);
+        const uint32_t off = (key0 + 16 * kb) & pmask;
+        const uint8_t* vp = vbase + (page * a.c.v.page + off * (uint32_t)a.c.v.tok);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t p = vlane + j * (uint32_t)a.c.v.tok;
@@ -286,7 +289,7 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
           }
         }
         if constexpr (INT4)
-          vsr[kb] = kv_load<u32x2>(a.c.v.scale + (page * a.c.v.s_page + h * a.c.v.s_head + off), 8 * g);
+          vsr[kb] = kv_load<u32x2>(vscale + (page * vspage + 2 * off), 8 * g);
       }
     };
 
@@ -416,16 +419,13 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
       const bool full = (key0 >= (a.window > 0 ? max(kfirst, p0 + nq - a.window) : kfirst) || (SINKS && key0 + TK <= a.sinks)) &&
                         key0 + TK - 1 <= (a.causal ? min(klast, p0) : klast);
       auto key_of = [&](int s) { return key0 + 16 * (s >> 2) + 4 * g + (s & 3); };
-      float ks[8 * KP], vs[8 * KP];
+      // (scales stay fp16: x s + 0 widens s in the same operation)
+      f16x2_t ks[4 * KP], vs[4 * KP];
       if constexpr (INT4) {
 #pragma unroll
-        for (int s = 0; s < 8 * KP; s += 2) {
-          const uint32_t w = ksr[s >> 2][(s >> 1) & 1];
-          const f16x2_t h = kv_scale2(w);
-          ks[s] = (float)h[0];
-          ks[s + 1] = (float)h[1];
-        }
+        for (int s = 0; s < 4 * KP; ++s) ks[s] = kv_scale2(ksr[s >> 1][s & 1]);
       }
+      auto scaled = [](float x, const f16x2_t* y, int s) { return __builtin_fmaf(x, (float)y[s >> 1][s & 1], 0.f); };
       // S^T: sc[n][4 kb + e] is key 16 kb + 4 g + e
       float sc[NQ][8 * KP];
 #pragma unroll
@@ -462,17 +462,14 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
           big = absmax16(absmax16(big, w0), w1);
         }
 #pragma unroll
-        for (int s = 0; s < 8 * KP; ++s) {
-          const uint32_t w = vsr[s >> 2][(s >> 1) & 1];
-          vs[s] = (float)__builtin_bit_cast(_Float16, (uint16_t)(s & 1 ? w >> 16 : w & 0xffffu));
-        }
+        for (int s = 0; s < 4 * KP; ++s) vs[s] = __builtin_bit_cast(f16x2_t, (uint32_t)vsr[s >> 1][s & 1]);
         float top = (float)__builtin_bit_cast(_Float16, (uint16_t)absmax16(big));
         if (__any(!(top < __builtin_ldexpf(1.f, ve + 1)))) {
           // of the keys that count, without infinities and NaN
           top = 0.f;
 #pragma unroll
           for (int s = 0; s < 8 * KP; ++s)
-            if (counts(key_of(s)) && vs[s] < 65536.f) top = fmaxf(top, vs[s]);
+            if (const float x = (float)vs[s >> 1][s & 1]; counts(key_of(s)) && x < 65536.f) top = fmaxf(top, x);
 #pragma unroll
           for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x, 64));
           // (of 0 the exponent would be 0: the largest may be that of a key which does not count)
@@ -499,17 +496,23 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         float top = KV_NEG_INF;
+        if constexpr (INT4)
 #pragma unroll
-        for (int s = 0; s < 8 * KP; ++s) {
-          if constexpr (INT4) sc[n][s] *= ks[s];
-          if (!full) {
+          for (int s = 0; s < 8 * KP; ++s) sc[n][s] = scaled(sc[n][s], ks, s);
+        if (!full) {
+          // (one branch a tile and none a score: the compiler makes them of a branch inside the loop above and of &&.
+          // Keys of these tiles that are sinks are at or past kfirst.)
+          const int hi = a.causal ? min(klast, qpos[n]) : klast;
+          const int lo = a.window > 0 ? max(kfirst, qpos[n] - a.window + 1) : kfirst;
+#pragma unroll
+          for (int s = 0; s < 8 * KP; ++s) {
             const int key = key_of(s);
-            const bool in = key >= kfirst && key <= klast && (!a.causal || key <= qpos[n]) &&
-                            (a.window <= 0 || key > qpos[n] - a.window || (SINKS && key < a.sinks));
+            const bool in = (key <= hi) & ((key >= lo) | (SINKS && key < a.sinks));
             sc[n][s] = in ? sc[n][s] : KV_NEG_INF;
           }
-          top = fmaxf(top, sc[n][s]);
         }
+#pragma unroll
+        for (int s = 0; s < 8 * KP; ++s) top = fmaxf(top, sc[n][s]);
         if (__any(top > m[n] + lag[n])) {
           top = fmaxf(top, __shfl_xor(top, 16, 64));
           top = fmaxf(top, __shfl_xor(top, 32, 64));
@@ -526,7 +529,7 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
         for (int s = 0; s < 8 * KP; ++s) {
           p[s] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][s], qs[n], base));
           l[n] += p[s];
-          if constexpr (INT4) p[s] *= vs[s];
+          if constexpr (INT4) p[s] = scaled(p[s], vs, s);
         }
         if (INT4 && !full) {  // whatever the scale of a masked place is
 #pragma unroll
@@ -544,9 +547,9 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
             u32x4 f0, f1;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              // byte i / 2 of two keys' words, each alone in a half, offset by 8
+              // byte i / 2 of two keys' words, each alone in a half
               const int s = 8 * kp + 2 * w;
-              const uint32_t x = __builtin_amdgcn_perm(vr[s + 1][0], vr[s][0], 0x0c040c00u + 0x00010001u * (i / 2)) ^ 0x00880088u;
+              const uint32_t x = __builtin_amdgcn_perm(vr[s + 1][0], vr[s][0], 0x0c040c00u + 0x00010001u * (i / 2));
               f0[w] = kv_code_lo(x);
               f1[w] = kv_code_hi(x);
             }
@@ -613,10 +616,12 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
         for (int w = 0; w < NW; ++w) {
           const float f = __builtin_amdgcn_exp2f(sm[w][q] - kv_base(mx));
           sum += f * sl[w][q];
-          // a wave that saw nothing for this row adds nothing
+          // a wave that saw nothing for this row adds nothing (read all the same: in the branches that the compiler made
+          // of it the reads waited one after another, 3 to 5 us of a call)
           const bool none = sm[w][q] == KV_NEG_INF && sl[w][q] == 0.f;
+          const f32x4 y[2] = {*reinterpret_cast<const f32x4*>(&so[w][q][8 * i0]), *reinterpret_cast<const f32x4*>(&so[w][q][8 * i0 + 4])};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] += none ? 0.f : f * so[w][q][8 * i0 + e];
+          for (int e = 0; e < 8; ++e) x[e] += none ? 0.f : f * y[e >> 2][e & 3];
         }
         if ((uint32_t)(q0 + tok) < (uint64_t)a.q_tokens) {
           if (whole) {
