@@ -75,15 +75,35 @@ __device__ __forceinline__ void kv_bfly(float* v) {
     for (int i = 0; i < N; ++i)
       if (!(i & h)) bfly(v[i], v[i + h]);
 }
-// The butterfly between lanes that differ in lane bit `m` (the lane with the
-// bit clear holds the lower index).
-template <int N>
-__device__ __forceinline__ void kv_lane_bfly(float* v, int m, int lane) {
-  const bool up = lane & m;
+template <int M>  // the value of the lane that differs in lane bit M = 1, 2, 4, 8
+__device__ __forceinline__ uint32_t kv_lane_xor(uint32_t x) {
+  constexpr int QUAD = M == 1 ? 0xb1 : M == 2 ? 0x4e : 0x1b;  // quad_perm: lane ^ 1, ^ 2, ^ 3
+  if constexpr (M == 4) x = __builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true);  // row_half_mirror: lane ^ 7
+  return __builtin_amdgcn_mov_dpp(x, M == 8 ? 0x128 : QUAD, 0xf, 0xf, true);     // row_ror:8
+}
+// The butterfly between lanes that differ in lane bit M (the lane with the bit
+// clear holds the lower index), without the way through LDS.  16 and 32 (all
+// lanes of the wave at work): two values change places with the other lane's,
+// each lane does both operations of one of them, and they change back.
+template <int N, int M>
+__device__ __forceinline__ void kv_lane_bfly(float* v, int lane) {
+  if constexpr (M >= 16) {
+    auto change = [](float& a, float& b) {
+      const auto r = M == 32 ? __builtin_amdgcn_permlane32_swap(as_u(a), as_u(b), false, false)
+                             : __builtin_amdgcn_permlane16_swap(as_u(a), as_u(b), false, false);
+      a = as_f(r[0]);
+      b = as_f(r[1]);
+    };
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float o = __shfl_xor(v[i], m, 64);
-    v[i] = up ? o - v[i] : v[i] + o;
+    for (int i = 0; i < N; i += 2) {
+      change(v[i], v[i + 1]);
+      bfly(v[i], v[i + 1]);
+      change(v[i], v[i + 1]);
+    }
+  } else {
+    const float sg = lane & M ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __builtin_fmaf(v[i], sg, as_f(kv_lane_xor<M>(as_u(v[i]))));
   }
 }
 

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
         if (a.c.signs) kv_sign8(x + 8 * kk, (a.c.signs[c >> 2] >> (8 * (c & 3))) & 255u);
       }
       kv_bfly<8 * KK>(x);
-      kv_lane_bfly<8 * KK>(x, 32, lane);
+      kv_lane_bfly<8 * KK, 32>(x, lane);
       float top = 0.f;
 #pragma unroll
       for (int e = 0; e < 8 * KK; ++e) {
@@ -641,7 +641,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv_chunk(const KvAttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 16 * DB; ++e) x[e] = o[e >> 4][e & 15];
         kv_bfly<16 * DB>(x);
-        kv_lane_bfly<16 * DB>(x, 32, lane);
+        kv_lane_bfly<16 * DB, 32>(x, lane);
 #pragma unroll
         for (int e = 0; e < 16 * DB; ++e) {
           const int dim = 8 * (e >> 2) + 4 * hf + (e & 3);

@@ -132,12 +132,6 @@ __device__ __forceinline__ void kv_turn(float (&x)[16], const KvTurn& a, const K
   }
 }
 
-template <int M>  // the value of the lane that differs in lane bit M = 1, 2, 4
-__device__ __forceinline__ uint32_t kv_lane_xor(uint32_t x) {
-  constexpr int QUAD = M == 1 ? 0xb1 : M == 2 ? 0x4e : 0x1b;  // quad_perm: lane ^ 1, ^ 2, ^ 3
-  if constexpr (M == 4) x = __builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true);  // row_half_mirror: lane ^ 7
-  return __builtin_amdgcn_mov_dpp(x, QUAD, 0xf, 0xf, true);
-}
 // Butterflies between lanes whose values differ in lane bit M.
 template <int M>
 __device__ __forceinline__ void kv_near_bfly(float (&x)[16], int i) {

@@ -53,7 +53,7 @@ __device__ __forceinline__ void kv_join_row(const KvAttnArgs& a, int64_t tok, in
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] *= inv;
-  if constexpr (INT4) kv_row_rht<D, 8, true>(x, i0, 1, lane, a.c.signs);
+  if constexpr (INT4) kv_row_rht<D, 8, 1, true>(x, i0, lane, a.c.signs);
   stg<u32x4>(a.out + tok * a.o_tok + head * a.o_head + 16 * i0, kv_round8<T>(x));
   if (a.lse && i0 == 0) a.lse[tok * a.heads + head] = sum == 0.f ? KV_NEG_INF : (mx + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
 }

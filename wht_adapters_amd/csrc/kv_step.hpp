@@ -47,9 +47,9 @@ namespace whtq {
 
 // The row transform x -> Hn S x over a group of D / N lanes with N values
 // each: lane (sub) holds values N sub .. N sub + N - 1, lanes differ by
-// `step` (a power of two).  SIGN_AFTER applies S last (the inverse).
-template <int D, int N, bool SIGN_AFTER>
-__device__ __forceinline__ void kv_row_rht(float* x, int sub, int step, int lane, const uint32_t* signs) {
+// STEP (a power of two).  SIGN_AFTER applies S last (the inverse).
+template <int D, int N, int STEP, bool SIGN_AFTER>
+__device__ __forceinline__ void kv_row_rht(float* x, int sub, int lane, const uint32_t* signs) {
   auto sign = [&] {
     if (!signs) return;
 #pragma unroll
@@ -60,8 +60,11 @@ __device__ __forceinline__ void kv_row_rht(float* x, int sub, int step, int lane
   };
   if constexpr (!SIGN_AFTER) sign();
   kv_bfly<N>(x);
-#pragma unroll
-  for (int m = 1; m < D / N; m *= 2) kv_lane_bfly<N>(x, m * step, lane);
+  if constexpr (D / N > 1) kv_lane_bfly<N, STEP>(x, lane);
+  if constexpr (D / N > 2) kv_lane_bfly<N, 2 * STEP>(x, lane);
+  if constexpr (D / N > 4) kv_lane_bfly<N, 4 * STEP>(x, lane);
+  if constexpr (D / N > 8) kv_lane_bfly<N, 8 * STEP>(x, lane);
+  static_assert(D / N <= 16, "");
 #pragma unroll
   for (int e = 0; e < N; ++e) x[e] *= D == 64 ? 0.125f : 0.08838834764831845f;  // 1 / sqrt(D)
   if constexpr (SIGN_AFTER) sign();
@@ -331,7 +334,7 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
           kv_widen8<T>(live ? ldg<u32x4>(qp + g * (D / 2) + 16 * kk) : u32x4{0u, 0u, 0u, 0u}, x + 8 * kk);
-        kv_row_rht<D, D / 4, false>(x, g, 16, lane, a.c.signs);
+        kv_row_rht<D, D / 4, 16, false>(x, g, lane, a.c.signs);
         float top = 0.f;
 #pragma unroll
         for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(x[e]));
@@ -628,7 +631,7 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= inv;
-            if constexpr (INT4) kv_row_rht<D, 8, true>(x, i0, 1, lane, a.c.signs);
+            if constexpr (INT4) kv_row_rht<D, 8, 1, true>(x, i0, lane, a.c.signs);
             stg<u32x4>(a.out + (int64_t)(q0 + tok) * a.o_tok + (int64_t)head * a.o_head + 16 * i0, kv_round8<T>(x));
             if (a.lse && i0 == 0)
               a.lse[(int64_t)(q0 + tok) * a.heads + head] =
