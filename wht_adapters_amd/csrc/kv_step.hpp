@@ -296,18 +296,42 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
       }
     };
 
+    // The lane's queries, column r of each block of 16: asked for first, since
+    // memory answers in order, and read for rows that are not there too (the
+    // first row of all; a branch around each load would wait for each).  They
+    // have arrived with the first table entries, and are taken then: later they
+    // would be waited for with the keys and values.
+    u32x4 raw[NQ][KK];
+    bool live[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int row = 16 * n + r, tok = row / a.group;
+      live[n] = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
+      const uint8_t* qp = live[n] ? a.q + (int64_t)(q0 + tok) * a.q_tok + (int64_t)(h * a.group + row % a.group) * a.q_head : a.q;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) raw[n][kk] = ldg<u32x4>(qp + (INT4 ? g * (D / 2) + 16 * kk : 64 * kk + 16 * g));
+    }
+
     const bool work = kfirst <= klast;
     const int t1 = SINKS ? v1 - 1 : klast / TK;
     // memory answers in order: the next tile's table entries are asked for
     // before this tile's keys and values, and so are there with them
     int t = (SINKS ? from * NW : kfirst / TK) + wave, entry = 0;
-    if (work && t <= t1) {
-      const int at0 = tile_of(t) * TK, pages = kv_page(a, look_up(at0));
+    const bool has = work && t <= t1;
+    const int at0 = has ? tile_of(t) * TK : 0;
+    int pages = has ? look_up(at0) : 0;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) asm volatile("" : "+v"(raw[n][kk]));
+    asm volatile("" : "+v"(pages));
+    if (has) {
+      pages = kv_page(a, pages);
       entry = look_up(tile_of(t + NW) * TK);
       fetch_k(at0, pages);
       fetch_v(at0, pages);
     }
-    // the lane's queries (column r of each block of 16) and what they see
+    // the queries and what they see
     // INT4: the rotated query is rounded to fp16 for its product, 2^-12 of each
     // value.  bf16 outputs hide that (it adds 1 % to their own 2^-9); fp16
     // outputs would be off by twice their own rounding, so there what the
@@ -318,22 +342,18 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
     const uint32_t turn = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const int row = 16 * n + r, tok = row / a.group;
-      const bool live = row < rows && (uint32_t)(q0 + tok) < (uint64_t)a.q_tokens;
-      qpos[n] = p0 + tok;
+      const uint32_t there = live[n] ? ~0u : 0u;
+      qpos[n] = p0 + (16 * n + r) / a.group;
       // 0 would turn a masked -inf into NaN; the results are the same (a score in
       // these units is below 2^27 where INT4's power of two takes part)
       qs[n] = fmaxf(fabsf(a.scale), 1e-30f);
-      const uint8_t* qp = a.q + (int64_t)(q0 + tok) * a.q_tok + (int64_t)(h * a.group + row % a.group) * a.q_head;
       if constexpr (!INT4) {
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-          qf[n][kk] = live ? ldg<u32x4>(qp + 64 * kk + 16 * g) ^ turn : u32x4{0u, 0u, 0u, 0u};
+        for (int kk = 0; kk < KK; ++kk) qf[n][kk] = (raw[n][kk] ^ turn) & there;
       } else {
         float x[D / 4];
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-          kv_widen8<T>(live ? ldg<u32x4>(qp + g * (D / 2) + 16 * kk) : u32x4{0u, 0u, 0u, 0u}, x + 8 * kk);
+        for (int kk = 0; kk < KK; ++kk) kv_widen8<T>(raw[n][kk] & there, x + 8 * kk);
         kv_row_rht<D, D / 4, 16, false>(x, g, lane, a.c.signs);
         float top = 0.f;
 #pragma unroll
