@@ -22,19 +22,19 @@
 // the keys.
 //
 // Measured (kernel times): 64 sequences of 17 to 8191 keys, 32 heads on 8 of
-// 128, bf16: 363 MB in 74 us, 4.9 TB/s (a large copy moves as much), and 4.8 us
+// 128, bf16: 363 MB in 70 us, 5.2 TB/s (a large copy moves 4.9), and 4.8 us
 // for the join.  Two INT4 contexts of 100003 and 131072 keys, 64 heads on 8:
-// 244 MB in 54 us, 4.5 TB/s, and 7.1 us for the join (62 us with two more
+// 244 MB in 53 us, 4.6 TB/s, and 6.8 us for the join (62 us with two more
 // operations a pair of codes and a branch a score).  One token over 777 keys:
-// 8 + 4 us, all latency.
-// With 4 sinks: 64 sequences under a window of 4096, 396 MB in 80 us, 4.9 TB/s;
+// 7 + 4.5 us, all latency.
+// With 4 sinks: 64 sequences under a window of 4096, 396 MB in 79 us, 5.0 TB/s;
 // 16 sequences of 64 heads on 8, INT4, 37 sinks and a window of 16384, 248 MB in
-// 65 us, 3.8 TB/s, the vector pipes about half busy with two waves a SIMD.  One
-// token under a window of 1024, wherever it stands in the sequence: 9 + 4 us.
-// Registers: the INT4 builds keep about 100 scalars in vector lanes, two column
+// 63 us, 4.0 TB/s, the vector pipes half busy with two waves a SIMD.  One token
+// under a window of 1024, wherever it stands in the sequence: 7.7 + 4.3 us.
+// Registers: the INT4 builds keep 100 to 160 scalars in vector lanes, two column
 // blocks (17 to 32 rows) leave one wave a SIMD, and the 16-bit build for several
-// tokens has up to 24 vector registers in scratch (take_out, unrolled over the
-// tile): the 64 sequences with 4 tokens each take 114 us.
+// tokens has up to 31 vector registers in scratch (take_out, unrolled over the
+// tile): the 64 sequences with 4 tokens each take 106 us a call.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -640,7 +640,7 @@ __global__ __launch_bounds__(64 * NW, NQ == 1 ? 2 : 1) void k_kv_step(const KvAt
           const float f = __builtin_amdgcn_exp2f(sm[w][q] - kv_base(mx));
           sum += f * sl[w][q];
           // a wave that saw nothing for this row adds nothing (read all the same: in the branches that the compiler made
-          // of it the reads waited one after another, 3 to 5 us of a call)
+          // of it the reads waited one after another, 2 to 4 us of a call)
           const bool none = sm[w][q] == KV_NEG_INF && sl[w][q] == 0.f;
           const f32x4 y[2] = {*reinterpret_cast<const f32x4*>(&so[w][q][8 * i0]), *reinterpret_cast<const f32x4*>(&so[w][q][8 * i0 + 4])};
 #pragma unroll
