@@ -1,4 +1,6 @@
 """token_logprobs and its gradient on the GPU against oracle/lm.py in fp64."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
@@ -94,6 +96,27 @@ def test_rows(W, dtype, rows, vocab, top, offset):
     for scale in (1.0, 0.7):
         r = W.token_logprobs(xd, torch.from_numpy(t).to(DEV), top=top, scale=scale)
         check(r, host64(x), t, scale, top)
+
+
+@pytest.mark.parametrize("more", [-1, 0])
+def test_one_block_a_row_or_several(W, more):
+    """On either side of the number of rows from which a block has a row to itself, and the largest vocabulary either way."""
+    rows = -(-5 * torch.cuda.get_device_properties(0).multi_processor_count // 2) + more
+    rng = np.random.default_rng(21)
+    x, xd = make(rng, rows, 33001, torch.bfloat16, 1)
+    t = rng.integers(0, 33001, rows)
+    assert (W.token_logprobs_workspace_bytes(rows, 33001, 2) == 0) == (more == 0)
+    check(W.token_logprobs(xd, torch.from_numpy(t).to(DEV), top=2), host64(x), t, 1.0, 2)
+    vocab, few = 2 ** 20, 2
+    x, xd = make(rng, few, vocab, torch.float16)
+    t = rng.integers(0, vocab, few)
+    if more < 0:
+        return check(W.token_logprobs(xd, torch.from_numpy(t).to(DEV), top=32), host64(x), t, 1.0, 32)
+    long = xd.repeat(rows // few, 1)  # (whatever its size: each row by a block of its own)
+    r = W.token_logprobs(long, torch.from_numpy(t).to(DEV).repeat(rows // few), top=32)
+    names = ("logprob", "lse", "entropy", "row_ref", "row_sum", "top_logprob", "top_id")
+    last = SimpleNamespace(**{n: v[-few:] for n, v in zip(names, parts(r))})
+    check(last, host64(x), t, 1.0, 32)
 
 
 @pytest.mark.parametrize("dtype", DTS)
