@@ -598,7 +598,8 @@ whtq_status kv_append_norm(const whtq_kv_cache* cache, const void* k, const int6
  *   share them) as fp32 dq_norm, dk_norm [dim], or [heads][dim] where the
  *   weights have a head stride.  dq, dk may be dq_out's, dk_out's or q's, k's
  *   own rows.  A token outside the positions leaves its rows alone and adds
- *   nothing; no tokens give weights' gradients of 0.
+ *   nothing; no tokens give weights' gradients of 0.  A row whose squares
+ *   overflow has gradients of 0 (its output is 0).
  *   workspace: device memory of ..._workspace_bytes (16-byte aligned; may be
  *   NULL when that is 0), overwritten.  fp32 sums; deterministic.
  */

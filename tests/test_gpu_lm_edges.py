@@ -1,0 +1,38 @@
+"""Norms and log probabilities at calls that their documentation allows, or
+refuses, beside those of test_gpu_qk_norm.py and test_gpu_logprob.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import lm
+from tests.gpu_util import DEV, host64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def W():
+    from wht_adapters_amd import whtq
+    return whtq
+
+
+def test_gradient_of_rows_whose_squares_overflow(W):
+    """Such a row gives 0 (r is 0), and 0 is its gradient; other rows and the weights' gradient do without it."""
+    rng = np.random.default_rng(31)
+    x, dy = (torch.from_numpy(rng.standard_normal((6, 2, 64)).astype(np.float32)).bfloat16().to(DEV) for _ in range(2))
+    w = torch.from_numpy(rng.standard_normal(64).astype(np.float32)).to(DEV)
+    want = W.qk_norm_rope_backward(dy, dy[:, :1], x, x[:, :1], q_norm=w, k_norm=w)
+    big = x.clone()
+    big[2, 1] = 3e38 * x[2, 1].sign()   # sums of its products overflow as well
+    big[4, 0] = 1e20 * x[4, 0].sign()
+    y, _ = W.qk_norm_rope(big, x[:, :1], q_norm=w, k_norm=w)
+    assert (y[2, 1] == 0).all() and (y[4, 0] == 0).all()
+    dq, dk, dwq, dwk = W.qk_norm_rope_backward(dy, dy[:, :1], big, x[:, :1], q_norm=w, k_norm=w)
+    assert (dq[2, 1] == 0).all() and (dq[4, 0] == 0).all()
+    dq[2, 1], dq[4, 0] = want[0][2, 1], want[0][4, 0]
+    assert torch.equal(dq, want[0]) and torch.equal(dk, want[1]) and torch.equal(dwk, want[3])
+    keep = np.array([[(t, h) not in ((2, 1), (4, 0)) for h in range(2)] for t in range(6)])
+    x64, dy64 = host64(x), host64(dy) * keep[..., None]
+    _, dw = lm.norm_rope_backward(dy64, x64, host64(w), 1e-6)
+    mass = np.abs(dy64 * x64 * lm.rms(x64, 1e-6)).sum((0, 1))
+    assert np.all(np.abs(host64(dwq) - dw) <= (12 + 40 + 14 + 2) * 2.0 ** -24 * mass)  # (as for ordinary rows)

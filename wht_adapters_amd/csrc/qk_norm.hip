@@ -5,7 +5,7 @@
 //   r = (mean x^2 + eps)^-1/2,  y = R (w o x r)
 // and with g = R^T dy (the opposite rotation), u = w o g:
 //   dw = sum g o x r  over tokens (and heads that share w),
-//   dx = r (u - x r^2 mean(u o x)).
+//   dx = r (u - x r mean(u o x r)).
 // The backward pass takes x again and computes r itself: two numbers a row
 // less to keep, and x has to be read anyway.
 //
@@ -110,14 +110,17 @@ __global__ __launch_bounds__(256) void k_qk_norm_back(const QkArgs a) {
     kv_widen8<T>(g1, g + 8);
     const float r = kv_rms<D>(x, a.eps);
     kv_turn<D, WAY, true>(g, a.turn, cs, pos, i, [&](int ch, float* o) { kv_widen8<T>(ldg<u32x4>(dp + 16 * ch), o); });
+    // x r first: of a row whose squares overflow r is 0, and so are x r and the gradients (x r^2 mean(u x) is 0 times
+    // infinity there)
     float dot = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      dw[e] = __builtin_fmaf(g[e], x[e] * r, dw[e]);
+      x[e] *= r;
+      dw[e] = __builtin_fmaf(g[e], x[e], dw[e]);
       g[e] *= w[e];
       dot = __builtin_fmaf(g[e], x[e], dot);
     }
-    dot = kv_row_sum<L>(dot) * (1.f / D) * r * r;
+    dot = kv_row_sum<L>(dot) * (1.f / D);
 #pragma unroll
     for (int e = 0; e < 16; ++e) g[e] = r * (g[e] - x[e] * dot);
     uint8_t* o = const_cast<uint8_t*>(s.dx.p) + t * s.dx.tok + h * s.dx.head;
