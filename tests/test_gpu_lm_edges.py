@@ -36,3 +36,14 @@ def test_gradient_of_rows_whose_squares_overflow(W):
     _, dw = lm.norm_rope_backward(dy64, x64, host64(w), 1e-6)
     mass = np.abs(dy64 * x64 * lm.rms(x64, 1e-6)).sum((0, 1))
     assert np.all(np.abs(host64(dwq) - dw) <= (12 + 40 + 14 + 2) * 2.0 ** -24 * mass)  # (as for ordinary rows)
+
+
+def test_results_keep_no_scratch(W):
+    """Few long rows have far more scratch than results: it is not the results' to hold."""
+    x = torch.zeros((5, 2 ** 19), dtype=torch.bfloat16, device=DEV)
+    t = torch.zeros(5, dtype=torch.int64, device=DEV)
+    need = W.token_logprobs_workspace_bytes(5, 2 ** 19, 20)
+    assert need > 20000
+    r = W.token_logprobs(x, t, top=20)
+    assert r.logprob.untyped_storage().nbytes() <= 1024
+    assert r.top_id[0].tolist() == list(range(20))
