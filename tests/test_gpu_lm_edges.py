@@ -47,3 +47,19 @@ def test_results_keep_no_scratch(W):
     r = W.token_logprobs(x, t, top=20)
     assert r.logprob.untyped_storage().nbytes() <= 1024
     assert r.top_id[0].tolist() == list(range(20))
+
+
+def test_gradient_refuses_another_s_result(W):
+    """A result of another vocabulary or scale would give wrong numbers without an error."""
+    x = torch.randn(3, 100, device=DEV)
+    t = torch.zeros(3, dtype=torch.int64, device=DEV)
+    g = torch.ones(3, device=DEV)
+    r = W.token_logprobs(x, t, scale=0.7)
+    want = W.token_logprobs_backward(x, t, r, g, g, scale=0.7)
+    assert torch.equal(W.token_logprobs_backward(x.double().float(), t, r, g, g, scale=0.7), want)
+    with pytest.raises(ValueError):
+        W.token_logprobs_backward(x, t, r, g, g)
+    with pytest.raises(ValueError):
+        W.token_logprobs_backward(x[:, :99], t, r, g, g, scale=0.7)
+    with pytest.raises(ValueError):
+        W.token_logprobs_backward(x[:2], t[:2], r, g[:2], g[:2], scale=0.7)

@@ -1002,10 +1002,10 @@ class TokenLogprobs:
     and entropy; top_logprob float32 and top_id int64 [rows, top] (None for top
     = 0).  row_ref (a logit near the row's largest) and row_sum (of the
     exponentials relative to it) are for the gradient."""
-    __slots__ = ("_buf", "_at", "_n", "_targets", "top_logprob", "top_id")
+    __slots__ = ("_buf", "_at", "_n", "_of", "_targets", "top_logprob", "top_id")
 
-    def __init__(self, buf, at, rows, targets, top_logprob, top_id):
-        self._buf, self._at, self._n, self._targets = buf, at, rows, targets
+    def __init__(self, buf, at, rows, vocab, scale, targets, top_logprob, top_id):
+        self._buf, self._at, self._n, self._of, self._targets = buf, at, rows, (vocab, scale), targets
         self.top_logprob, self.top_id = top_logprob, top_id
 
     def _row(self, i):  # parts of one tensor, taken out when they are asked for
@@ -1073,7 +1073,7 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, workspace=None):
     at = max(need, 0) // 4
     buf = torch.empty(at + 5 * rows, dtype=torch.float32, device=logits.device)
     ws_p, wbytes = _workspace(workspace, dev, "the logits'") if need == 0 else (buf.data_ptr(), need)
-    r = TokenLogprobs(buf, at, rows, t_p is not None, top_logprob, top_id)
+    r = TokenLogprobs(buf, at, rows, vocab, scale, t_p is not None, top_logprob, top_id)
     _check("token_logprobs", _on_device(
         dev, _lib.token_logprobs, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p,
         None if t_p is None else r._ptr(4), r._ptr(0), r._ptr(1), r._ptr(2), r._ptr(3), top, top_lp, top_ip, ws_p, wbytes))
@@ -1083,7 +1083,8 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, workspace=None):
 def token_logprobs_backward(logits, targets, result, dlogprob=None, dentropy=None, *, scale=1.0, out=None):
     """The gradient of the logits for float32 [rows] gradients of `result`'s
     logprob and entropy (either may be None), `result` being token_logprobs's of
-    the same logits, targets and scale.  out: a tensor of the logits' shape and
+    the same logits, targets and scale (one of another shape or scale is
+    refused, other values are not noticed).  out: a tensor of the logits' shape and
     type (out=logits works in place)."""
     ld = _logits("logits", logits)
     (rows, vocab), dev = logits.shape, logits.get_device()
@@ -1094,8 +1095,9 @@ def token_logprobs_backward(logits, targets, result, dlogprob=None, dentropy=Non
         raise ValueError("out must have the logits' dtype")
     t_p = _ints("targets", targets, torch.int64, dev, rows, "the logits'") if targets is not None else None
     of = lambda name, t: _row_floats(name, t, rows, dev) if t is not None else None
-    if not isinstance(result, TokenLogprobs) or result._n != rows or result._buf.get_device() != dev:
-        raise ValueError("result must be token_logprobs's of these logits")
+    if not isinstance(result, TokenLogprobs) or result._n != rows or result._of != (vocab, scale) or \
+            result._buf.get_device() != dev:
+        raise ValueError("result must be token_logprobs's of these logits and this scale")
     _check("token_logprobs_backward", _on_device(
         dev, _lib.token_logprobs_backward, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p,
         result._ptr(1), result._ptr(2), result._ptr(3), of("dlogprob", dlogprob), of("dentropy", dentropy), out.data_ptr(), ldd))
