@@ -63,3 +63,15 @@ def test_gradient_refuses_another_s_result(W):
         W.token_logprobs_backward(x[:, :99], t, r, g, g, scale=0.7)
     with pytest.raises(ValueError):
         W.token_logprobs_backward(x[:2], t[:2], r, g[:2], g[:2], scale=0.7)
+
+
+def test_too_many_of_the_likeliest(W):
+    """More than the library holds is not supported; more than there are is not valid."""
+    x = torch.zeros((2, 100), device=DEV)
+    with pytest.raises(W.WhtqError) as e:
+        W.token_logprobs(x, top=33)
+    assert e.value.status == 2
+    for top in (101, -1):
+        with pytest.raises(W.WhtqError) as e:
+            W.token_logprobs(x, top=top)
+        assert e.value.status == 1

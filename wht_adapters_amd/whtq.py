@@ -1051,8 +1051,8 @@ def token_logprobs_workspace_bytes(rows, vocab, top=0, device="cuda"):
 def token_logprobs(logits, targets=None, *, top=0, scale=1.0, workspace=None):
     """Log probabilities under softmax(scale * logits) of logits [rows, vocab]:
     of targets (int64 [rows]; one outside the vocabulary gives 0), the `top`
-    likeliest tokens of each row (equal logits: the lower index first) and the
-    entropy, in one pass.  workspace: a tensor of
+    (at most 32) likeliest tokens of each row (equal logits: the lower index
+    first) and the entropy, in one pass.  workspace: a tensor of
     token_logprobs_workspace_bytes, allocated here if not given.  Returns
     TokenLogprobs."""
     ld = _logits("logits", logits)
@@ -1072,7 +1072,7 @@ def token_logprobs(logits, targets=None, *, top=0, scale=1.0, workspace=None):
     # a small workspace and the results in one tensor
     at = max(need, 0) // 4
     buf = torch.empty(at + 5 * rows, dtype=torch.float32, device=logits.device)
-    ws_p, wbytes = _workspace(workspace, dev, "the logits'") if need == 0 else (buf.data_ptr(), need)
+    ws_p, wbytes = _workspace(workspace, dev, "the logits'") if need <= 0 else (buf.data_ptr(), need)
     r = TokenLogprobs(buf, at, rows, vocab, scale, t_p is not None, top_logprob, top_id)
     _check("token_logprobs", _on_device(
         dev, _lib.token_logprobs, logits.data_ptr(), _DT[logits.dtype], rows, vocab, ld, scale, t_p,
