@@ -68,7 +68,7 @@ def head_step(head, adapter, x, targets, bonus=0.01):
     logits = head(x) + adapter(x)
     r = whtq.token_logprobs(logits, targets)
     given = (targets >= 0).float()
-    weight = -given / given.sum()
+    weight = -given / given.sum().clamp(min=1)
     dlogits = whtq.token_logprobs_backward(logits, targets, r, weight, bonus * weight)
     return logits, r, dlogits, adapter.gradient(x, dlogits)
 

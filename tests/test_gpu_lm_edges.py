@@ -1,5 +1,8 @@
 """Norms and log probabilities at calls that their documentation allows, or
 refuses, beside those of test_gpu_qk_norm.py and test_gpu_logprob.py."""
+import os
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +11,7 @@ from oracle import lm
 from tests.gpu_util import DEV, host64
 
 pytestmark = pytest.mark.gpu
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 
 @pytest.fixture(scope="module")
@@ -75,3 +79,15 @@ def test_too_many_of_the_likeliest(W):
         with pytest.raises(W.WhtqError) as e:
             W.token_logprobs(x, top=top)
         assert e.value.status == 1
+
+
+def test_example_without_targets():
+    """A batch of nothing but padding has a gradient of 0, with the bonus for entropy too."""
+    import score_and_adapt as E
+    from kv_cache_decode import Linear
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    bits = torch.randint(-2 ** 31, 2 ** 31 - 1, (128,), dtype=torch.int32, device=DEV, generator=gen)
+    head, adapter = Linear(256, 4096, bits, gen), E.Adapter(256, 4096, 4000, 1, DEV)
+    x = torch.randn(4, 4096, device=DEV, generator=gen).bfloat16()
+    *_, dlogits, dc = E.head_step(head, adapter, x, torch.full((4,), -1, dtype=torch.int64, device=DEV), 0.1)
+    assert (dlogits == 0).all() and (dc == 0).all()
