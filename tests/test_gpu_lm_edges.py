@@ -9,8 +9,10 @@ import torch
 
 from oracle import lm
 from tests.gpu_util import DEV, host64
+from tests.test_gpu_logprob import DTS, check, make
 
-pytestmark = pytest.mark.gpu
+# (infinities are subtracted in the bounds and then left out)
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:invalid value encountered")]
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 
@@ -79,6 +81,27 @@ def test_too_many_of_the_likeliest(W):
         with pytest.raises(W.WhtqError) as e:
             W.token_logprobs(x, top=top)
         assert e.value.status == 1
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("rows,vocab,offset", [
+    (2, 4096, 1), (3, 4095, 7), (2, 32761, 7), (2, 32762, 0), (3, 32762, 7), (2, 32767, 1), (2, 32768, 0), (5, 32768, 3),
+    (2, 262144, 3), (650, 32768, 7)])
+def test_at_the_borders_of_the_rules(W, dtype, rows, vocab, offset):
+    """Either side of the lengths from which rows are split and groups of logits get longer; rows that begin inside 16
+    bytes have one group more than the same row aligned, which may be more than are picked from at once."""
+    rng = np.random.default_rng(rows + vocab + offset)
+    x, xd = make(rng, min(rows, 5), vocab, dtype, offset)
+    if rows > 5:  # the same few again and again
+        storage = torch.empty((rows, vocab + offset + 3), dtype=dtype, device=DEV)
+        storage[:, offset:offset + vocab] = x.to(DEV).repeat(rows // 5, 1)
+        xd = storage[:, offset:offset + vocab]
+    t = rng.integers(0, vocab, min(rows, 5))
+    r = W.token_logprobs(xd, torch.from_numpy(t).to(DEV).repeat(max(1, rows // 5)), top=32)
+    if rows > 5:
+        names = ("logprob", "lse", "entropy", "row_ref", "row_sum", "top_logprob", "top_id")
+        r = type("Last", (), {n: getattr(r, n)[-5:] for n in names})
+    check(r, host64(x), t, 1.0, 32)
 
 
 def test_example_without_targets():

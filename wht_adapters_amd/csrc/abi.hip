@@ -1225,9 +1225,10 @@ LpPlan lp_plan(int64_t rows, int64_t vocab, int64_t top, int cus) {
                  ? 1
                  : (int)std::max<int64_t>(1, std::min(8 * (int64_t)cus / std::max<int64_t>(rows, 1), chunks / 16));
   if (top) {
-    // groups enough that the last one's maximum leaves few candidates (64 and more of them, 512 at most but for
-    // vocabularies above 262144), large enough that their maxima are few bytes
-    p.width = vocab <= 4096 ? 8 : vocab <= 32768 ? 64 : LP_CHUNK;
+    // groups enough that the last one's maximum leaves few candidates, large enough that their maxima are few bytes: at
+    // most 512 up to 262144 logits, but for a row of 4096, 32768 or 262144 that does not begin at 16 bytes (one more, and
+    // they are picked from in pairs).  A row over several blocks has more than 64 chunks, each a group.
+    p.width = p.splits > 1 || vocab > 32768 ? LP_CHUNK : vocab <= 4096 ? 8 : 64;
     p.groups = (int)((vocab + 7 + p.width - 1) / p.width);  // (7: a row may begin inside 16 bytes)
   }
   // a block that has all of its row keeps both to itself

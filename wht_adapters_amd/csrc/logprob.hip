@@ -589,8 +589,6 @@ hipError_t rows_launch(LpArgs a, hipStream_t s) {
     else if (whole && a.width == 8) hipLaunchKernelGGL((k_lp_row<DT, 1, true>), grid, dim3(256), 0, s, a);
     else if (whole && a.width == 64) hipLaunchKernelGGL((k_lp_row<DT, 8, true>), grid, dim3(256), 0, s, a);
     else if (whole) hipLaunchKernelGGL((k_lp_row<DT, 64, true>), grid, dim3(256), 0, s, a);
-    else if (a.width == 8) hipLaunchKernelGGL((k_lp_row<DT, 1, false>), grid, dim3(256), 0, s, a);
-    else if (a.width == 64) hipLaunchKernelGGL((k_lp_row<DT, 8, false>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_lp_row<DT, 64, false>), grid, dim3(256), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
