@@ -200,21 +200,13 @@ static hipError_t by_tokens(int64_t tokens, int64_t per, int lanes, F launch) {
   return hipSuccess;
 }
 
-#define KV_DISPATCH(KERNEL, D, T, INT4, GRID, S, ARGS)                                                      \
-  do {                                                                                                      \
-    if ((D) == 128 && (T) == KV_BF16 && (INT4)) hipLaunchKernelGGL((KERNEL<128, KV_BF16, true>), GRID, dim3(256), 0, S, ARGS); \
-    else if ((D) == 128 && (T) == KV_BF16) hipLaunchKernelGGL((KERNEL<128, KV_BF16, false>), GRID, dim3(256), 0, S, ARGS);     \
-    else if ((D) == 128 && (INT4)) hipLaunchKernelGGL((KERNEL<128, KV_F16, true>), GRID, dim3(256), 0, S, ARGS);               \
-    else if ((D) == 128) hipLaunchKernelGGL((KERNEL<128, KV_F16, false>), GRID, dim3(256), 0, S, ARGS);                        \
-    else if ((T) == KV_BF16 && (INT4)) hipLaunchKernelGGL((KERNEL<64, KV_BF16, true>), GRID, dim3(256), 0, S, ARGS);           \
-    else if ((T) == KV_BF16) hipLaunchKernelGGL((KERNEL<64, KV_BF16, false>), GRID, dim3(256), 0, S, ARGS);                    \
-    else if ((INT4)) hipLaunchKernelGGL((KERNEL<64, KV_F16, true>), GRID, dim3(256), 0, S, ARGS);                              \
-    else hipLaunchKernelGGL((KERNEL<64, KV_F16, false>), GRID, dim3(256), 0, S, ARGS);                                         \
-  } while (0)
-
 template <int D, int T, bool INT4>
 static void append_launch(const KvAppendArgs& a, dim3 grid, hipStream_t s) {
   hipLaunchKernelGGL((k_kv_append<D, T, INT4>), grid, dim3(256), 0, s, a);
+}
+template <int D, int T, bool INT4>
+static void gather_launch(const KvGatherArgs& a, dim3 grid, hipStream_t s) {
+  hipLaunchKernelGGL((k_kv_gather<D, T, INT4>), grid, dim3(256), 0, s, a);
 }
 
 hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const void* k,
@@ -262,7 +254,7 @@ hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_
     (void)hipGetDevice(&dev);
     const bool apart = ko && vo && 2 * n * per * (dim / 16) <= 2048 * (int64_t)device_cu_count(dev);
     const dim3 grid((unsigned)((n * per + rb - 1) / rb), apart ? 2 : 1);
-    KV_DISPATCH(k_kv_gather, dim, dt, int4, grid, s, a);
+    KV_PICK(gather_launch, dim, dt, int4, a, grid, s);
   });
 }
 

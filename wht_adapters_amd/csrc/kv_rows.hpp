@@ -7,6 +7,8 @@
 // cover contiguous runs.
 #pragma once
 
+#include <type_traits>
+
 #include "kv.hpp"
 
 namespace whtq {
@@ -31,68 +33,13 @@ struct KvNorm {
   float eps;
 };
 
-// The two chunks of a lane rotated in place (BACK: by the opposite angle).
-// Each product and each sum is rounded by itself (no contraction), so the
-// result is the same wherever it is computed.  `load` gives a chunk of the
-// row as it was before the rotation.
-template <int D, bool BACK = false, typename Load>
-__device__ __forceinline__ void kv_rotate(float (&x)[16], const KvTurn& a, int64_t pos, int i, Load load) {
-#pragma clang fp contract(off)
-  constexpr int L = D / 16;
-  const float* cs = a.cos + pos * a.ld;
-  const float* sn = a.sin + pos * a.ld;
-  if (!a.interleaved && a.rot == D) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4 c = ldg<f32x4>(cs + 8 * i + 4 * h);
-      f32x4 s = ldg<f32x4>(sn + 8 * i + 4 * h);
-      if constexpr (BACK) s = -s;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float u = x[4 * h + e], w = x[8 + 4 * h + e];
-        x[4 * h + e] = u * c[e] - w * s[e];
-        x[8 + 4 * h + e] = w * c[e] + u * s[e];
-      }
-    }
-    return;
-  }
-  const int pair = a.rot / 16;  // chunks in a half
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const int ch = i + b * L;
-    if (ch * 8 >= a.rot) continue;
-    if (a.interleaved) {
-      const f32x4 c = ldg<f32x4>(cs + 4 * ch);
-      f32x4 s = ldg<f32x4>(sn + 4 * ch);
-      if constexpr (BACK) s = -s;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float u = x[8 * b + 2 * e], w = x[8 * b + 2 * e + 1];
-        x[8 * b + 2 * e] = u * c[e] - w * s[e];
-        x[8 * b + 2 * e + 1] = w * c[e] + u * s[e];
-      }
-    } else {
-      const bool low = ch < pair;
-      const int at = low ? ch : ch - pair;
-      float o[8];
-      load(low ? ch + pair : ch - pair, o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float c = cs[8 * at + e], s = BACK ? -sn[8 * at + e] : sn[8 * at + e], u = x[8 * b + e];
-        const float os = o[e] * s;
-        x[8 * b + e] = low ? u * c - os : u * c + os;
-      }
-    }
-  }
-}
-
 // The ways of a rotation, each a kernel of its own where registers count: a
 // whole row in halves, interleaved pairs, or halves of a part of the row.
 enum KvWay : int { KV_STILL = 0, KV_HALVES = 1, KV_PAIRS = 2, KV_PART = 3 };
 inline int kv_way(const KvTurn& a, int dim) {
   return !a.pos ? KV_STILL : a.interleaved ? KV_PAIRS : a.rot == dim ? KV_HALVES : KV_PART;
 }
-// kv_rotate with the table's entries taken beforehand (but for KV_PART, whose
+// The table's entries of a lane, taken beforehand (but for KV_PART, whose
 // pairs lie in other lanes).
 struct KvCs {
   f32x4 c[2], s[2];
@@ -111,10 +58,33 @@ __device__ __forceinline__ void kv_load_cs(KvCs& t, const KvTurn& a, int64_t pos
     }
   }
 }
+// The two chunks of a lane rotated in place (BACK: by the opposite angle).
+// Each product and each sum is rounded by itself (no contraction), so the
+// result is the same wherever it is computed.  `load` gives a chunk of the
+// row as it was before the rotation (KV_PART).
 template <int D, int WAY, bool BACK, typename Load>
 __device__ __forceinline__ void kv_turn(float (&x)[16], const KvTurn& a, const KvCs& t, int64_t pos, int i, Load load) {
 #pragma clang fp contract(off)
-  if constexpr (WAY == KV_PART) kv_rotate<D, BACK>(x, a, pos, i, load);
+  if constexpr (WAY == KV_PART) {
+    const float* cs = a.cos + pos * a.ld;
+    const float* sn = a.sin + pos * a.ld;
+    const int pair = a.rot / 16;  // chunks in a half
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int ch = i + b * (D / 16);
+      if (ch * 8 >= a.rot) continue;
+      const bool low = ch < pair;
+      const int at = low ? ch : ch - pair;
+      float o[8];
+      load(low ? ch + pair : ch - pair, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float c = cs[8 * at + e], s = BACK ? -sn[8 * at + e] : sn[8 * at + e], u = x[8 * b + e];
+        const float os = o[e] * s;
+        x[8 * b + e] = low ? u * c - os : u * c + os;
+      }
+    }
+  }
   if constexpr (WAY == KV_HALVES || WAY == KV_PAIRS) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -130,6 +100,18 @@ __device__ __forceinline__ void kv_turn(float (&x)[16], const KvTurn& a, const K
       }
     }
   }
+}
+// The same where the way is known to the call alone.
+template <int D, typename Load>
+__device__ __forceinline__ void kv_rotate(float (&x)[16], const KvTurn& a, int64_t pos, int i, Load load) {
+  auto by = [&](auto way) __attribute__((always_inline)) {
+    KvCs t;
+    kv_load_cs<D, way.value>(t, a, pos, i);
+    kv_turn<D, way.value, false>(x, a, t, pos, i, load);
+  };
+  if (a.interleaved) by(std::integral_constant<int, KV_PAIRS>{});
+  else if (a.rot == D) by(std::integral_constant<int, KV_HALVES>{});
+  else by(std::integral_constant<int, KV_PART>{});
 }
 
 // Butterflies between lanes whose values differ in lane bit M.
@@ -225,14 +207,12 @@ __device__ __forceinline__ float kv_rms(const float (&x)[16], float eps) {
   for (int e = 0; e < 16; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
   return rsqrtf(kv_row_sum<D / 16>(ss) * (1.f / D) + eps);
 }
-// The lane's chunks times r and their weights; returns r.  Without weights the row is left as it is.
+// The lane's chunks times r and their weights; returns r.
 template <int D>
 __device__ __forceinline__ float kv_norm(float (&x)[16], const uint8_t* w, int dt, float eps, int i) {
   const float r = kv_rms<D>(x, eps);
-  if (w) {
-    kv_weigh8(x, w, dt, i, r);
-    kv_weigh8(x + 8, w, dt, i + D / 16, r);
-  }
+  kv_weigh8(x, w, dt, i, r);
+  kv_weigh8(x + 8, w, dt, i + D / 16, r);
   return r;
 }
 
