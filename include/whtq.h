@@ -536,8 +536,14 @@ typedef struct {
  * eps)^-1/2, before it is rotated.  q and k are weights of dim contiguous
  * values in `dtype` (fp32, bf16 or fp16; 16-byte aligned): one vector for all
  * heads with a head stride of 0, or one a head (strides in elements, 16-byte
- * aligned in bytes).  eps >= 0.
+ * aligned in bytes).  eps >= 0.  dtype may carry WHTQ_CLEAR_Q and WHTQ_CLEAR_K
+ * (dtype | flag): the dense output rows of a token whose position lies outside
+ * [0, max_position), q_out's (backward: dq's) or k_out's (dk's), become 0;
+ * without the flag they stay as they are.
  */
+#define WHTQ_CLEAR_Q 0x100
+#define WHTQ_CLEAR_K 0x200
+
 typedef struct {
   const void* q;
   const void* k;
@@ -590,16 +596,17 @@ whtq_status kv_append_norm(const whtq_kv_cache* cache, const void* k, const int6
  *   pointers: that side is absent), weights of both sides, rope NULL for no
  *   rotation.  dim 64 or 128, dtype bf16 or fp16.  Output rows may be the
  *   input's own (equal pointer and strides).  A token whose position lies
- *   outside [0, max_position) leaves its output rows alone.
+ *   outside [0, max_position) leaves its output rows alone, or clears them
+ *   (WHTQ_CLEAR_Q, WHTQ_CLEAR_K).
  * qk_norm_rope_backward -- from the gradients of the outputs (dq_out, dk_out)
  *   and the same inputs, the rows' gradients
  *     dx = r (u - x r^2 mean(u x)),  u = w g,  g = R(position)^T dy
  *   in `dtype`, and the weights' sum g x r over the tokens (and heads that
  *   share them) as fp32 dq_norm, dk_norm [dim], or [heads][dim] where the
  *   weights have a head stride.  dq, dk may be dq_out's, dk_out's or q's, k's
- *   own rows.  A token outside the positions leaves its rows alone and adds
- *   nothing; no tokens give weights' gradients of 0.  A row whose squares
- *   overflow has gradients of 0 (its output is 0).
+ *   own rows.  A token outside the positions leaves its rows alone, or clears
+ *   them, and adds nothing; no tokens give weights' gradients of 0.  A row
+ *   whose squares overflow has gradients of 0 (its output is 0).
  *   workspace: device memory of ..._workspace_bytes (16-byte aligned; may be
  *   NULL when that is 0), overwritten.  fp32 sums; deterministic.
  */

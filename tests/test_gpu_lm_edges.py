@@ -44,6 +44,41 @@ def test_gradient_of_rows_whose_squares_overflow(W):
     assert np.all(np.abs(host64(dwq) - dw) <= (12 + 40 + 14 + 2) * 2.0 ** -24 * mass)  # (as for ordinary rows)
 
 
+def test_rows_outside_the_positions(W):
+    """A padded batch: rows that were not given are 0 there, forward and backward (whatever the memory held), and an
+    adapter's gradient, summed over all rows, is that of the tokens alone.  Rows that were given stay as they were."""
+    rng = np.random.default_rng(32)
+    n, d = 70, 128
+    q, k, dqo, dko = (torch.from_numpy(rng.standard_normal((n, h, d)).astype(np.float32)).bfloat16().to(DEV)
+                      for h in (8, 2, 8, 2))
+    w = torch.from_numpy(rng.standard_normal(d).astype(np.float32)).to(DEV)
+    angle = np.arange(50)[:, None] * 10000.0 ** (-np.arange(0, d, 2) / d)
+    cos, sin = (torch.from_numpy(f(angle).astype(np.float32)).to(DEV) for f in (np.cos, np.sin))
+    pos = torch.arange(n, dtype=torch.int32, device=DEV) % 50
+    gone = [0, 13, 14, 69]
+    pos[gone] = torch.tensor([-1, 50, -2 ** 31, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    keep = torch.tensor([t for t in range(n) if t not in gone], device=DEV)
+    for kw in (dict(), dict(rot_dim=48), dict(interleaved=True)):
+        kw.update(q_norm=w, k_norm=w, cos=cos, sin=sin)
+        for _ in range(3):  # freed memory of NaN is what the next allocations get
+            torch.full((2 ** 22,), float("nan"), dtype=torch.bfloat16, device=DEV)
+            held = [torch.full_like(t, float("nan")) for t in (q, k, q, k)]
+            del held
+            outs = W.qk_norm_rope(q, k, positions=pos, **kw)
+            grads = W.qk_norm_rope_backward(dqo, dko, q, k, positions=pos, **kw)
+            assert all((t[gone] == 0).all() for t in (*outs, *grads[:2]))
+        part = [t[keep] for t in (dqo, dko, q, k)]
+        want = (*W.qk_norm_rope(*part[2:], positions=pos[keep], **kw),
+                *W.qk_norm_rope_backward(*part, positions=pos[keep], **kw)[:2])
+        assert all(torch.equal(a[keep], b) for a, b in zip((*outs, *grads[:2]), want))
+        three = torch.full_like(q, 3.0)
+        yq, yk = W.qk_norm_rope(q, k, positions=pos, q_out=three, **kw)
+        assert (yq[gone] == 3).all() and (yk[gone] == 0).all()
+        three = torch.full_like(k, 3.0)
+        dq, dk, *_ = W.qk_norm_rope_backward(dqo, dko, q, k, positions=pos, dk=three, **kw)
+        assert (dq[gone] == 0).all() and (dk[gone] == 3).all()
+
+
 def test_results_keep_no_scratch(W):
     """Few long rows have far more scratch than results: it is not the results' to hold."""
     x = torch.zeros((5, 2 ** 19), dtype=torch.bfloat16, device=DEV)

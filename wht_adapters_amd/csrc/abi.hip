@@ -807,18 +807,19 @@ KvTurn kv_turn_of(const whtq_rope* r) {
   return KvTurn{r->cos, r->sin, r->positions, r->ld, r->max_position, r->rot_dim, r->interleaved};
 }
 // the rules of norm weights, but for alignment
+int kv_norm_dtype(const whtq_qk_norm* n) { return n->dtype & ~(WHTQ_CLEAR_Q | WHTQ_CLEAR_K); }
 whtq_status kv_norm_check(const whtq_qk_norm* n) {
-  if (!dt_valid(n->dtype) || !std::isfinite(n->eps) || n->eps < 0.f) return WHTQ_EINVAL;
+  if (!dt_valid(kv_norm_dtype(n)) || !std::isfinite(n->eps) || n->eps < 0.f) return WHTQ_EINVAL;
   if (n->q_head < 0 || n->k_head < 0) return WHTQ_EINVAL;
   return WHTQ_OK;
 }
 bool kv_norm_aligned(const whtq_qk_norm* n) {
-  const int64_t esz = dt_bytes(n->dtype);
+  const int64_t esz = dt_bytes(kv_norm_dtype(n));
   return aligned16(n->q) && aligned16(n->k) && !(n->q_head * esz & 15) && !(n->k_head * esz & 15);
 }
 KvNorm kv_norm_of(const whtq_qk_norm* n) {
-  const int64_t esz = dt_bytes(n->dtype);
-  return KvNorm{{(const uint8_t*)n->q, n->q_head * esz}, {(const uint8_t*)n->k, n->k_head * esz}, n->dtype, n->eps};
+  const int64_t esz = dt_bytes(kv_norm_dtype(n));
+  return KvNorm{{(const uint8_t*)n->q, n->q_head * esz}, {(const uint8_t*)n->k, n->k_head * esz}, kv_norm_dtype(n), n->eps};
 }
 
 // how an attention call runs: which kernel, and over how many blocks the keys of a row are split
@@ -966,7 +967,7 @@ whtq_status kv_append_norm(const whtq_kv_cache* cache, const void* k, const int6
   QkForwardArgs a{};
   a.f[0] = {kv_rows_of(k, k_stride), {}, c.k, n.k, rope != nullptr, {}, 0, 0};
   a.f[1] = {kv_rows_of(v, v_stride), {}, c.v, {}, false, {}, 0, 0};
-  if (q) a.f[2] = {kv_rows_of(q, q_stride), kv_rows_of(q_out, q_out_stride), {}, n.q, rope != nullptr, {}, 0, 0};
+  if (q) a.f[2] = {kv_rows_of(q, q_stride), kv_rows_of(q_out, q_out_stride), {}, n.q, rope != nullptr, {}, 0, 0, (norm->dtype & WHTQ_CLEAR_Q) != 0};
   a.c = c;
   a.slots = slots;
   a.capacity = capacity;
@@ -1137,8 +1138,8 @@ whtq_status qk_norm_rope(const void* q, const int64_t* q_stride, int64_t heads, 
   if (st != WHTQ_OK) return st;
   const KvNorm n = kv_norm_of(norm);
   QkForwardArgs a{};
-  if (heads) a.f[0] = {kv_rows_of(q, q_stride), kv_rows_of(q_out, q_out_stride), {}, n.q, rope != nullptr, {}, 0, 0};
-  if (kv_heads) a.f[1] = {kv_rows_of(k, k_stride), kv_rows_of(k_out, k_out_stride), {}, n.k, rope != nullptr, {}, 0, 0};
+  if (heads) a.f[0] = {kv_rows_of(q, q_stride), kv_rows_of(q_out, q_out_stride), {}, n.q, rope != nullptr, {}, 0, 0, (norm->dtype & WHTQ_CLEAR_Q) != 0};
+  if (kv_heads) a.f[1] = {kv_rows_of(k, k_stride), kv_rows_of(k_out, k_out_stride), {}, n.k, rope != nullptr, {}, 0, 0, (norm->dtype & WHTQ_CLEAR_K) != 0};
   a.turn = kv_turn_of(rope);
   a.dt = n.dt;
   a.eps = n.eps;
@@ -1178,9 +1179,9 @@ whtq_status qk_norm_rope_backward(const void* dq_out, const int64_t* dq_out_stri
   const KvNorm n = kv_norm_of(norm);
   QkArgs a{};
   a.q = {kv_rows_of(q, q_stride), kv_rows_of(dq_out, dq_out_stride), kv_rows_of(dq, dq_stride), n.q, dq_norm, (int)heads,
-         qk_classes(heads, norm->q_head), 0};
+         qk_classes(heads, norm->q_head), 0, (norm->dtype & WHTQ_CLEAR_Q) != 0};
   a.k = {kv_rows_of(k, k_stride), kv_rows_of(dk_out, dk_out_stride), kv_rows_of(dk, dk_stride), n.k, dk_norm, (int)kv_heads,
-         qk_classes(kv_heads, norm->k_head), 0};
+         qk_classes(kv_heads, norm->k_head), 0, (norm->dtype & WHTQ_CLEAR_K) != 0};
   a.turn = kv_turn_of(rope);
   a.tokens = tokens;
   a.dt = n.dt;

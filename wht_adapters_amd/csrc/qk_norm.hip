@@ -67,7 +67,11 @@ __global__ __launch_bounds__(256) void k_qk_norm(const QkForwardArgs a) {
       if (w) kv_weigh8(o, w, a.dt, ch, r);
     });
   if (f.out.p) {
-    if (!ok) return;
+    if (!ok) {
+      if (!live || !f.clear) return;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = 0.f;
+    }
     uint8_t* o = const_cast<uint8_t*>(f.out.p) + t * f.out.tok + h * f.out.head;
     stg<u32x4>(o + 16 * i, kv_round8<T>(x));
     stg<u32x4>(o + 16 * (i + L), kv_round8<T>(x + 8));
@@ -100,7 +104,14 @@ __global__ __launch_bounds__(256) void k_qk_norm_back(const QkArgs a) {
     const uint8_t* dp = s.dy.p + t * s.dy.tok + h * s.dy.head;
     const u32x4 x0 = ldg<u32x4>(xp + 16 * i), x1 = ldg<u32x4>(xp + 16 * (i + L));
     const u32x4 g0 = ldg<u32x4>(dp + 16 * i), g1 = ldg<u32x4>(dp + 16 * (i + L));
-    if (WAY && (pos < 0 || pos >= a.turn.max_pos)) continue;
+    uint8_t* o = const_cast<uint8_t*>(s.dx.p) + t * s.dx.tok + h * s.dx.head;
+    if (WAY && (pos < 0 || pos >= a.turn.max_pos)) {
+      if (s.clear) {
+        stg<u32x4>(o + 16 * i, u32x4{0u, 0u, 0u, 0u});
+        stg<u32x4>(o + 16 * (i + L), u32x4{0u, 0u, 0u, 0u});
+      }
+      continue;
+    }
     KvCs cs;
     kv_load_cs<D, WAY>(cs, a.turn, pos, i);
     float x[16], g[16];
@@ -123,7 +134,6 @@ __global__ __launch_bounds__(256) void k_qk_norm_back(const QkArgs a) {
     dot = kv_row_sum<L>(dot) * (1.f / D);
 #pragma unroll
     for (int e = 0; e < 16; ++e) g[e] = r * (g[e] - x[e] * dot);
-    uint8_t* o = const_cast<uint8_t*>(s.dx.p) + t * s.dx.tok + h * s.dx.head;
     stg<u32x4>(o + 16 * i, kv_round8<T>(g));
     stg<u32x4>(o + 16 * (i + L), kv_round8<T>(g + 8));
   }

@@ -19,6 +19,7 @@ struct QkForward {
   bool turned;     // rotated
   KvDiv heads;
   uint32_t rows, blocks;
+  bool clear;      // rows of out whose token is outside the positions become 0
 };
 struct QkForwardArgs {
   QkForward f[3];
@@ -37,6 +38,7 @@ struct QkSide {  // backward: queries or keys; heads 0: none
   int heads;
   int classes;  // weight vectors: 1 or heads
   int blocks;   // blocks of a class
+  bool clear;   // rows of dx whose token is outside the positions become 0
 };
 struct QkArgs {
   QkSide q, k;

@@ -702,6 +702,7 @@ def kv_cache_alloc(num_pages, page_size, kv_heads, dim, *, int4=False, dtype=tor
 
 
 _NORM_DT = frozenset((torch.float32, torch.bfloat16, torch.float16))
+_CLEAR_Q, _CLEAR_K = 0x100, 0x200  # WHTQ_CLEAR_Q, WHTQ_CLEAR_K
 _pair = functools.lru_cache(maxsize=1024)(lambda a, b: (_i64 * 2)(a, b))  # strides as the library takes them
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -804,7 +805,9 @@ def kv_append(cache, k, v, slots, *, q=None, cos=None, sin=None, positions=None,
     2] tables, or None for no rotation; positions: int32 [tokens].  q_norm,
     k_norm: weights of norms of each head vector before the rotation, [dim] or
     [heads, dim] (x / sqrt(mean x^2 + norm_eps) * weight; None: no norm).
-    Returns the rotated queries (q_out, q's shape; q_out=q rotates in place)."""
+    Returns the rotated queries (q_out, q's shape; q_out=q rotates in place).  A
+    token whose position lies outside the tables is not written anywhere: its
+    rows of a q_out allocated here are undefined."""
     dtype = _rows_dtype("k", k, cache)
     tokens, dev = k.shape[0], cache._dev
     ks = _head_rows("k", k, cache, tokens, cache.kv_heads, dtype)
@@ -857,9 +860,12 @@ def qk_norm_rope(q, k, *, q_norm, k_norm, norm_eps=1e-6, cos=None, sin=None, pos
     """Norms of each head vector of q [tokens, heads, dim] and k [tokens,
     kv_heads, dim] with weights [dim] or [heads, dim], then their rotation, as
     in kv_append, into dense rows.  Returns (q_out, k_out); q_out=q and k_out=k
-    work in place."""
+    work in place.  A token whose position lies outside the tables (-1 for
+    padding) leaves its rows of a given q_out or k_out as they are; of those
+    allocated here they are 0."""
     dtype, dev, tokens, heads, kv_heads, dim, rows, qs, ks, norm, rope = _qk_call(
         q, k, q_norm, k_norm, norm_eps, cos, sin, positions, rot_dim, interleaved)
+    norm.dtype |= (_CLEAR_Q if q_out is None else 0) | (_CLEAR_K if k_out is None else 0)
     q_out = _rows_like(q) if q_out is None else q_out
     k_out = _rows_like(k) if k_out is None else k_out
     qos, kos = rows("q_out", q_out, heads), rows("k_out", k_out, kv_heads)
@@ -873,14 +879,17 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, *, q_norm, k_norm, norm_eps=1e-6
     """The gradients of qk_norm_rope's inputs from those of its outputs and the
     same inputs: (dq, dk, dq_norm, dk_norm), the weights' in float32 and their
     shape.  dq and dk may be any rows of q's and k's shapes, dq_out and dk_out
-    among them.  workspace: a tensor of qk_norm_rope_backward_workspace_bytes,
-    allocated here if not given."""
+    among them.  A token outside the tables adds nothing to the weights'
+    gradients; its rows of a given dq or dk stay as they are, of those allocated
+    here they are 0.  workspace: a tensor of
+    qk_norm_rope_backward_workspace_bytes, allocated here if not given."""
     dtype, dev, tokens, heads, kv_heads, dim, rows, qs, ks, norm, rope = _qk_call(
         q, k, q_norm, k_norm, norm_eps, cos, sin, positions, rot_dim, interleaved)
     for nm, t in (("q_norm", q_norm), ("k_norm", k_norm)):
         if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) == 0:
             raise ValueError(f"{nm} is one vector expanded over the heads: pass it as [dim], its gradient is one vector too")
     dqos, dkos = rows("dq_out", dq_out, heads), rows("dk_out", dk_out, kv_heads)
+    norm.dtype |= (_CLEAR_Q if dq is None else 0) | (_CLEAR_K if dk is None else 0)
     dq = _rows_like(q) if dq is None else dq
     dk = _rows_like(k) if dk is None else dk
     dqs, dks = rows("dq", dq, heads), rows("dk", dk, kv_heads)
