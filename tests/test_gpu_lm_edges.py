@@ -1,5 +1,6 @@
 """Norms and log probabilities at calls that their documentation allows, or
 refuses, beside those of test_gpu_qk_norm.py and test_gpu_logprob.py."""
+import ctypes
 import os
 import sys
 
@@ -77,6 +78,38 @@ def test_rows_outside_the_positions(W):
         three = torch.full_like(k, 3.0)
         dq, dk, *_ = W.qk_norm_rope_backward(dqo, dko, q, k, positions=pos, dk=three, **kw)
         assert (dq[gone] == 0).all() and (dk[gone] == 3).all()
+
+
+@pytest.mark.parametrize("n", [60, 3000])
+@pytest.mark.parametrize("queries", [True, False])
+def test_one_side_alone(W, n, queries):
+    """The library's call for queries or keys alone (3000 tokens: partial sums are joined): rows as beside the other side."""
+    rng = np.random.default_rng(33)
+    heads, d = 3, 64
+    x, dy = (torch.from_numpy(rng.standard_normal((n, heads, d)).astype(np.float32)).bfloat16().to(DEV) for _ in range(2))
+    w = torch.from_numpy(rng.standard_normal(d).astype(np.float32)).to(DEV)
+    both = (W.qk_norm_rope(x, x, q_norm=w, k_norm=w)[1 - queries],
+            W.qk_norm_rope_backward(dy, dy, x, x, q_norm=w, k_norm=w)[1 - queries])
+    lib, st = W.raw(), (ctypes.c_int64 * 2)(heads * d, d)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    norm = W._Norm(p(w) if queries else 0, 0 if queries else p(w), 0, 0, W.F32, 1e-6)
+
+    def sides(*own):  # pointer, stride and count where they stand, for either side
+        gone = tuple(0 if v == heads else None for v in own)
+        return (*own, *gone) if queries else (*gone, *own)
+    y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(d, device=DEV)
+    s = torch.cuda.current_stream().cuda_stream
+    assert lib.qk_norm_rope(*sides(p(x), st, heads), W.BF16, d, n, norm, None, *sides(p(y), st), s) == 0
+    need = lib.qk_norm_rope_backward_workspace_bytes(*((heads, 0) if queries else (0, heads)), d, n, norm)
+    assert (need > 0) == (n == 3000)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+    assert lib.qk_norm_rope_backward(*sides(p(dy), st, p(x), st, heads), W.BF16, d, n, norm, None, *sides(p(dx), st),
+                                     p(dw) if queries else None, None if queries else p(dw), p(ws), need, s) == 0
+    assert torch.equal(y, both[0]) and torch.equal(dx, both[1])
+    x64, dy64 = host64(x), host64(dy)
+    _, want = lm.norm_rope_backward(dy64, x64, host64(w), 1e-6)
+    # a term: r (14 units) and a product (2); no more additions in a row than a lane's turns (6 at 3000 tokens) and 60 joins
+    assert np.all(np.abs(host64(dw) - want) <= (6 + 60 + 16) * 2.0 ** -24 * np.abs(dy64 * x64 * lm.rms(x64, 1e-6)).sum((0, 1)))
 
 
 def test_results_keep_no_scratch(W):
