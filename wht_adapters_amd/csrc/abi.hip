@@ -806,7 +806,7 @@ KvTurn kv_turn_of(const whtq_rope* r) {
   if (!r) return KvTurn{};
   return KvTurn{r->cos, r->sin, r->positions, r->ld, r->max_position, r->rot_dim, r->interleaved};
 }
-// the rules of norm weights, but for alignment
+// the type of norm weights; their rules, but for alignment
 int kv_norm_dtype(const whtq_qk_norm* n) { return n->dtype & ~(WHTQ_CLEAR_Q | WHTQ_CLEAR_K); }
 whtq_status kv_norm_check(const whtq_qk_norm* n) {
   if (!dt_valid(kv_norm_dtype(n)) || !std::isfinite(n->eps) || n->eps < 0.f) return WHTQ_EINVAL;
@@ -838,13 +838,15 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
   const int64_t group = heads / c->kv_heads, kvh = c->kv_heads;
   const bool int4 = c->format == WHTQ_KV_INT4;
   p.splits = 1;
-  // Figures here are of bf16 rows, 32 heads on 8 of 128 unless said.  The step
+  // Figures here are of bf16 rows, 32 heads on 8 of 128 unless said: a call in a
+  // captured graph of calls on caches in turn, all of one machine.  The step
   // kernel reads an INT4 row once for up to 32 rows (32 sequences of 1000 to
-  // 1500 keys, 4 tokens each: 27 us against the chunk kernel's 93, 8 tokens: 77
-  // against 99) and shares ragged sequences evenly (64 of 17 to 8191 keys, 16-bit
-  // pages, 2 tokens each: 110 us against 121, 4 tokens: 114 against 111).  With 17
-  // to 32 rows of 16-bit pages it would hold 300 registers: 58 us against the
-  // chunk kernel's 30 (128 sequences of 1000 to 1500 keys, 32 heads on one).
+  // 1500 keys, 4 tokens each: 19 us against the chunk kernel's 55, 8 tokens: 54
+  // against 59; under a window of 700 with 4 sinks 18 and 42, 41 and 43) and
+  // shares ragged sequences evenly (64 of 17 to 8191 keys, 16-bit pages, 2 tokens
+  // each: 110 us against 126, 4 tokens: 113 with either).  With 17 to 32 rows of
+  // 16-bit pages it would hold 255 + 132 registers: 41 us against the chunk
+  // kernel's 33 (128 sequences of 1000 to 1500 keys, 32 heads on one).
   p.step = max_q * group <= (int4 ? 32 : 16);
   if (p.step) {
     p.nq = max_q * group <= 16 ? 1 : 2;
@@ -852,9 +854,9 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
     // A block of 8 waves takes a whole sequence, which saves the joining
     // kernel, when every block has a CU at once and its sequence is short, the
     // shorter the fewer blocks there are.  One token, 16-bit pages (a unit is
-    // 256 keys), whole against shared, us: 64 keys 7.5 and 9.1; 32 sequences
-    // (256 blocks) of 1024 keys 26.6 and 28.8; 16 of 512 keys 14.4 and 16.1; but
-    // 4 of 512 keys 13.7 and 11.6, 64 of 256 keys 26.0 and 19.0.
+    // 256 keys), whole against shared, us: 64 keys 5.5 and 7.3, 256 keys 8.6 and
+    // 9.7; 32 sequences (256 blocks) of 1024 keys 28.8 and 32.8; 16 of 512 keys
+    // 14.2 and 16.3; but 4 of 512 keys 11.1 and 10.5, 64 of 256 keys 22.4 and 19.7.
     const int64_t unit = kv_step_unit((int)c->dim, int4, true), shared = kv_step_unit((int)c->dim, int4, false);
     if (p.nq == 1 && seqs * kvh <= cus && max_kv <= std::max<int64_t>(1, 4 * seqs * kvh / cus) * unit) {
       p.grid = seqs * kvh;
@@ -868,7 +870,7 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
   } else {
     // INT4 tiles are unpacked once a block: blocks of 8 waves halve that work
     // where there are rows for them (64 heads on 8, 512 tokens over 20000 keys:
-    // 420 us against 470 with 4 waves; 40 tokens: 75 against 71).  16-bit tiles
+    // 370 us against 412 with 4 waves; 40 tokens: 65 against 61).  16-bit tiles
     // cost a copy, and blocks of 4 waves wait for fewer others.
     p.waves = int4 && max_q * group > 128 ? 8 : 4;
     const int64_t rows = 32 * p.waves;
@@ -876,20 +878,20 @@ KvPlan kv_plan(const whtq_kv_cache* c, int64_t q_tokens, int64_t heads, int64_t 
     // of 4 waves need more: 2 are held at 64 dims and, with fp16 rows, 1 at 128
     // dims.  Counting those instead helps as often as it hurts, because blocks
     // that sequences do not fill are not counted either (INT4, fp16 rows, 128
-    // dims: 12 x 8 rows on 8 key heads over 33000 keys 72 -> 59 us, 100 rows on
-    // 32 over 4000 53 -> 41, but 24 sequences of 16 x 4 rows on 8 over 4000 160
-    // -> 196; 64 dims: the last 81 -> 71, 4 sequences of 100 rows on 32 61 -> 67).
+    // dims: 12 x 8 rows on 8 key heads over 33000 keys 69 -> 56 us, 100 rows on
+    // 32 over 4000 51 -> 40, but 24 sequences of 16 x 4 rows on 8 over 4000 154
+    // -> 189; 64 dims: the last 81 -> 70, 4 sequences of 100 rows on 32 63 -> 69).
     const int64_t slots = (p.waves == 8 ? 1 : c->dim == 64 ? 3 : 2) * (int64_t)cus;
     // (as if sequences filled their tiles: many short chunks split more, which
     // evens out ragged lengths: 64 sequences of 17 to 8191 keys, 16-bit pages, 2
-    // tokens each, 121 us against 180 counting a tile for each; 128 of 1000 to
-    // 1500: 152 and 127)
+    // tokens each, 124 us against 180 counting a tile for each; 128 of 1000 to
+    // 1500: 159 and 127)
     const int64_t blocks = (q_tokens * group + rows - 1) / rows * kvh;
     const int64_t keys = window > 0 ? std::min(max_kv, std::min(window, kMost) + std::min(sinks, kMost) + rows / group + 64) : max_kv;
     // split the keys of a block's rows where that shortens the longest chain
     // of tiles a slot works off; the joining kernel costs about 8 tiles' time
-    // (16-bit pages, 512 tokens over 33000 keys: 328 us against 626 unsplit and
-    // 353 in 16; 64 over 8000: 31 against 156 and 33)
+    // (16-bit pages, 512 tokens over 33000 keys: 303 us against 661 unsplit and
+    // 314 in 16; 64 over 8000: 32 against 172 and 33)
     const int64_t tiles = (keys + 63) / 64;
     int64_t best = (blocks + slots - 1) / slots * tiles, splits = 1;
     const bool joins = q_tokens * heads * (c->dim / 8) <= kLaunchThreads;  // the joining kernel's threads
@@ -1217,11 +1219,17 @@ struct LpPlan {
 LpPlan lp_plan(int64_t rows, int64_t vocab, int64_t top, int cus) {
   LpPlan p{};
   const int64_t chunks = (vocab + 7 + LP_CHUNK - 1) / LP_CHUNK;
-  // A block for each row saves the second kernel and its launch: where rows are short (one row of 32000, 5 tokens, a
-  // call among others: 12.8 us against 15.5 over several blocks; alone 31.8 and 29.3) and where there are enough of
-  // them (700 rows of 50257: 22.5 and 24.6, 1000 of 131072: 51.2 and 54.5; but 600 of 131072: 41.5 and 37.3, 300:
-  // 33.3 and 25.9).  Otherwise as many blocks as the machine holds, each of 4 chunks a wave or more (64 rows of
-  // 131072: 15.0 with 16 blocks a row, 15.1 with 32).
+  // A block for each row saves the second kernel and its launch, which is 2.5 us of a call.  It is taken where rows are
+  // short (64 chunks), by what calls take one after another from Python.  bf16, 5 tokens, us a call so, one block
+  // against the best of 2 to 16: 1 row of 8192 13.0 and 15.5, of 32000 13.0 and 15.4, of 32768 (65 chunks) 13.0 and
+  // 15.3; 64 rows of 16384 13.1 and 15.4, of 32000 17.3 and 17.4; but 300 of 32000 18.8 and 17.3.  Between captured
+  // calls the second kernel costs next to nothing, and from 16384 logits on several blocks are the faster: 1 row of 8192
+  // 6.9 and 7.5, of 16384 8.4 and 7.5, of 32000 12.8 and 7.9; 64 rows of 32000 17.2 and 10.1, 300 18.7 and 15.2.  fp32
+  // rows are within 1.5 us of these times, but for 300 over several blocks (16384: 13.5 against one block's 11.9; 32000:
+  // 17.5 against 18.2).
+  // It is taken too where there are enough rows (700 rows of 50257: 22.5 and 24.6, 1000 of 131072: 51.2 and 54.5; but
+  // 600 of 131072: 41.5 and 37.3, 300: 33.3 and 25.9).  Otherwise as many blocks as the machine holds, each of 4 chunks
+  // a wave or more (64 rows of 131072: 15.0 with 16 blocks a row, 15.1 with 32).
   p.splits = chunks <= 64 || 2 * rows >= 5 * (int64_t)cus
                  ? 1
                  : (int)std::max<int64_t>(1, std::min(8 * (int64_t)cus / std::max<int64_t>(rows, 1), chunks / 16));

@@ -24,9 +24,16 @@
 // 64 heads on 8 of 128: 549 GFLOP in 600 to 675 us and 10 us for the join.  Six
 // fp16 chunks of 5 to 1500 tokens under a window of 1000, 24 heads on 8 of
 // 64: 35 us, 1.25 us a tile of two waves a SIMD, about 10 us before and after.
-// The prompt under a window of 1500 with 4 sinks: 183 GFLOP in 245 us, 740
-// TFLOP/s; of the work done, with what the masked tiles at the window's two
-// ends cost, 950.  Without the sinks 229.
+// The prompt under a window of 1500: 183 GFLOP in 219 us, with 4 sinks in 231
+// (calls in a row; 245 among other kernels), 835 and 795 TFLOP/s.  A block of 32
+// tokens visits 24 or 25 tiles, 1.04 times what its rows see: 870 and 830 of the
+// work done, where the prompt without a window does 990 in the same loop.  Copies
+// for timing without the scan of masked tiles for values that are not finite and
+// without the masks take 3 to 4 us less, with sinks 6; most of the rest is the
+// beginning and end of a block, about 6 us of 55, four after another in each place
+// (a window of 4000: 970 TFLOP/s).  Sinks cost 10 us in those copies too: what is
+// left are their tests in every tile's copies and ranges (10 scalars are in vector
+// lanes for them), which were not measured apart.
 #pragma once
 
 #include <hip/hip_runtime.h>

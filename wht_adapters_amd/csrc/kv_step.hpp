@@ -31,10 +31,10 @@
 // 16 sequences of 64 heads on 8, INT4, 37 sinks and a window of 16384, 248 MB in
 // 63 us, 4.0 TB/s, the vector pipes half busy with two waves a SIMD.  One token
 // under a window of 1024, wherever it stands in the sequence: 7.7 + 4.3 us.
-// Registers: the INT4 builds keep 100 to 160 scalars in vector lanes, two column
-// blocks (17 to 32 rows) leave one wave a SIMD, and the 16-bit build for several
-// tokens has up to 31 vector registers in scratch (take_out, unrolled over the
-// tile): the 64 sequences with 4 tokens each take 106 us a call.
+// Registers: the INT4 builds keep 50 scalars in vector lanes, with sinks 130 to
+// 160, two column blocks (17 to 32 rows) leave one wave a SIMD, and the 16-bit
+// build for several tokens has up to 30 vector registers in scratch (take_out,
+// unrolled over the tile): the 64 sequences with 4 tokens each take 106 us a call.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -5,10 +5,14 @@
 // With z = scale x, m a logit near the row's largest, S = sum e^(z - scale m)
 // and T = sum e^(z - scale m) (z - scale m):
 //   lse = scale m + log S,  logprob = scale (x_t - m) - log S,
-//   entropy = log S - T / S  (every term of one sign).
+//   entropy = log S - T / S.
 // Each lane keeps (m, S, T) of its own logits over one pass; m may lag behind
 // the largest by LP_LAG, so that S and T are rescaled a few times in a row and
-// not for every vector.  Exponents are differences of logits times a factor
+// not for every vector.  Terms above m are positive then, and what log S and
+// T / S have in common, LP_LAG log 2 = 4.2 at most, cancels: a few 2^-24 times
+// that of lse, logprob and entropy.  m is a logit of the row and keeps 1.5 % of
+// the largest's weight, so that an entropy near 0 is only ever taken from the
+// largest itself.  Exponents are differences of logits times a factor
 // and never products that could overflow: rows masked with the type's lowest
 // value, even all of a row, come out right.  The gradient takes m and S again
 // rather than lse, whose rounding would be an error of every p.

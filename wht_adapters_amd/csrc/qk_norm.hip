@@ -19,7 +19,7 @@
 // Measured (kernel times; 8192 tokens, 32 query and 8 key heads of 128, bf16):
 // into a 16-bit cache 209 MB in 40 us, 5.2 TB/s (a large copy moves 4.9);
 // dense rows 176 MB in 36 us; backward 256 MB in 46 us, 5.5 TB/s, and 4.7 us
-// for the join.  A kind's blocks together, with the rotation's kinds as
+// for the join (a weight vector a head: 63 us, a block walks one head's rows).  A kind's blocks together, with the rotation's kinds as
 // branches, took 50 and 59 us: the branches keep registers of every kind.
 // 2, 3 or 6 rows a group of lanes: 55 to 60 us against 45 at the time, fewer
 // waves to wait side by side.  1 token, 48 heads: 3.3 us; 61 tokens of 80 heads
