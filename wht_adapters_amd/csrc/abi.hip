@@ -66,10 +66,6 @@ hipError_t launch_qi_select(const float* f, int64_t ldf, int64_t rows, int n, co
 hipError_t launch_qi_refine(const float* g, int64_t n, const float* p, int64_t rows, const int32_t* row_ptr,
                             const int32_t* col_idx, float* vals, hipStream_t s);
 
-hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const void* k,
-                            const int64_t* ks, const void* v, const int64_t* vs, const int64_t* slots,
-                            int64_t capacity, const KvTurn& turn, const void* q, const int64_t* qs, int heads,
-                            void* qo, const int64_t* qos, hipStream_t s);
 hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const int64_t* slots,
                             int64_t capacity, void* ko, const int64_t* ks, void* vo, const int64_t* vs,
                             hipStream_t s);
@@ -961,15 +957,11 @@ whtq_status kv_append_norm(const whtq_kv_cache* cache, const void* k, const int6
   if (st != WHTQ_OK) return st;
   const bool int4 = cache->format == WHTQ_KV_INT4;
   const int64_t capacity = cache->num_pages * cache->page_size;
-  if (!norm || (!norm->q && !norm->k))
-    return hip_status(launch_kv_append(c, (int)cache->dim, dtype, int4, tokens, k, k_stride, v, v_stride, slots, capacity,
-                                       kv_turn_of(rope), q, q_stride, q ? (int)heads : 0, q_out, q_out_stride,
-                                       (hipStream_t)stream));
-  const KvNorm n = kv_norm_of(norm);
+  const KvNorm n = norm ? kv_norm_of(norm) : KvNorm{};
   QkForwardArgs a{};
   a.f[0] = {kv_rows_of(k, k_stride), {}, c.k, n.k, rope != nullptr, {}, 0, 0};
   a.f[1] = {kv_rows_of(v, v_stride), {}, c.v, {}, false, {}, 0, 0};
-  if (q) a.f[2] = {kv_rows_of(q, q_stride), kv_rows_of(q_out, q_out_stride), {}, n.q, rope != nullptr, {}, 0, 0, (norm->dtype & WHTQ_CLEAR_Q) != 0};
+  if (q) a.f[2] = {kv_rows_of(q, q_stride), kv_rows_of(q_out, q_out_stride), {}, n.q, rope != nullptr, {}, 0, 0, norm && (norm->dtype & WHTQ_CLEAR_Q)};
   a.c = c;
   a.slots = slots;
   a.capacity = capacity;

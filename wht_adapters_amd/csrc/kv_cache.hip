@@ -1,22 +1,17 @@
-// kv_append and kv_gather: rows between dense tensors and a paged cache.
+// kv_gather: rows of a paged cache as dense tensors (kv_append, the way into
+// it, is in qk_norm.hip).
 //
 // A row (one head vector of D values) belongs to L = D / 16 lanes; lane i
-// holds the 8-value chunks i and i + L, so that a full-width rotation in
-// halves pairs values inside a lane, every access is 16 bytes and L lanes
-// cover contiguous runs.  The transform of an INT4 row is then one butterfly
-// between the two chunks, three inside a chunk and log2 L between lanes.
+// holds the 8-value chunks i and i + L, so that every access is 16 bytes and L
+// lanes cover contiguous runs.  The transform of an INT4 row is then one
+// butterfly between the two chunks, three inside a chunk and log2 L between
+// lanes.
 //
-// Both kernels move bytes: what bounds them is memory (and, for a few
-// tokens, the latency of the chain slot / position -> table row -> store).
-// Rows of one token follow each other in the grid, so that a token's cos, sin
-// and slot come from near caches.
+// The kernel moves bytes: what bounds it is memory (and, for a few tokens, the
+// latency of the chain slot -> entry -> store).
 //
-// Measured (kernel times): a prompt of 8192 tokens, 32 + 2 x 8 heads of 128,
-// bf16 pages: 205 MB in 41 us, 5.0 TB/s (a large copy moves 4.75).  4093
-// tokens, 3 x 24 heads of 64, fp16 into INT4: 57 MB in 21 us, the vector
-// pipes half busy with the transform, the rest latency of the one row a group
-// of lanes has.  30011 entries of 8 INT4 heads of 128 read back: 155 MB in
-// 33 us, 4.7 TB/s.  One token: 2.6 us.
+// Measured (kernel times): 30011 entries of 8 INT4 heads of 128 read back:
+// 155 MB in 33 us, 4.7 TB/s (a large copy moves 4.75).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,49 +21,6 @@
 #include "launch.hpp"
 
 namespace whtq {
-
-struct KvAppendArgs {
-  KvCache c;
-  KvRows k, v, q, qo;
-  const int64_t* slots;
-  KvTurn turn;
-  int64_t capacity;
-  uint32_t rows;  // tokens * (heads + 2 kv_heads)
-  int heads;
-};
-
-template <int D, int T, bool INT4>
-__global__ __launch_bounds__(256) void k_kv_append(const KvAppendArgs a) {
-  constexpr int L = D / 16, RB = 256 / L;
-  const uint32_t r = blockIdx.x * RB + threadIdx.x / L;
-  const int i = threadIdx.x % L;
-  const uint32_t per = a.heads + 2 * a.c.kv_heads;
-  const bool live = r < a.rows;
-  const uint32_t t = live ? r / per : 0, hs = live ? r % per : 0;
-  const int64_t pos = a.turn.pos ? (int64_t)a.turn.pos[t] : 0;
-  // head slots of a token: its keys, its values, its queries
-  const bool is_k = hs < (uint32_t)a.c.kv_heads, is_q = hs >= 2u * a.c.kv_heads;
-  const int h = is_k ? hs : is_q ? hs - 2 * a.c.kv_heads : hs - a.c.kv_heads;
-  const KvRows& in = is_k ? a.k : is_q ? a.q : a.v;
-  const uint8_t* row = in.p + t * in.tok + h * in.head;
-  float x[16];
-  kv_widen8<T>(ldg<u32x4>(row + 16 * i), x);
-  kv_widen8<T>(ldg<u32x4>(row + 16 * (i + L)), x + 8);
-  bool ok = live;
-  if (a.turn.pos) ok = ok && pos >= 0 && pos < a.turn.max_pos;
-  if (a.turn.pos && ok && (is_k || is_q))
-    kv_rotate<D>(x, a.turn, pos, i, [&](int ch, float* o) { kv_widen8<T>(ldg<u32x4>(row + 16 * ch), o); });
-  if (is_q) {
-    if (ok) {
-      uint8_t* o = const_cast<uint8_t*>(a.qo.p) + t * a.qo.tok + h * a.qo.head;
-      stg<u32x4>(o + 16 * i, kv_round8<T>(x));
-      stg<u32x4>(o + 16 * (i + L), kv_round8<T>(x + 8));
-    }
-    return;
-  }
-  const int64_t slot = a.slots[t];
-  kv_keep<D, T, INT4>(x, a.c, is_k ? a.c.k : a.c.v, h, slot, ok && slot >= 0 && slot < a.capacity, i);
-}
 
 // The unscaled transform of a row's codes, as whole numbers: at most 8 D = 1024
 // in size, so fp16 holds every step exactly and two values go in one
@@ -201,38 +153,8 @@ static hipError_t by_tokens(int64_t tokens, int64_t per, int lanes, F launch) {
 }
 
 template <int D, int T, bool INT4>
-static void append_launch(const KvAppendArgs& a, dim3 grid, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv_append<D, T, INT4>), grid, dim3(256), 0, s, a);
-}
-template <int D, int T, bool INT4>
 static void gather_launch(const KvGatherArgs& a, dim3 grid, hipStream_t s) {
   hipLaunchKernelGGL((k_kv_gather<D, T, INT4>), grid, dim3(256), 0, s, a);
-}
-
-hipError_t launch_kv_append(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const void* k,
-                            const int64_t* ks, const void* v, const int64_t* vs, const int64_t* slots,
-                            int64_t capacity, const KvTurn& turn, const void* q, const int64_t* qs, int heads,
-                            void* qo, const int64_t* qos, hipStream_t s) {
-  const int64_t per = (q ? heads : 0) + 2 * (int64_t)c.kv_heads;
-  const int rb = 256 / (dim / 16);
-  return by_tokens(tokens, per, dim / 16, [&](int64_t t0, int64_t n) {
-    KvAppendArgs a{};
-    a.c = c;
-    a.k = {(const uint8_t*)k + t0 * ks[0] * 2, ks[0] * 2, ks[1] * 2};
-    a.v = {(const uint8_t*)v + t0 * vs[0] * 2, vs[0] * 2, vs[1] * 2};
-    if (q) {
-      a.q = {(const uint8_t*)q + t0 * qs[0] * 2, qs[0] * 2, qs[1] * 2};
-      a.qo = {(const uint8_t*)qo + t0 * qos[0] * 2, qos[0] * 2, qos[1] * 2};
-      a.heads = heads;
-    }
-    a.slots = slots + t0;
-    a.capacity = capacity;
-    a.turn = turn;
-    if (turn.pos) a.turn.pos += t0;
-    a.rows = (uint32_t)(n * per);
-    const dim3 grid((unsigned)((n * per + rb - 1) / rb));
-    KV_PICK(append_launch, dim, dt, int4, a, grid, s);
-  });
 }
 
 hipError_t launch_kv_gather(const KvCache& c, int dim, int dt, bool int4, int64_t tokens, const int64_t* slots,

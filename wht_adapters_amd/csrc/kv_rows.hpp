@@ -7,8 +7,6 @@
 // cover contiguous runs.
 #pragma once
 
-#include <type_traits>
-
 #include "kv.hpp"
 
 namespace whtq {
@@ -101,19 +99,6 @@ __device__ __forceinline__ void kv_turn(float (&x)[16], const KvTurn& a, const K
     }
   }
 }
-// The same where the way is known to the call alone.
-template <int D, typename Load>
-__device__ __forceinline__ void kv_rotate(float (&x)[16], const KvTurn& a, int64_t pos, int i, Load load) {
-  auto by = [&](auto way) __attribute__((always_inline)) {
-    KvCs t;
-    kv_load_cs<D, way.value>(t, a, pos, i);
-    kv_turn<D, way.value, false>(x, a, t, pos, i, load);
-  };
-  if (a.interleaved) by(std::integral_constant<int, KV_PAIRS>{});
-  else if (a.rot == D) by(std::integral_constant<int, KV_HALVES>{});
-  else by(std::integral_constant<int, KV_PART>{});
-}
-
 // Butterflies between lanes whose values differ in lane bit M.
 template <int M>
 __device__ __forceinline__ void kv_near_bfly(float (&x)[16], int i) {

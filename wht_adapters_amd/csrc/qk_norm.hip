@@ -1,6 +1,6 @@
-// kv_append with norms, qk_norm_rope and its backward pass: norms of each
-// head's queries and keys and their rotary positions, into a cache's slots
-// and dense rows.
+// kv_append (with norms or without), qk_norm_rope and its backward pass: norms
+// of each head's queries and keys and their rotary positions, into a cache's
+// slots and dense rows.
 //
 //   r = (mean x^2 + eps)^-1/2,  y = R (w o x r)
 // and with g = R^T dy (the opposite rotation), u = w o g:
@@ -9,7 +9,7 @@
 // The backward pass takes x again and computes r itself: two numbers a row
 // less to keep, and x has to be read anyway.
 //
-// Both directions move bytes.  A row belongs to D / 16 lanes as in kv_append.
+// Both directions move bytes.  A row belongs to D / 16 lanes (kv_rows.hpp).
 // Forward, the blocks of keys, values and queries are apart, so that a row's
 // kind, its bases and strides are scalars.  Backward, a block walks rows of
 // one weight vector, so that a lane's part of dw stays in registers; blocks
@@ -17,13 +17,17 @@
 // atomics: the same result every time).
 //
 // Measured (kernel times; 8192 tokens, 32 query and 8 key heads of 128, bf16):
-// into a 16-bit cache 209 MB in 40 us, 5.2 TB/s (a large copy moves 4.9);
-// dense rows 176 MB in 36 us; backward 256 MB in 46 us, 5.5 TB/s, and 4.7 us
-// for the join (a weight vector a head: 63 us, a block walks one head's rows).  A kind's blocks together, with the rotation's kinds as
-// branches, took 50 and 59 us: the branches keep registers of every kind.
-// 2, 3 or 6 rows a group of lanes: 55 to 60 us against 45 at the time, fewer
-// waves to wait side by side.  1 token, 48 heads: 3.3 us; 61 tokens of 80 heads
-// into INT4: 4.9 us; 333 tokens, 48 heads of 64 with a weight vector each:
+// into a 16-bit cache 209 MB in 40 us, 5.2 TB/s (a large copy moves 4.9), without
+// norms, from rows that lie close, 205 MB in 35; dense rows 176 MB in 36; backward
+// 256 MB in 46 us, 5.5 TB/s, and 4.7 us for the join (a weight vector a head: 63
+// us, a block walks one head's rows).  A kind's blocks together, with the
+// rotation's kinds as branches, took 50 and 59 us, without norms 41: the branches
+// keep registers of every kind.  2, 3 or 6 rows a group of lanes: 55 to 60 us
+// against 45 at the time, fewer waves to wait side by side.  4093 tokens, 3 x 24
+// heads of 64, fp16 into INT4 without norms: 57 MB in 17 us (21 with all kinds
+// together), the vector pipes half busy with the transform, the rest latency of
+// the one row a group of lanes has.  1 token, 48 heads: 3.3 us; 61 tokens of 80
+// heads into INT4: 4.9 us; 333 tokens, 48 heads of 64 with a weight vector each:
 // 3.9 us and 9.3 us, the latter the 11 rows in a row that a group of lanes has.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
