@@ -80,6 +80,34 @@ def test_rows_outside_the_positions(W):
         assert (dq[gone] == 0).all() and (dk[gone] == 3).all()
 
 
+@pytest.mark.parametrize("normed", [True, False])
+@pytest.mark.parametrize("clear", [True, False])
+def test_append_clears_queries(W, normed, clear):
+    """The library's append may be asked to clear the queries of tokens outside the positions; the cache has none of them."""
+    rng = np.random.default_rng(34)
+    n, d, hq, hk = 21, 64, 4, 2
+    q, k, v = (torch.from_numpy(rng.standard_normal((n, h, d)).astype(np.float32)).bfloat16().to(DEV) for h in (hq, hk, hk))
+    w, table = torch.ones(d, device=DEV), torch.ones((30, d // 2), device=DEV)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    pos[[2, 20]] = torch.tensor([-1, 30], dtype=torch.int32, device=DEV)
+    slots = torch.arange(n, device=DEV)
+    caches = [W.kv_cache_alloc(2, 16, hk, d, device=DEV) for _ in range(2)]
+    out, want = (torch.full_like(q, 3.0) for _ in range(2))
+    rope = dict(cos=table, sin=table, positions=pos)
+    W.kv_append(caches[0], k, v, slots, q=q, q_out=want, **rope, **(dict(q_norm=w, k_norm=w) if normed else {}))
+    assert (want[[2, 20]] == 3).all()
+    p, st = (lambda t: t.data_ptr()), lambda h: (ctypes.c_int64 * 2)(h * d, d)  # noqa: E731
+    norm = W._Norm(p(w) if normed else 0, p(w) if normed else 0, 0, 0, W.F32 | (W._CLEAR_Q if clear else 0), 1e-6)
+    turn = W._Rope(p(table), p(table), p(pos), d // 2, 30, d, 0)
+    assert W.raw().kv_append_norm(caches[1]._c, p(k), st(hk), p(v), st(hk), W.BF16, n, p(slots), norm, turn, p(q), st(hq), hq,
+                                  p(out), st(hq), torch.cuda.current_stream().cuda_stream) == 0
+    if clear:
+        want[[2, 20]] = 0
+    assert torch.equal(out, want)
+    assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
+    assert (caches[1].k[0, :, 2] == 0).all() and (caches[1].v[1, :, 4] == 0).all()
+
+
 @pytest.mark.parametrize("n", [60, 3000])
 @pytest.mark.parametrize("queries", [True, False])
 def test_one_side_alone(W, n, queries):
